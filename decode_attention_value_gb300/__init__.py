@@ -10,6 +10,7 @@ missing, and every call raises on a non-zero return code.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -29,6 +30,10 @@ STATUS_BAD_TAIL = 32
 STATUS_Q_RANGE = 64
 
 ERR_OUT_OF_SPACE = -7
+
+# kvz_append_tokens
+ROPE_INTERLEAVED = 1
+ROPE_MAX_AXES = 4
 
 # attention launch flags (kvz_decode_attention_ex / kvz_decode_attention_raw_ex)
 ATTN_OVERLAP_PREVIOUS = 1
@@ -52,6 +57,7 @@ EXPORTS = (
     "kvz_selftest_bounded_wait", "kvz_encode_sizes", "kvz_alloc_reserve_granules", "kvz_alloc_room",
     "kvz_f8_calibrate", "kvz_f8_encode_pages", "kvz_f8_decode_blocks", "kvz_f8_decode_attention",
     "kvz_decode_attention_ex", "kvz_decode_attention_raw_ex", "kvz_selftest_late_writer",
+    "kvz_append_tokens",
 )
 
 
@@ -86,6 +92,8 @@ def _load() -> ctypes.CDLL:
                                                    P, ctypes.c_uint32, P]),
         "kvz_decode_attention_raw_ex": (ctypes.c_int, [Dims, i32, i32, P, P, i32, P, P, i64, P, P, sz, P,
                                                        ctypes.c_uint32, P]),
+        "kvz_append_tokens": (ctypes.c_int, [Dims, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P, i32, P, i32,
+                                             ctypes.c_uint32, ctypes.c_float, P, P, i64, P, P]),
         "kvz_selftest_late_writer": (ctypes.c_int, [P, P, u64, u64, P]),
         "kvz_alloc_create": (ctypes.c_int, [u64, ctypes.c_uint32, i32, i32, ctypes.POINTER(P)]),
         "kvz_alloc_destroy": (None, [P]),
@@ -144,6 +152,14 @@ def _ptr(t: torch.Tensor | None, dtype=None, name: str = "") -> int | None:
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _ptr_on(t: torch.Tensor, dtype, name: str, dev: int) -> int:
+    """_ptr for a tensor that has to be on CUDA device dev."""
+    p = _ptr(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on CUDA device {dev}, got {t.device}")
+    return p
 
 
 def _stream(stream) -> int | None:
@@ -279,6 +295,97 @@ def decode_attention_raw(q, page_ids, seq_lens, raw_pool, out, status, workspace
         _check("kvz_decode_attention_raw_ex", _lib.kvz_decode_attention_raw_ex(*args, int(flags), _stream(stream)))
     else:
         _check("kvz_decode_attention_raw", _lib.kvz_decode_attention_raw(*args, _stream(stream)))
+
+
+# ------------------------------------------------------------------------------------
+# new tokens into the raw pages
+# ------------------------------------------------------------------------------------
+def rope_table(inv_freq: torch.Tensor, axis: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotary frequencies laid out for append_tokens, built once per model: int64
+    [pairs][2] on inv_freq's device.  inv_freq: radians per position of each rotary pair
+    (float64 keeps far positions exact); axis: the position axis each pair turns with
+    (all 0 when omitted)."""
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq: expected one frequency per rotary pair, got {tuple(inv_freq.shape)}")
+    if axis is not None and axis.shape != inv_freq.shape:
+        raise ValueError(f"axis: expected {tuple(inv_freq.shape)}, got {tuple(axis.shape)}")
+    turns = inv_freq.to(torch.float64) / (2 * math.pi)
+    turns = ((turns - turns.round()) * 2.0 ** 64).round().clamp(-(2.0 ** 63), 2.0 ** 63 - 1024).to(torch.int64)
+    axis = torch.zeros_like(turns) if axis is None else axis.to(device=turns.device, dtype=torch.int64)
+    return torch.stack([turns, axis], 1)
+
+
+def _heads(t: torch.Tensor, name: str, tokens: int, heads: int | None, dev: int):
+    """Pointer, token stride and head stride of a BF16 [tokens][heads][128] tensor whose
+    heads are contiguous."""
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != HEAD_DIM or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name}: expected [{tokens}][{heads or 'heads'}][{HEAD_DIM}], got {tuple(t.shape)}")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on CUDA device {dev}, got {t.device}")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name}: expected contiguous heads")
+    # a stride nothing steps by may be any number
+    return t.data_ptr(), ts if tokens > 1 else 0, hs if t.shape[1] > 1 else 0
+
+
+def append_tokens(k, v, slots, raw_pool, status, q=None, q_out=None, rope=None, positions=None,
+                  interleaved: bool = False, rope_scale: float = 1.0, stream=None):
+    """Write the keys and values of new tokens, BF16 [T][Hkv][128] (any token and head
+    stride of 8 elements), to rows slots (int32 [T], page * 16 + row, -1 = padding) of the
+    raw pages raw_pool (BF16 [P][Hkv][2][16][128]), rotating the keys by rope (see
+    rope_table) at positions (int32 [T] or [axes][T]).  q [T][Hq][128], when given, is
+    rotated into q_out (allocated when None; may be q).  k, v, slots and raw_pool may all
+    be None to rotate queries alone.  Returns q_out."""
+    dev = status.get_device()
+    first = q if k is None else k
+    if first is None:
+        raise ValueError("append_tokens: no tokens (k and q are both None)")
+    if (k is None) != (v is None) or (k is None) != (slots is None) or (k is None) != (raw_pool is None):
+        raise ValueError("append_tokens: k, v, slots and raw_pool go together")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"status: expected a tensor on the current CUDA device, got {status.device}")
+    T = first.shape[0]
+    hq = hkv = 0
+    qa = ka = va = (None, 0, 0)
+    pool = pages = sl = qo = None
+    if k is not None:
+        hkv = k.shape[1] if k.dim() == 3 else 0
+        ka, va = _heads(k, "k", T, hkv, dev), _heads(v, "v", T, hkv, dev)
+        if raw_pool.dim() != 5 or tuple(raw_pool.shape[1:]) != (hkv, 2, PAGE, HEAD_DIM):
+            raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(raw_pool.shape)}")
+        pool, pages = _ptr_on(raw_pool, torch.bfloat16, "raw_pool", dev), raw_pool.shape[0]
+        if slots.shape != (T,):
+            raise ValueError(f"slots: expected [{T}], got {tuple(slots.shape)}")
+        sl = _ptr_on(slots, torch.int32, "slots", dev)
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qa = _heads(q, "q", T, hq, dev)
+        if q_out is None:
+            q_out = torch.empty((T, hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError(f"q_out: expected {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        qo = _ptr_on(q_out, torch.bfloat16, "q_out", dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = axes = 0
+    rp = pp = None
+    if rope is not None:
+        if rope.dim() != 2 or rope.shape[1] != 2:
+            raise ValueError(f"rope: expected a rope_table, got {tuple(rope.shape)}")
+        if positions is None:
+            raise ValueError("rope without positions")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.shape[-1] != T or positions.dim() not in (1, 2):
+            raise ValueError(f"positions: expected [{T}] or [axes][{T}], got {tuple(positions.shape)}")
+        rot, rp = 2 * rope.shape[0], _ptr_on(rope, torch.int64, "rope", dev)
+        pp = _ptr_on(positions, torch.int32, "positions", dev)
+    _check("kvz_append_tokens", _lib.kvz_append_tokens(
+        _dims(max(hkv, 1)), T, hq, *qa, *ka, *va, sl, pp, axes, rp, rot, ROPE_INTERLEAVED if interleaved else 0,
+        rope_scale, qo, pool, pages or 0, _ptr_on(status, _U32, "status", dev), _stream(stream)))
+    return q_out
 
 
 def apply_cursor_updates(idx, pos, end, cursors, stream=None):

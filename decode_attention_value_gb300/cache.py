@@ -19,12 +19,32 @@ import numpy as np
 import torch
 
 from . import Allocator, ERR_OUT_OF_SPACE, KvzError, PAGE, HEAD_DIM
-from . import apply_cursor_updates, attention_workspace_size, decode_attention, decode_attention_raw
+from . import append_tokens, apply_cursor_updates, attention_workspace_size, decode_attention
+from . import decode_attention_raw
 from . import encode_pages, encode_sizes, encode_workspace_size, new_status
 
 
 class OutOfSpace(RuntimeError):
     """The arena has no free chunk for a reservation (nothing was changed)."""
+
+
+def _append_rows(pools, pages, rows, kv, status, q, rope, positions, interleaved):
+    """One token for each of n sequences in every layer, by one append call over the layers'
+    pages viewed as one pool.  pools: BF16 [layers][per][hkv][2][16][128]; pages, rows: the
+    sequences' raw page within a layer and row (host int64 [n]); kv [layers][n][hkv][2][128];
+    q [layers][n][hq][128], rotated in the result, or None; positions [n] or [axes][n]."""
+    L, per, n = pools.shape[0], pools.shape[1], kv.shape[1]
+    dev = pools.device
+    kv = kv.to(device=dev, dtype=torch.bfloat16).contiguous().view(L * n, *kv.shape[2:])
+    slots = (np.arange(L)[:, None] * per + np.asarray(pages)[None]) * PAGE + np.asarray(rows)[None]
+    slots = torch.from_numpy(slots.reshape(-1).astype(np.int32)).to(dev)
+    if rope is not None:
+        positions = torch.as_tensor(positions, dtype=torch.int32, device=dev).reshape(-1, 1, n)
+        positions = positions.expand(-1, L, n).reshape(-1, L * n)
+    q_out = append_tokens(kv[:, :, 0], kv[:, :, 1], slots, pools.view(L * per, *pools.shape[2:]), status,
+                          q=None if q is None else q.reshape(L * n, *q.shape[2:]), rope=rope,
+                          positions=positions if rope is not None else None, interleaved=interleaved)
+    return None if q is None else q_out.view(q.shape)
 
 
 class CompressedKVCache:
@@ -135,18 +155,24 @@ class CompressedKVCache:
             self.tails[:, slot] = prompt[:, full]
         self.lens[slot] = n_tokens
 
-    def append(self, slots, kv: torch.Tensor):
+    def append(self, slots, kv: torch.Tensor, q=None, rope=None, positions=None, interleaved: bool = False):
         """One new token for each sequence in `slots` (host list, distinct), every layer.
         kv: BF16 [layers][len(slots)][hkv][2][128].  Pages that fill are encoded here.
-        Raises OutOfSpace, with nothing changed, when a filled page has no room."""
+        Raises OutOfSpace, with nothing changed, when a filled page has no room.  With rope
+        (append_tokens' table) the keys are rotated to positions (int [n] or [axes][n];
+        each sequence's length so far when None), and so are the step's queries q
+        [layers][n][hq][128]: the rotated copy is returned."""
         slots = list(slots)
+        if len(set(slots)) != len(slots):
+            raise ValueError("append: a slot is named twice")
+        if not slots:
+            return None if q is None else q.clone()
         done = sorted(s for s in slots if (self.lens[s] + 1) % PAGE == 0)
         pos = self.lens[slots] % PAGE
         idx = torch.as_tensor(slots, dtype=torch.int64, device=self.device)
-        p = torch.as_tensor(pos, dtype=torch.int64, device=self.device)
         saved = self.tails[:, idx].clone() if done else None
-        # separated index tensors put the indexed dimension first: [n][layers][hkv][2][128]
-        self.tails[:, idx, :, :, p, :] = kv.transpose(0, 1)
+        q = _append_rows(self.tails, slots, pos, kv, self.status, q, rope,
+                         self.lens[slots] if positions is None else positions, interleaved)
         if done:
             try:
                 self._finalize(done)
@@ -154,6 +180,7 @@ class CompressedKVCache:
                 self.tails[:, idx] = saved  # nothing changed
                 raise
         self.lens[slots] += 1
+        return q
 
     def _finalize(self, done):
         """Encode the filled tail pages of `done` in every layer, placed by exact
@@ -254,17 +281,23 @@ class RawKVCache:
         if n:
             self.pool[:, torch.as_tensor(ids, device=self.device)] = prompt[:, :n]
 
-    def append(self, slots, kv: torch.Tensor):
+    def append(self, slots, kv: torch.Tensor, q=None, rope=None, positions=None, interleaved: bool = False):
+        """CompressedKVCache.append."""
         slots = list(slots)
+        if len(set(slots)) != len(slots):
+            raise ValueError("append: a slot is named twice")
+        if not slots:
+            return None if q is None else q.clone()
         starting = [s for s in slots if self.lens[s] % PAGE == 0]  # a new page starts
         if len(starting) > len(self.free):
             raise OutOfSpace("no free page slot")
         for s in starting:
             self.pages[s].append(self.free.pop())
-        page = torch.as_tensor([self.pages[s][int(self.lens[s]) // PAGE] for s in slots], device=self.device)
-        pos = torch.as_tensor(self.lens[slots] % PAGE, dtype=torch.int64, device=self.device)
-        self.pool[:, page, :, :, pos, :] = kv.transpose(0, 1)
+        page = [self.pages[s][int(self.lens[s]) // PAGE] for s in slots]
+        q = _append_rows(self.pool, page, self.lens[slots] % PAGE, kv, self.status, q, rope,
+                         self.lens[slots] if positions is None else positions, interleaved)
         self.lens[slots] += 1
+        return q
 
     def release(self, slot: int):
         self.free.extend(reversed(self.pages[slot]))

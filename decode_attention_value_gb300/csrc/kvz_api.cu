@@ -666,6 +666,63 @@ int kvz_f8_decode_attention(kvz_dims dims, int32_t format, int32_t batch, int32_
                          workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                      const void *v, int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots,
+                      const int32_t *positions, int32_t num_axes, const uint64_t *rope, int32_t rot_dim,
+                      uint32_t flags, float rope_scale, void *q_out, void *raw_pool, int64_t num_raw_pages,
+                      uint32_t *status, kvz_stream_t stream)
+{
+    if (!dims_ok(dims)) return dims.num_kv_heads >= 1 ? KVZ_ERR_UNSUPPORTED : KVZ_ERR_INVALID_ARG;
+    if (num_tokens < 0 || num_q_heads < 0 || num_raw_pages < 0 || (flags & ~KVZ_ROPE_FLAGS_ALL))
+        return KVZ_ERR_INVALID_ARG;
+    if (rot_dim < 0 || rot_dim > kDim || num_axes < 0) return KVZ_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0 || num_axes > KVZ_ROPE_MAX_AXES) return KVZ_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return KVZ_OK;
+    const bool kv = k || v || slots || raw_pool;  // all of them, or none (queries alone)
+    if ((!kv && !q) || !status) return KVZ_ERR_INVALID_ARG;
+    if (kv && (!k || !v || !slots || !raw_pool)) return KVZ_ERR_INVALID_ARG;
+    if ((num_q_heads > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return KVZ_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!rope || !positions || num_axes < 1)) return KVZ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(raw_pool, 16) ||
+        !aligned(rope, 16) || !aligned(slots, 4) || !aligned(positions, 4) || !aligned(status, 4))
+        return KVZ_ERR_ALIGNMENT;
+    const int64_t strides[6] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
+                                v_head_stride};
+    for (int i = q ? 0 : 2; i < (kv ? 6 : 2); ++i)
+        if (strides[i] < 0 || strides[i] % 8 != 0) return KVZ_ERR_ALIGNMENT;
+    if ((int64_t)num_tokens * (num_q_heads + 2LL * dims.num_kv_heads) > (int64_t)1 << 36) return KVZ_ERR_UNSUPPORTED;
+    const int sms = sm_count();
+    if (sms < 1) return KVZ_ERR_DEVICE;
+    AppendParams P;
+    memset(&P, 0, sizeof P);
+    P.tokens = num_tokens;
+    P.hq = num_q_heads;
+    P.hkv = kv ? dims.num_kv_heads : 0;
+    P.rot = rot_dim;
+    P.axes = num_axes;
+    P.neighbours = (flags & KVZ_ROPE_INTERLEAVED) != 0;
+    P.scale = rope_scale;
+    P.q = static_cast<const uint16_t *>(q);
+    P.k = static_cast<const uint16_t *>(k);
+    P.v = static_cast<const uint16_t *>(v);
+    P.q_token = q_token_stride;
+    P.q_head = q_head_stride;
+    P.k_token = k_token_stride;
+    P.k_head = k_head_stride;
+    P.v_token = v_token_stride;
+    P.v_head = v_head_stride;
+    P.slots = slots;
+    P.positions = positions;
+    P.rope = rope;
+    P.q_out = static_cast<uint16_t *>(q_out);
+    P.raw_pool = static_cast<uint16_t *>(raw_pool);
+    P.num_raw_pages = num_raw_pages;
+    P.status = status;
+    cudaError_t e = launch_append(P, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
+}
+
 int kvz_apply_cursor_updates(const int32_t *idx, const uint32_t *pos, const uint32_t *end, int32_t n,
                              uint32_t *cursors, int32_t num_cursors, kvz_stream_t stream)
 {

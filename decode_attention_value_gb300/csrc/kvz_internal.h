@@ -108,6 +108,22 @@ inline size_t attn_ws_bytes(int batch, int hkv, int grid, int G = 4)
     return slots * gs * 128 * 4 + slots * gs * 2 * 4;
 }
 
+// New tokens into raw pages (append.cu).  Strides in elements.
+struct AppendParams {
+    int tokens, hq, hkv, rot, axes;
+    bool neighbours;  // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
+    float scale;      // on the sines and cosines
+    const uint16_t *q, *k, *v;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+    const int32_t *slots, *positions;  // [tokens], [axes][tokens]
+    const uint64_t *rope;              // [rot / 2][2]: turns per position (2^-64 units), axis
+    uint16_t *q_out, *raw_pool;
+    int64_t num_raw_pages;
+    uint32_t *status;
+    int rows_per_block;  // set by the launcher
+};
+cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream);
+
 cudaError_t launch_encode(const EncodeParams &P, cudaStream_t stream);
 cudaError_t launch_enc_prepare(const EncodeParams &P, cudaStream_t stream);
 cudaError_t launch_encode_sizes(const EncodeParams &P, cudaStream_t stream);

@@ -253,6 +253,46 @@ int kvz_decode_attention_noalloc(kvz_dims dims, int32_t batch, int32_t num_q_hea
                                  int64_t num_raw_pages, float *out, uint32_t *status, kvz_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * kvz_append_tokens -- write new tokens' keys and values into raw pages (a decode step's
+ * token per sequence, or a batch of prompts), with the rotary position applied to the
+ * keys on the way, and rotate the tokens' queries for the attention call that follows.
+ * The pages name no such call; it fills the raw pool and tail pages that they read.
+ *
+ *  q, k, v      BF16; head h of token t starts at t * token_stride + h * head_stride
+ *               elements (strides multiples of 8, bases 16-byte aligned), its 128 values
+ *               contiguous: slices of one fused projection need no copy.  num_q_heads is
+ *               any number here.  q = NULL with num_q_heads = 0 and q_out = NULL: keys and
+ *               values alone; k, v, slots and raw_pool all NULL: queries alone
+ *  slots[t]     int32, raw page * 16 + token within the page; -1 = padding token, nothing
+ *               of its keys and values is written (its query is).  Other values out of
+ *               range: the same, and KVZ_STATUS_BAD_INDEX.  No two tokens of a call may
+ *               name the same slot: what that slot holds afterwards is then unspecified,
+ *               a mix of the tokens' values; nothing else is touched
+ *  positions    int32 [num_axes][num_tokens], any int32 value (1 <= num_axes <= 4)
+ *  rope         uint64 [rot_dim / 2][2], 16-byte aligned: per rotary pair its frequency as
+ *               a fraction of a turn per position in units of 2^-64 (modulo one turn), and
+ *               the axis whose position it takes.  An axis >= num_axes: the pair is not
+ *               turned, KVZ_STATUS_BAD_INDEX.  Angles wrap exactly at every position
+ *  rot_dim      rotated dimensions, a multiple of 16 up to 128; the dimensions behind them
+ *               are copied.  0: no rotation (rope and positions may be NULL)
+ *  flags        KVZ_ROPE_INTERLEAVED: pair i is dims (2i, 2i+1), else (i, i + rot_dim/2)
+ *  rope_scale   factor on the sines and cosines (1 for plain rotation)
+ *  q_out        BF16 [num_tokens][num_q_heads][128], 16-byte aligned; may be q itself when q
+ *               has that layout, no other overlap of q, k, v with q_out or raw_pool
+ *  raw_pool     raw pool of this layer (see layouts), num_raw_pages pages
+ * Rotation runs in fp32 with one rounding to BF16; values are copied bit for bit.
+ * --------------------------------------------------------------------------------- */
+#define KVZ_ROPE_INTERLEAVED 1u
+#define KVZ_ROPE_FLAGS_ALL 1u
+#define KVZ_ROPE_MAX_AXES 4
+int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                      const void *v, int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots,
+                      const int32_t *positions, int32_t num_axes, const uint64_t *rope, int32_t rot_dim,
+                      uint32_t flags, float rope_scale, void *q_out, void *raw_pool, int64_t num_raw_pages,
+                      uint32_t *status, kvz_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * Group-adaptive additive tiles: a second compressed format, from the page "GAAC:
  * Lossless KV Compression for Bandwidth-Efficient LLM Inference on Personal Devices"
  * (section "Lossless KV Compression": "Contiguous exponent concentration" and

@@ -31,6 +31,10 @@ STATUS_Q_RANGE = 64
 
 ERR_OUT_OF_SPACE = -7
 
+# output types of the prefix attention calls
+OUT_F32 = 0
+OUT_BF16 = 1
+
 # kvz_append_tokens
 ROPE_INTERLEAVED = 1
 ROPE_MAX_AXES = 4
@@ -57,7 +61,7 @@ EXPORTS = (
     "kvz_selftest_bounded_wait", "kvz_encode_sizes", "kvz_alloc_reserve_granules", "kvz_alloc_room",
     "kvz_f8_calibrate", "kvz_f8_encode_pages", "kvz_f8_decode_blocks", "kvz_f8_decode_attention",
     "kvz_decode_attention_ex", "kvz_decode_attention_raw_ex", "kvz_selftest_late_writer",
-    "kvz_append_tokens",
+    "kvz_append_tokens", "kvz_prefix_attention_workspace_size", "kvz_prefix_attention", "kvz_prefix_attention_raw",
 )
 
 
@@ -92,6 +96,11 @@ def _load() -> ctypes.CDLL:
                                                    P, ctypes.c_uint32, P]),
         "kvz_decode_attention_raw_ex": (ctypes.c_int, [Dims, i32, i32, P, P, i32, P, P, i64, P, P, sz, P,
                                                        ctypes.c_uint32, P]),
+        "kvz_prefix_attention_workspace_size": (sz, [Dims, i32, i32, i32, i32, i32]),
+        "kvz_prefix_attention": (ctypes.c_int, [Dims, i32, i32, P, i32, P, P, i32, P, P, P, i32, P, P, P, i64, P, u64, P,
+                                                i64, P, i32, P, sz, P, P]),
+        "kvz_prefix_attention_raw": (ctypes.c_int, [Dims, i32, i32, P, i32, P, P, i32, P, P, i32, P, P, i64, P, i32, P,
+                                                    sz, P, P]),
         "kvz_append_tokens": (ctypes.c_int, [Dims, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P, i32, P, i32,
                                              ctypes.c_uint32, ctypes.c_float, P, P, i64, P, P]),
         "kvz_selftest_late_writer": (ctypes.c_int, [P, P, u64, u64, P]),
@@ -295,6 +304,96 @@ def decode_attention_raw(q, page_ids, seq_lens, raw_pool, out, status, workspace
         _check("kvz_decode_attention_raw_ex", _lib.kvz_decode_attention_raw_ex(*args, int(flags), _stream(stream)))
     else:
         _check("kvz_decode_attention_raw", _lib.kvz_decode_attention_raw(*args, _stream(stream)))
+
+
+# ------------------------------------------------------------------------------------
+# attention of sequences that share prefixes
+# ------------------------------------------------------------------------------------
+def prefix_attention_workspace_size(hkv: int, batch: int, num_q_heads: int, groups: int, prefix_pages: int,
+                                    own_pages: int) -> int:
+    """Workspace bytes of a prefix attention call, compressed or raw, with prefix_ids
+    [groups][prefix_pages] and page_ids [batch][own_pages]."""
+    size = int(_lib.kvz_prefix_attention_workspace_size(_dims(hkv), batch, num_q_heads, groups, prefix_pages + 1,
+                                                        own_pages + 1))
+    if size == 0:
+        raise KvzError("kvz_prefix_attention_workspace_size", -1)
+    return size
+
+
+def _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens, out, status, workspace, stream):
+    """Checks shared by the two prefix attention calls: (device, batch, query heads, groups,
+    prefix columns, own columns, output type, workspace)."""
+    dev = status.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"status: expected a tensor on the current CUDA device, got {status.device}")
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        raise ValueError(f"q: expected [batch][heads][{HEAD_DIM}], got {tuple(q.shape)}")
+    B, hq = q.shape[0], q.shape[1]
+    n = prefix_lens.numel()
+    if prefix_lens.dim() != 1 or group_start.shape != (n + 1,):
+        raise ValueError(f"group_start: expected [{n + 1}] for {n} groups, got {tuple(group_start.shape)}")
+    if prefix_ids.dim() != 2 or prefix_ids.shape[0] != n:
+        raise ValueError(f"prefix_ids: expected [{n}][pages], got {tuple(prefix_ids.shape)}")
+    if page_ids.dim() != 2 or page_ids.shape[0] != B:
+        raise ValueError(f"page_ids: expected [{B}][pages], got {tuple(page_ids.shape)}")
+    if seq_lens.shape != (B,):
+        raise ValueError(f"seq_lens: expected [{B}], got {tuple(seq_lens.shape)}")
+    if out.shape != q.shape:
+        raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
+    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+        raise ValueError(f"out: expected torch.float32 or torch.bfloat16, got {out.dtype}")
+    if workspace is None:
+        workspace = torch.empty(prefix_attention_workspace_size(hkv, B, hq, n, prefix_ids.shape[1], page_ids.shape[1]),
+                                dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    return dev, B, hq, n, prefix_ids.shape[1], page_ids.shape[1], OUT_BF16 if out.dtype is torch.bfloat16 else OUT_F32, \
+        workspace
+
+
+def prefix_attention(q, group_start, prefix_ids, prefix_lens, prefix_tail, page_ids, seq_lens, tail_page, meta, arena,
+                     raw_pool, out, status, workspace=None, stream=None):
+    """decode_attention of sequences that share prefixes: group g is the sequences
+    [group_start[g], group_start[g + 1]) (int32 [groups + 1]), its prefix prefix_lens[g]
+    tokens in the compressed pages prefix_ids[g] plus the raw page prefix_tail[g];
+    page_ids, seq_lens and tail_page are each sequence's own tokens behind it.  The prefix
+    is read once for all sequences of its group.  out: float32 or BF16 [B][Hq][128]."""
+    hkv = meta.shape[1] if meta.dim() >= 2 else raw_pool.shape[1]
+    dev, B, hq, n, pp, op, ot, workspace = _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens,
+                                                        out, status, workspace, stream)
+    if prefix_tail.shape != (n,) or tail_page.shape != (B,):
+        raise ValueError(f"prefix_tail, tail_page: expected [{n}] and [{B}]")
+    if tuple(meta.shape[1:]) != (hkv, 2) or tuple(raw_pool.shape[1:]) != (hkv, 2, PAGE, HEAD_DIM):
+        raise ValueError(f"meta, raw_pool: expected [pages][{hkv}][2] and [pages][{hkv}][2][{PAGE}][{HEAD_DIM}]")
+    i32 = torch.int32
+    _check("kvz_prefix_attention", _lib.kvz_prefix_attention(
+        _dims(hkv), B, hq, _ptr_on(q, torch.bfloat16, "q", dev), n, _ptr_on(group_start, i32, "group_start", dev),
+        _ptr_on(prefix_ids, i32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, i32, "prefix_lens", dev),
+        _ptr_on(prefix_tail, i32, "prefix_tail", dev), _ptr_on(page_ids, i32, "page_ids", dev), op,
+        _ptr_on(seq_lens, i32, "seq_lens", dev), _ptr_on(tail_page, i32, "tail_page", dev),
+        _ptr_on(meta, _U64, "meta", dev), meta.shape[0], _ptr_on(arena, _U8, "arena", dev), arena.numel(),
+        _ptr_on(raw_pool, torch.bfloat16, "raw_pool", dev), raw_pool.shape[0], _ptr_on(out, None, "out", dev), ot,
+        _ptr_on(workspace, _U8, "workspace", dev), workspace.numel(), _ptr_on(status, _U32, "status", dev),
+        _stream(stream)))
+
+
+def prefix_attention_raw(q, group_start, prefix_ids, prefix_lens, page_ids, seq_lens, raw_pool, out, status,
+                         workspace=None, stream=None):
+    """prefix_attention over plain BF16 pages: prefix_ids and page_ids name raw pages and
+    cover the last, partial ones."""
+    hkv = raw_pool.shape[1]
+    dev, B, hq, n, pp, op, ot, workspace = _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens,
+                                                        out, status, workspace, stream)
+    if tuple(raw_pool.shape[1:]) != (hkv, 2, PAGE, HEAD_DIM):
+        raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(raw_pool.shape)}")
+    i32 = torch.int32
+    _check("kvz_prefix_attention_raw", _lib.kvz_prefix_attention_raw(
+        _dims(hkv), B, hq, _ptr_on(q, torch.bfloat16, "q", dev), n, _ptr_on(group_start, i32, "group_start", dev),
+        _ptr_on(prefix_ids, i32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, i32, "prefix_lens", dev),
+        _ptr_on(page_ids, i32, "page_ids", dev), op, _ptr_on(seq_lens, i32, "seq_lens", dev),
+        _ptr_on(raw_pool, torch.bfloat16, "raw_pool", dev), raw_pool.shape[0], _ptr_on(out, None, "out", dev), ot,
+        _ptr_on(workspace, _U8, "workspace", dev), workspace.numel(), _ptr_on(status, _U32, "status", dev),
+        _stream(stream)))
 
 
 # ------------------------------------------------------------------------------------

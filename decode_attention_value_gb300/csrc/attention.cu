@@ -1112,7 +1112,7 @@ cudaError_t attn_ctas_per_sm(int batch, int *out)
 }
 
 template <int kFmt, bool kG8>
-static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream_t stream)
+static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream_t stream, bool merge)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1126,7 +1126,7 @@ static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream
     if (!P.overlap) {
         k_attn<kFmt, kG8><<<P.grid, kThreads, Smem::bytes(P.batch, kFmt >= kFmtGa), stream>>>(P, map);
         e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || !merge) return e;
         if (groups)
             k_attn_merge<kMergeGroups><<<P.batch * P.hkv, 128 * kMergeGroups, 0, stream>>>(P);
         else
@@ -1145,7 +1145,7 @@ static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream
     cfg.attrs = at;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, k_attn<kFmt, kG8>, P, map);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || !merge) return e;
     cfg.gridDim = dim3(P.batch * P.hkv);
     cfg.blockDim = dim3(groups ? 128 * kMergeGroups : 128);
     cfg.dynamicSmemBytes = 0;
@@ -1155,21 +1155,28 @@ static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream
 }
 
 template <bool kG8>
-static cudaError_t launch_format(const AttnParams &P, int format, const void *tmap, cudaStream_t stream)
+static cudaError_t launch_format(const AttnParams &P, int format, const void *tmap, cudaStream_t stream, bool merge)
 {
     switch (format) {
-    case kFmtRaw: return launch_impl<kFmtRaw, kG8>(P, tmap, stream);
-    case kFmtZf: return launch_impl<kFmtZf, kG8>(P, tmap, stream);
-    case kFmtGa: return launch_impl<kFmtGa, kG8>(P, tmap, stream);
-    case kFmtF8E4: return launch_impl<kFmtF8E4, kG8>(P, tmap, stream);
-    case kFmtF8E5: return launch_impl<kFmtF8E5, kG8>(P, tmap, stream);
+    case kFmtRaw: return launch_impl<kFmtRaw, kG8>(P, tmap, stream, merge);
+    case kFmtZf: return launch_impl<kFmtZf, kG8>(P, tmap, stream, merge);
+    case kFmtGa: return launch_impl<kFmtGa, kG8>(P, tmap, stream, merge);
+    case kFmtF8E4: return launch_impl<kFmtF8E4, kG8>(P, tmap, stream, merge);
+    case kFmtF8E5: return launch_impl<kFmtF8E5, kG8>(P, tmap, stream, merge);
     default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_attention(const AttnParams &P, int format, const void *tmap, cudaStream_t stream)
 {
-    return P.G > 4 ? launch_format<true>(P, format, tmap, stream) : launch_format<false>(P, format, tmap, stream);
+    return P.G > 4 ? launch_format<true>(P, format, tmap, stream, true)
+                   : launch_format<false>(P, format, tmap, stream, true);
+}
+
+cudaError_t launch_attention_partials(const AttnParams &P, int format, const void *tmap, cudaStream_t stream)
+{
+    return P.G > 4 ? launch_format<true>(P, format, tmap, stream, false)
+                   : launch_format<false>(P, format, tmap, stream, false);
 }
 
 }  // namespace kvz

@@ -98,6 +98,26 @@ int raw_tensor_map(const void *raw_pool, int64_t num_raw_pages, int hkv, CUtenso
     return KVZ_OK;
 }
 
+// The same rows in boxes of one page's 16 K or V rows x 64 columns (the prefix kernel's
+// operand halves).
+int prefix_tensor_map(const void *raw_pool, int64_t num_raw_pages, int hkv, CUtensorMap *map)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return KVZ_ERR_DEVICE;
+    cuuint64_t dims[2] = {(cuuint64_t)kDim, (cuuint64_t)(num_raw_pages * hkv * 32)};
+    cuuint64_t strides[1] = {(cuuint64_t)kDim * 2};
+    cuuint32_t box[2] = {64, kPage};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(raw_pool), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        g_last_cuda = (int)r;
+        return KVZ_ERR_CUDA;
+    }
+    return KVZ_OK;
+}
+
 int check_attention_common(const kvz_dims &d, int batch, int hq, const void *q, const int32_t *seq_lens,
                            const void *raw_pool, int64_t num_raw_pages, const float *out, const void *ws,
                            const uint32_t *status, int max_pages, const int32_t *page_ids)
@@ -125,22 +145,14 @@ struct FormatArgs {
     const uint8_t *ga_bases;
 };
 
-int run_attention(const FormatArgs &F, const kvz_dims &d, int batch, int hq, const void *q, const int32_t *page_ids,
-                  int max_pages, const int32_t *seq_lens, const int32_t *tail_page, int64_t num_meta_pages,
-                  const uint8_t *arena, uint64_t arena_bytes, const void *raw_pool, int64_t num_raw_pages, float *out,
-                  void *ws, size_t ws_bytes, uint32_t *status, cudaStream_t stream, uint32_t flags = 0)
+// Parameters of the split kernel over a workspace of attn_ws_bytes; launches nothing.
+void attention_params(AttnParams *out_params, const FormatArgs &F, const kvz_dims &d, int batch, int hq, int grid,
+                      const void *q, const int32_t *page_ids, int max_pages, const int32_t *seq_lens,
+                      const int32_t *tail_page, int64_t num_meta_pages, const uint8_t *arena, uint64_t arena_bytes,
+                      int64_t num_raw_pages, float *out, void *ws, uint32_t *status, uint32_t flags)
 {
     const int hkv = d.num_kv_heads;
-    const int table_pages = F.format != kFmtRaw ? max_pages + 1 : max_pages;
-    int grid = 0;
-    int rc = attention_grid(batch, hkv, table_pages, &grid);
-    if (rc) return rc;
-    if (attn_ws_bytes(batch, hkv, grid, hq / hkv) > ws_bytes) return KVZ_ERR_WORKSPACE;
-    CUtensorMap map;
-    // a pool with no pages still needs a valid map object; it is never dereferenced
-    rc = raw_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &map);
-    if (rc) return rc;
-    AttnParams P;
+    AttnParams &P = *out_params;
     memset(&P, 0, sizeof P);
     P.batch = batch;
     P.hkv = hkv;
@@ -167,8 +179,115 @@ int run_attention(const FormatArgs &F, const kvz_dims &d, int batch, int hq, con
     P.status = status;
     P.scale_log2 = (float)(1.4426950408889634 / 11.313708498984761);  // log2(e) / sqrt(128)
     P.overlap = (flags & KVZ_ATTN_OVERLAP_PREVIOUS) ? 1 : 0;
+}
+
+int run_attention(const FormatArgs &F, const kvz_dims &d, int batch, int hq, const void *q, const int32_t *page_ids,
+                  int max_pages, const int32_t *seq_lens, const int32_t *tail_page, int64_t num_meta_pages,
+                  const uint8_t *arena, uint64_t arena_bytes, const void *raw_pool, int64_t num_raw_pages, float *out,
+                  void *ws, size_t ws_bytes, uint32_t *status, cudaStream_t stream, uint32_t flags = 0)
+{
+    const int hkv = d.num_kv_heads;
+    const int table_pages = F.format != kFmtRaw ? max_pages + 1 : max_pages;
+    int grid = 0;
+    int rc = attention_grid(batch, hkv, table_pages, &grid);
+    if (rc) return rc;
+    if (attn_ws_bytes(batch, hkv, grid, hq / hkv) > ws_bytes) return KVZ_ERR_WORKSPACE;
+    CUtensorMap map;
+    // a pool with no pages still needs a valid map object; it is never dereferenced
+    rc = raw_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &map);
+    if (rc) return rc;
+    AttnParams P;
+    attention_params(&P, F, d, batch, hq, grid, q, page_ids, max_pages, seq_lens, tail_page, num_meta_pages, arena,
+                     arena_bytes, num_raw_pages, out, ws, status, flags);
     cudaError_t e = launch_attention(P, F.format, &map, stream);
     return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
+}
+
+// CTAs of the prefix kernel: one per SM, at most one per block of the longest prefixes.
+int prefix_grid(int batch, int hkv, int G, int groups, int prefix_pages, int *grid)
+{
+    const int sms = sm_count();
+    if (sms < 1) return KVZ_ERR_DEVICE;
+    const int64_t blocks = pfx_max_units(batch, hkv, G, groups) * (((int64_t)prefix_pages + 7) / 8);
+    if (blocks > INT32_MAX) return KVZ_ERR_UNSUPPORTED;
+    *grid = groups > 0 ? (int)(blocks < sms ? blocks : sms) : 0;
+    return KVZ_OK;
+}
+
+struct PrefixArgs {
+    int groups;
+    const int32_t *group_start, *ids;
+    int max_pages;
+    const int32_t *lens, *tail;
+};
+
+int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int hq, const void *q, const PrefixArgs &X,
+                         const int32_t *page_ids, int max_pages, const int32_t *seq_lens, const int32_t *tail_page,
+                         int64_t num_meta_pages, const uint8_t *arena, uint64_t arena_bytes, const void *raw_pool,
+                         int64_t num_raw_pages, void *out, int32_t out_type, void *ws, size_t ws_bytes,
+                         uint32_t *status, cudaStream_t stream)
+{
+    const int hkv = d.num_kv_heads, G = hq / hkv;
+    const bool raw = F.format == kFmtRaw;
+    int grid = 0, pgrid = 0;
+    int rc = attention_grid(batch, hkv, raw ? max_pages : max_pages + 1, &grid);
+    if (rc) return rc;
+    rc = prefix_grid(batch, hkv, G, X.groups, raw ? X.max_pages : X.max_pages + 1, &pgrid);
+    if (rc) return rc;
+    const size_t rows = pfx_part_rows(pfx_max_units(batch, hkv, G, X.groups), pgrid);
+    const size_t prefix_bytes = rows * (kDim + 2) * 4;
+    if (prefix_bytes + attn_ws_bytes(batch, hkv, grid, G) > ws_bytes) return KVZ_ERR_WORKSPACE;
+    CUtensorMap map, pmap;
+    rc = raw_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &map);
+    if (!rc) rc = prefix_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &pmap);
+    if (rc) return rc;
+    AttnParams A;
+    // the own pages' kernel follows the prefix kernel as its programmatic dependent
+    attention_params(&A, F, d, batch, hq, grid, q, page_ids, max_pages, seq_lens, tail_page, num_meta_pages, arena,
+                     arena_bytes, num_raw_pages, nullptr, static_cast<uint8_t *>(ws) + prefix_bytes, status,
+                     pgrid > 0 ? KVZ_ATTN_OVERLAP_PREVIOUS : 0u);
+    PrefixParams P;
+    memset(&P, 0, sizeof P);
+    P.batch = batch;
+    P.hkv = hkv;
+    P.G = G;
+    P.num_groups = X.groups;
+    P.max_pages = X.max_pages;
+    P.max_tokens = X.max_pages * kPage + (raw ? 0 : kPage - 1);
+    P.unit_rows = pfx_unit_rows(batch, G, X.groups);
+    P.grid = pgrid;
+    P.q = static_cast<const uint16_t *>(q);
+    P.group_start = X.group_start;
+    P.prefix_ids = X.ids;
+    P.prefix_lens = X.lens;
+    P.prefix_tail = X.tail;
+    P.meta = F.meta;
+    P.num_meta_pages = num_meta_pages;
+    P.arena = arena;
+    P.arena_bytes = arena_bytes;
+    P.raw_pool = static_cast<const uint16_t *>(raw_pool);
+    P.num_raw_pages = num_raw_pages;
+    P.part_o = static_cast<float *>(ws);
+    P.part_ml = P.part_o + rows * kDim;
+    P.out = out;
+    P.out_bf16 = out_type == KVZ_OUT_BF16;
+    P.status = status;
+    P.scale_log2 = A.scale_log2;
+    cudaError_t e = launch_prefix(P, F.format, &pmap, A, &map, stream);
+    return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
+}
+
+int check_prefix(int batch, const PrefixArgs &X, const void *out, int32_t out_type)
+{
+    if (X.groups < 0 || X.max_pages < 0) return KVZ_ERR_INVALID_ARG;
+    if (out_type != KVZ_OUT_F32 && out_type != KVZ_OUT_BF16) return KVZ_ERR_INVALID_ARG;
+    if (X.groups > kPfxMaxGroups || X.max_pages > (INT32_MAX - kPage) / kPage) return KVZ_ERR_UNSUPPORTED;
+    if (batch == 0) return KVZ_OK;
+    if (X.groups > 0 && (!X.group_start || !X.lens || (X.max_pages > 0 && !X.ids))) return KVZ_ERR_INVALID_ARG;
+    if (!aligned(X.group_start, 4) || !aligned(X.lens, 4) || !aligned(X.ids, 4) || !aligned(X.tail, 4) ||
+        !aligned(out, 16))
+        return KVZ_ERR_ALIGNMENT;
+    return KVZ_OK;
 }
 
 // ---------------------------------------------------------------------------------
@@ -664,6 +783,58 @@ int kvz_f8_decode_attention(kvz_dims dims, int32_t format, int32_t batch, int32_
     return run_attention(FormatArgs{fmt, nullptr, meta, bases}, dims, batch, num_q_heads, q, page_ids, max_pages,
                          seq_lens, tail_page, num_meta_pages, arena, arena_bytes, raw_pool, num_raw_pages, out,
                          workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kvz_prefix_attention_workspace_size(kvz_dims dims, int32_t batch, int32_t num_q_heads, int32_t num_groups,
+                                           int32_t prefix_pages, int32_t table_pages)
+{
+    if (num_groups < 0 || num_groups > kPfxMaxGroups || prefix_pages < 0) return 0;
+    if (dims_ok(dims) && num_q_heads >= 1 && num_q_heads % dims.num_kv_heads != 0) return 0;
+    const size_t own = kvz_attention_workspace_size(dims, batch, num_q_heads, table_pages);
+    if (own == 0 || batch == 0) return own;
+    const int G = num_q_heads / dims.num_kv_heads;
+    int grid = 0;
+    if (prefix_grid(batch, dims.num_kv_heads, G, num_groups, prefix_pages, &grid) != KVZ_OK) return 0;
+    return own + pfx_part_rows(pfx_max_units(batch, dims.num_kv_heads, G, num_groups), grid) * (kDim + 2) * 4;
+}
+
+int kvz_prefix_attention(kvz_dims dims, int32_t batch, int32_t num_q_heads, const void *q, int32_t num_groups,
+                         const int32_t *group_start, const int32_t *prefix_ids, int32_t max_prefix_pages,
+                         const int32_t *prefix_lens, const int32_t *prefix_tail, const int32_t *page_ids,
+                         int32_t max_pages, const int32_t *seq_lens, const int32_t *tail_page, const uint64_t *meta,
+                         int64_t num_meta_pages, const uint8_t *arena, uint64_t arena_bytes, const void *raw_pool,
+                         int64_t num_raw_pages, void *out, int32_t out_type, void *workspace, size_t workspace_bytes,
+                         uint32_t *status, kvz_stream_t stream)
+{
+    const PrefixArgs X{num_groups, group_start, prefix_ids, max_prefix_pages, prefix_lens, prefix_tail};
+    int rc = check_attention_common(dims, batch, num_q_heads, q, seq_lens, raw_pool, num_raw_pages,
+                                    static_cast<const float *>(out), workspace, status, max_pages, page_ids);
+    if (!rc) rc = check_prefix(batch, X, out, out_type);
+    if (rc || batch == 0) return rc;
+    if (!tail_page || !meta || !arena || num_meta_pages < 0 || (num_groups > 0 && !prefix_tail))
+        return KVZ_ERR_INVALID_ARG;
+    if (!aligned(meta, 16) || !aligned(arena, 256) || !aligned(tail_page, 4)) return KVZ_ERR_ALIGNMENT;
+    return run_prefix_attention(FormatArgs{kFmtZf, meta, nullptr, nullptr}, dims, batch, num_q_heads, q, X, page_ids,
+                                max_pages, seq_lens, tail_page, num_meta_pages, arena, arena_bytes, raw_pool,
+                                num_raw_pages, out, out_type, workspace, workspace_bytes, status,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kvz_prefix_attention_raw(kvz_dims dims, int32_t batch, int32_t num_q_heads, const void *q, int32_t num_groups,
+                             const int32_t *group_start, const int32_t *prefix_ids, int32_t max_prefix_pages,
+                             const int32_t *prefix_lens, const int32_t *page_ids, int32_t max_pages,
+                             const int32_t *seq_lens, const void *raw_pool, int64_t num_raw_pages, void *out,
+                             int32_t out_type, void *workspace, size_t workspace_bytes, uint32_t *status,
+                             kvz_stream_t stream)
+{
+    const PrefixArgs X{num_groups, group_start, prefix_ids, max_prefix_pages, prefix_lens, nullptr};
+    int rc = check_attention_common(dims, batch, num_q_heads, q, seq_lens, raw_pool, num_raw_pages,
+                                    static_cast<const float *>(out), workspace, status, max_pages, page_ids);
+    if (!rc) rc = check_prefix(batch, X, out, out_type);
+    if (rc || batch == 0) return rc;
+    return run_prefix_attention(FormatArgs{kFmtRaw, nullptr, nullptr, nullptr}, dims, batch, num_q_heads, q, X,
+                                page_ids, max_pages, seq_lens, nullptr, 0, nullptr, 0, raw_pool, num_raw_pages, out,
+                                out_type, workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int64_t q_token_stride,

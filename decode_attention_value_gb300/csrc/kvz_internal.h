@@ -124,6 +124,42 @@ struct AppendParams {
 };
 cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream);
 
+// Shared-prefix attention (prefix.cu): the prefix half; the own pages go through AttnParams.
+constexpr int kPfxMaxGroups = 256;
+struct PrefixParams {
+    int batch, hkv, G, num_groups, max_pages;
+    int max_tokens;  // most prefix tokens the tables can name
+    int unit_rows;   // query rows of a CTA's tile: 128 or 256
+    int grid;        // CTAs
+    const uint16_t *q;
+    const int32_t *group_start, *prefix_ids, *prefix_lens, *prefix_tail;
+    const uint64_t *meta;
+    int64_t num_meta_pages;
+    const uint8_t *arena;
+    uint64_t arena_bytes;
+    const uint16_t *raw_pool;
+    int64_t num_raw_pages;
+    float *part_o;   // [slots][2][128][128]: slot = unit + CTA, then stream, row of the tile
+    float *part_ml;  // [slots][2][128][2]
+    void *out;
+    bool out_bf16;
+    uint32_t *status;
+    float scale_log2;
+};
+
+// Query rows per tile: two tiles of 128 share a CTA when the average group fills more than one.
+inline int pfx_unit_rows(int batch, int G, int groups) { return (int64_t)batch * G > 128LL * groups ? 256 : 128; }
+// Most units (group, KV head, tile) of a call.
+inline int64_t pfx_max_units(int batch, int hkv, int G, int groups)
+{
+    return (int64_t)hkv * (groups + (int64_t)batch * G / pfx_unit_rows(batch, G, groups));
+}
+inline size_t pfx_part_rows(int64_t units, int grid) { return grid > 0 ? (size_t)(units + grid - 1) * 2 * 128 : 0; }
+
+// prefix_map: tensor map of the raw pool with one page's 16 K or V rows x 64 columns a box
+cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_map, const AttnParams &A,
+                          const void *own_map, cudaStream_t stream);
+
 cudaError_t launch_encode(const EncodeParams &P, cudaStream_t stream);
 cudaError_t launch_enc_prepare(const EncodeParams &P, cudaStream_t stream);
 cudaError_t launch_encode_sizes(const EncodeParams &P, cudaStream_t stream);
@@ -147,6 +183,8 @@ cudaError_t launch_apply_cursor_updates(const int32_t *idx, const uint32_t *pos,
 // 3 / 4 FP8 E4M3 / E5M2 tiles (completed pages; the tail stays BF16)
 enum AttnFormat : int { kFmtRaw = 0, kFmtZf = 1, kFmtGa = 2, kFmtF8E4 = 3, kFmtF8E5 = 4 };
 cudaError_t launch_attention(const AttnParams &P, int format, const void *tmap, cudaStream_t stream);
+// the split kernel alone: partials in the workspace, no merge and no output
+cudaError_t launch_attention_partials(const AttnParams &P, int format, const void *tmap, cudaStream_t stream);
 // CTAs per SM both attention kernels can hold at this batch size (the smaller of the two)
 cudaError_t attn_ctas_per_sm(int batch, int *out);
 

@@ -1,0 +1,673 @@
+// prefix.cu -- decode attention of sequences that share a prefix: the prefix's pages are
+// read once for all sequences of a group.
+//
+// Mathematics.  For one KV head the queries of a group, n sequences x G heads, are the rows
+// of one matrix Q.  Over the group's prefix, S = Q K^T and O = exp2(S c - m) V are matrix
+// products with many rows, so they run on the tcgen05 tensor cores instead of once per
+// sequence: the bytes of the prefix are read n times less often, and the arithmetic per byte
+// grows with n G.  Each sequence's own pages go through the split kernel of attention.cu.
+// Both leave partial results (running maximum m, sum l, unnormalised O) and one merge adds
+// them: sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, in a fixed order.
+#include <cuda.h>
+
+#include <cstring>
+
+#include "kvz_internal.h"
+#include "tc.cuh"
+
+namespace kvz {
+
+constexpr int kPfxBlock = 128;                   // tokens of a block: 8 pages
+constexpr int kPfxPages = kPfxBlock / kPage;
+constexpr uint32_t kUnitBytes = kPfxBlock * kDim * 2;  // K or V of a block, BF16
+constexpr uint32_t kHalfBytes = kUnitBytes / 2;        // its 64-column halves
+constexpr int kPfxThreads = 320;  // two softmax warpgroups, the producer warp, the issuing warp
+constexpr int kInfoRing = 8;
+
+// Two streams of softmax threads share a CTA.  kTiles = 2: 256 query rows, stream s holds rows
+// [128 s, 128 s + 128) and both see every block.  kTiles = 1: 128 rows, the streams take
+// alternate blocks and leave separate partials.
+template <int kTiles>
+struct PfxSmem {
+    static constexpr int units = kTiles == 2 ? 5 : 6;  // ring of K and V blocks
+    static constexpr int q = 0;
+    static constexpr int ring = q + kTiles * (int)kUnitBytes;
+    static constexpr int full = ring + units * (int)kUnitBytes;
+    static constexpr int empty = full + units * 8;
+    static constexpr int qfull = empty + units * 8;
+    static constexpr int sfull = qfull + 8;   // [2] scores of a stream are in tensor memory
+    static constexpr int pready = sfull + 16;  // [2] its weights are
+    static constexpr int ofull = pready + 16;  // [2] its output of the segment is complete
+    static constexpr int drain = ofull + 16;
+    static constexpr int info = drain + 8;  // [kInfoRing] bad pages of a block
+    static constexpr int misc = info + kInfoRing * 4;  // tensor memory address, abort flag
+    static constexpr int plan = misc + 16;  // [groups + 1] {first unit, first block}
+    static int bytes(int groups) { return plan + (groups + 1) * 8; }
+};
+
+// Units and blocks of group g (0, 0 when it has no sequence or no prefix).
+struct PfxGroup {
+    int seq0, seqs, len, blocks, tiles;
+};
+
+__device__ __forceinline__ PfxGroup pfx_group(const PrefixParams &P, int g)
+{
+    PfxGroup r;
+    r.seq0 = P.group_start[g];
+    r.seqs = P.group_start[g + 1] - r.seq0;
+    r.len = min(max(P.prefix_lens[g], 0), P.max_tokens);
+    r.blocks = (r.len + kPfxBlock - 1) / kPfxBlock;
+    r.tiles = r.blocks > 0 ? (r.seqs * P.G + P.unit_rows - 1) / P.unit_rows : 0;
+    return r;
+}
+
+// One warp: group starts ordered and in range?
+__device__ __forceinline__ bool pfx_groups_ok(const PrefixParams &P, int lane)
+{
+    bool ok = true;
+    for (int g = lane; g < P.num_groups; g += 32) ok &= P.group_start[g] <= P.group_start[g + 1];
+    ok &= P.group_start[0] >= 0 && P.group_start[P.num_groups] <= P.batch;
+    return __all_sync(0xffffffffu, ok);
+}
+
+// First block of CTA c's range of W blocks over C CTAs.
+__device__ __forceinline__ int pfx_first(int c, int W, int C) { return (int)(((int64_t)c * W + C - 1) / C); }
+
+struct PfxSeg {
+    int g, kvh, tile, unit, block0, blocks, len, seq0, rows;  // rows of this unit's tile
+};
+
+__device__ __forceinline__ PfxSeg pfx_locate(const PrefixParams &P, const int2 *plan, int x, int hi)
+{
+    int lo = 0, top = P.num_groups - 1;
+    while (lo < top) {  // the last group that begins at or before x
+        const int mid = (lo + top + 1) >> 1;
+        if (plan[mid].y <= x) lo = mid;
+        else top = mid - 1;
+    }
+    const PfxGroup r = pfx_group(P, lo);
+    const int rem = x - plan[lo].y, ui = rem / r.blocks;
+    PfxSeg s;
+    s.g = lo;
+    s.block0 = rem - ui * r.blocks;
+    s.kvh = ui / r.tiles;
+    s.tile = ui - s.kvh * r.tiles;
+    s.unit = plan[lo].x + ui;
+    s.blocks = min(hi - x, r.blocks - s.block0);
+    s.len = r.len;
+    s.seq0 = r.seq0;
+    s.rows = min(r.seqs * P.G - s.tile * P.unit_rows, P.unit_rows);
+    return s;
+}
+
+// A bounded wait that gives up for the whole CTA.
+struct PfxWait {
+    uint32_t *status;
+    volatile uint32_t *abort;
+    bool ok;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity)
+    {
+        if (!ok) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((it & 255u) == 0 && (*abort || globaltimer_ns() - t0 > kWaitLimitNs)) {
+                atomicOr(status, KVZ_STATUS_TIMEOUT);
+                *abort = 1;
+                return ok = false;
+            }
+        }
+    }
+};
+
+template <int kTiles>
+__global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P, const __grid_constant__ CUtensorMap tmap)
+{
+    using S = PfxSmem<kTiles>;
+    constexpr int kUnits = S::units;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_addr(smem);
+    if (sbase & 1023u) {  // swizzled operands need 1024-byte alignment
+        if (threadIdx.x == 0) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
+        return;
+    }
+    pdl_launch_dependents();  // the own-pages kernel may be placed as CTAs here finish
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int2 *plan = reinterpret_cast<int2 *>(smem + S::plan);
+    uint32_t *info = reinterpret_cast<uint32_t *>(smem + S::info);
+    volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + S::misc);
+
+    if (tid == 0) {
+        for (int s = 0; s < kUnits; ++s) {
+            mbar_init(sbase + S::full + 8 * s, 1);
+            mbar_init(sbase + S::empty + 8 * s, 1);
+        }
+        mbar_init(sbase + S::qfull, 256);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(sbase + S::sfull + 8 * s, 1);
+            mbar_init(sbase + S::pready + 8 * s, 128);
+            mbar_init(sbase + S::ofull + 8 * s, 1);
+        }
+        mbar_init(sbase + S::drain, 1);
+        misc[1] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) tmem_alloc(sbase + S::misc, 512);
+    if (warp == 0) {  // units and blocks before each group
+        const bool ok = pfx_groups_ok(P, lane);
+        if (!ok && lane == 0) atomicOr(P.status, KVZ_STATUS_BAD_ORDER);
+        const int per = (P.num_groups + 31) / 32;
+        const int g0 = min(P.num_groups, lane * per), g1 = min(P.num_groups, g0 + per);
+        int u = 0, w = 0;
+        uint32_t bad = 0;
+        for (int g = g0; g < g1 && ok; ++g) {
+            const PfxGroup r = pfx_group(P, g);
+            bad |= P.prefix_lens[g] != r.len;
+            u += P.hkv * r.tiles;
+            w += P.hkv * r.tiles * r.blocks;
+        }
+        if (bad) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
+        int su = u, sw = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, su, off), b = __shfl_up_sync(0xffffffffu, sw, off);
+            if (lane >= off) {
+                su += a;
+                sw += b;
+            }
+        }
+        int ru = su - u, rw = sw - w;
+        for (int g = g0; g < g1; ++g) {
+            plan[g] = make_int2(ru, rw);
+            if (!ok) continue;
+            const PfxGroup r = pfx_group(P, g);
+            ru += P.hkv * r.tiles;
+            rw += P.hkv * r.tiles * r.blocks;
+        }
+        if (lane == 31) plan[P.num_groups] = make_int2(su, sw);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    const int W = plan[P.num_groups].y, C = min((int)gridDim.x, W), c = blockIdx.x;
+    const int lo = c < C ? pfx_first(c, W, C) : 0, hi = c < C ? pfx_first(c + 1, W, C) : 0;
+    PfxWait wait{P.status, misc + 1, true};
+
+    if (warp == 8) {
+        // =============================== producer ===============================
+        // One lane per page, 32 pages (four blocks) at a time; the ids of the next four
+        // blocks are fetched while these are copied.  Eight pages of 16 rows make a block's
+        // K (or V) operand: two boxes a page, one per 64-column half.
+        prefetch_tensormap(&tmap);
+        const uint64_t keep = l2_evict_last();
+        const int pages = (hi - lo) * kPfxPages;
+        auto prep = [&](int y) -> int {  // the page's first row in the raw pool, -1: none, -2: bad
+            if (y >= pages) return -1;
+            const PfxSeg s = pfx_locate(P, plan, lo + y / kPfxPages, hi);
+            const int p = s.block0 * kPfxPages + y % kPfxPages;
+            if (p * kPage >= s.len) return -1;
+            const int32_t id = ld_keep_s32(P.prefix_ids + (int64_t)s.g * P.max_pages + p, keep);
+            if (id < 0 || id >= P.num_raw_pages) return -2;
+            return (id * P.hkv + s.kvh) * 32;
+        };
+        int cur = prep(lane), nxt = prep(32 + lane);
+        bool ok = true;
+        for (int base = 0; base < pages && ok; base += 32) {
+            if (cur == -2) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
+            const uint32_t good = __ballot_sync(0xffffffffu, cur >= 0), bad = __ballot_sync(0xffffffffu, cur == -2);
+            const int nn = prep(base + 64 + lane);
+            for (int i = 0; i < 32 / kPfxPages; ++i) {
+                const int n = base / kPfxPages + i;  // block within the range
+                if (n >= hi - lo) break;
+                const uint32_t live = (good >> (kPfxPages * i)) & 0xFFu;
+                const int row = __shfl_sync(0xffffffffu, cur, kPfxPages * i + ((lane >> 1) & 7));
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int it = 2 * n + kv, slot = it % kUnits;
+                    const uint32_t fullbar = sbase + S::full + 8 * slot;
+                    ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, ((it / kUnits) & 1) ^ 1));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (kv == 0) info[n % kInfoRing] = (bad >> (kPfxPages * i)) & 0xFFu;
+                        if (live) mbar_arrive_expect_tx(fullbar, __popc(live) * (kPage * kDim * 2));
+                        else mbar_arrive(fullbar);
+                    }
+                    __syncwarp();
+                    if (lane < 16 && row >= 0) {
+                        const uint32_t dst =
+                            sbase + S::ring + slot * kUnitBytes + (lane & 1) * kHalfBytes + (lane >> 1) * (kPage * 128);
+                        tensor_copy_2d_g2s(dst, &tmap, (lane & 1) * 64, row + kv * kPage, fullbar);
+                    }
+                }
+                if (!ok) break;
+            }
+            cur = nxt;
+            nxt = nn;
+        }
+        // never leave with copies in flight: every fill is waited for by the products; after a
+        // wait that gave up, 1 ms (copies take microseconds)
+        if (!ok) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000) {}
+        }
+    } else if (warp == 9) {
+        // ============================ matrix products ============================
+        if (lane == 0) {
+            constexpr uint32_t kQk = mma_desc(128, kPfxBlock, false), kPv = mma_desc(128, kDim, true);
+            auto unit_addr = [&](int it) { return sbase + S::ring + (it % kUnits) * kUnitBytes; };
+            auto wait_unit = [&](int it) {
+                wait(sbase + S::full + 8 * (it % kUnits), (it / kUnits) & 1);
+                tc_fence_after();
+            };
+            auto free_unit = [&](int it) { mma_commit(sbase + S::empty + 8 * (it % kUnits)); };
+            // scores of stream s over K block n
+            auto qk = [&](int s, int n) {
+                const uint64_t a = smem_desc(sbase + S::q + (kTiles == 2 ? s * kUnitBytes : 0), 16, 1024);
+                const uint64_t b = smem_desc(unit_addr(2 * n), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {  // 16 of the 128 dims: 32 bytes within a half's rows
+                    const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                    mma_ss(tmem + s * 128, a + off, b + off, kQk, k > 0);
+                }
+                mma_commit(sbase + S::sfull + 8 * s);
+            };
+            // output of stream s: its weights (high and low parts) times V block n
+            auto pv = [&](int s, int n, bool add) {
+                const uint64_t b = smem_desc(unit_addr(2 * n + 1), kHalfBytes, 1024);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // 16 tokens: two atoms of V rows, eight columns of weights
+                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * 64 + k * 8, b + ((k * 2048) >> 4), kPv,
+                               add || part || k);
+            };
+            uint32_t pphase[2] = {0, 0};
+            int seg = 0;
+            for (int x = lo; x < hi && wait.ok; ++seg) {
+                const PfxSeg sg = pfx_locate(P, plan, x, hi);
+                const int n0 = x - lo, nb = sg.blocks;
+                wait(sbase + S::qfull, seg & 1);
+                constexpr int step = kTiles == 2 ? 1 : 2;  // blocks between a stream's blocks
+                for (int s = 0; s < 2; ++s) {
+                    const int j = kTiles == 2 ? 0 : s;
+                    if (j >= nb) break;
+                    if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j));
+                    if (!wait.ok) break;
+                    qk(s, n0 + j);
+                    if (kTiles == 1 || s == 1) free_unit(2 * (n0 + j));
+                }
+                for (int i = 0; i < (kTiles == 2 ? 2 * nb : nb) && wait.ok; ++i) {
+                    const int s = i & 1, j = kTiles == 2 ? i >> 1 : i;
+                    wait(sbase + S::pready + 8 * s, pphase[s]);
+                    pphase[s] ^= 1;
+                    if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j) + 1);
+                    else tc_fence_after();
+                    if (!wait.ok) break;
+                    pv(s, n0 + j, j >= step);
+                    if (j + step >= nb) mma_commit(sbase + S::ofull + 8 * s);
+                    if (kTiles == 1 || s == 1) free_unit(2 * (n0 + j) + 1);
+                    if (j + step < nb) {
+                        if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j + step));
+                        if (!wait.ok) break;
+                        qk(s, n0 + j + step);
+                        if (kTiles == 1 || s == 1) free_unit(2 * (n0 + j + step));
+                    }
+                }
+                x += nb;
+            }
+            if (!wait.ok) {  // no product in flight when tensor memory is given back
+                mma_commit(sbase + S::drain);
+                mbar_wait(sbase + S::drain, 0, P.status);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================================ softmax ================================
+        // Thread = query row.  Its 128 scores of a block come from tensor memory at once; the
+        // weights go back over them as two BF16 parts, p = high + low (16 bits of p).  The
+        // running maximum moves, and the output is rescaled, only when it grows by more than
+        // 2^8: weights up to 2^8 lose nothing in floating point.
+        const int s = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + 256 + s * 128 + lanes;
+        uint32_t sphase = 0, ophase = 0;
+        for (int x = lo; x < hi;) {  // (after a wait that gave up, every segment's barrier still)
+            const PfxSeg sg = pfx_locate(P, plan, x, hi);
+            const int n0 = x - lo, nb = sg.blocks;
+            // ---- queries to shared memory (every product of the last segment is complete) ----
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            for (int i = tid; i < kTiles * 128 * 16; i += 256) {
+                const int row = i >> 4, ch = i & 15, grow = sg.tile * P.unit_rows + row;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row < sg.rows)
+                    v = *reinterpret_cast<const uint4 *>(
+                        P.q + ((int64_t)(sg.seq0 + grow / P.G) * P.hkv * P.G + sg.kvh * P.G + grow % P.G) * kDim + ch * 8);
+                *reinterpret_cast<uint4 *>(smem + S::q + (row >> 7) * kUnitBytes + (ch >> 3) * kHalfBytes +
+                                           (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+            }
+            fence_async_shared();
+            mbar_arrive(sbase + S::qfull);
+            const int row0 = kTiles == 2 ? s * 128 : 0;
+            const bool active = row0 + quad * 32 < sg.rows;  // a warp without rows only keeps step
+            float m = -INFINITY, l = 0.f;
+            int mine = 0;
+            for (int j = kTiles == 2 ? 0 : s; j < nb; j += kTiles == 2 ? 1 : 2, ++mine) {
+                const int n = n0 + j;
+                wait(sbase + S::sfull + 8 * s, sphase);
+                sphase ^= 1;
+                if (!__all_sync(0xffffffffu, wait.ok)) break;
+                tc_fence_after();
+                const int left = sg.len - (sg.block0 + j) * kPfxBlock;
+                const uint32_t bad = info[n % kInfoRing];
+                const bool whole = left >= kPfxBlock && bad == 0;
+                uint32_t v[4][32];
+                if (active) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) tmem_ld32(tS + 32 * w, v[w]);
+                }
+                if (!whole) {
+                    // rows of V that hold no token: zero, so that weight 0 times them is 0
+                    const int it = 2 * n + 1;
+                    wait(sbase + S::full + 8 * (it % kUnits), (it / kUnits) & 1);
+                    if (r >= left || (bad >> (r >> 4) & 1)) {
+                        uint8_t *at = smem + S::ring + (it % kUnits) * kUnitBytes + r * 128;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            *reinterpret_cast<uint4 *>(at + 16 * i) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(at + kHalfBytes + 16 * i) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_async_shared();
+                    if (!__all_sync(0xffffffffu, wait.ok)) break;
+                }
+                if (active) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) tmem_wait_ld(v[w]);
+                    if (!whole) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int t = 32 * w + i;
+                                if (t >= left || (bad >> (t >> 4) & 1)) v[w][i] = 0xFF800000u;  // -inf
+                            }
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        top[w] = __uint_as_float(v[w][0]);
+#pragma unroll
+                        for (int i = 1; i < 32; ++i) top[w] = fmaxf(top[w], __uint_as_float(v[w][i]));
+                    }
+                    const float bm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale_log2;
+                    const bool grow = mine == 0 ? true : bm > m + 8.f;
+                    if (mine > 0 && __any_sync(0xffffffffu, grow)) {
+                        // (the products behind these scores were issued after every earlier
+                        // product of the stream, so the output is complete)
+                        const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - bm)) : 1.f;
+                        l *= f;
+#pragma unroll 1
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + 32 * w, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(tO + 32 * w, o);
+                        }
+                    }
+                    if (grow) m = bm;
+                    const float u = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t hi2[16], lo2[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float p0 = ex2(fmaf(__uint_as_float(v[w][2 * i]), P.scale_log2, -u));
+                            const float p1 = ex2(fmaf(__uint_as_float(v[w][2 * i + 1]), P.scale_log2, -u));
+                            sum[i & 3] += p0 + p1;
+                            hi2[i] = pack_bf16x2(p0, p1);
+                            lo2[i] = pack_bf16x2(p0 - __uint_as_float(hi2[i] << 16),
+                                                 p1 - __uint_as_float(hi2[i] & 0xFFFF0000u));
+                        }
+                        tmem_st16(tS + 16 * w, hi2);
+                        tmem_st16(tS + 64 + 16 * w, lo2);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(sbase + S::pready + 8 * s);
+            }
+            // ---- the segment's partial ----
+            const int64_t slot = ((int64_t)(sg.unit + c) * 2 + s) * 128 + r;
+            const bool live = row0 + r < sg.rows;
+            if (mine > 0) {
+                wait(sbase + S::ofull + 8 * s, ophase);
+                ophase ^= 1;
+                tc_fence_after();
+                if (__all_sync(0xffffffffu, wait.ok) && active) {
+#pragma unroll 1
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * w, o);
+                        tmem_wait_ld(o);
+                        if (live) {
+                            uint4 *at = reinterpret_cast<uint4 *>(P.part_o + slot * kDim + 32 * w);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) at[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            if (live) *reinterpret_cast<float2 *>(P.part_ml + slot * 2) = make_float2(m, l);
+            x += nb;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// merge: one block per (sequence, query head).  The partials of its row, prefix CTAs in order
+// and then own-page CTAs in order, are weighted by 2^(m - max) and added: each warp every
+// fourth one, then the four warps in order.
+// ---------------------------------------------------------------------------------
+constexpr int kMergeThreads = 128;
+
+__global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixParams P, const AttnParams A)
+{
+    extern __shared__ float2 ml[];  // [items]: (m, l), then weight in .x
+    __shared__ int red[4][6];
+    __shared__ float fred[4][2];
+    __shared__ float4 acc[4][32];
+    const int b = blockIdx.x / (P.hkv * P.G), h = blockIdx.x % (P.hkv * P.G), kvh = h / P.G, tid = threadIdx.x;
+    const int warp = tid >> 5, lane = tid & 31;
+    // ---- before the wait: what the lengths say (they were complete before the call) ----
+    // own pages of the sequences before b, of b, of all; prefix units and blocks before b's
+    // group and in all; b's group
+    int v[6] = {0, 0, 0, 0, 0, 0}, mine = -1;
+    for (int i = tid; i < P.batch; i += kMergeThreads) {
+        const int L = A.seq_lens[i], pages = L > 0 ? (L + kPage - 1) / kPage : 0;
+        v[0] += i < b ? pages : 0;
+        v[1] += i == b ? pages : 0;
+        v[2] += pages;
+    }
+    const bool ok = P.num_groups > 0 && pfx_groups_ok(P, lane);
+    if (ok)
+        for (int g = tid; g < P.num_groups; g += kMergeThreads) {
+            const PfxGroup r = pfx_group(P, g);
+            const int n = P.hkv * r.tiles;
+            if (r.seq0 + r.seqs <= b) {  // groups before b's
+                v[3] += n;
+                v[4] += n * r.blocks;
+            } else if (r.seq0 <= b) {
+                mine = g;
+            }
+            v[5] += n * r.blocks;
+        }
+    mine = __reduce_max_sync(0xffffffffu, mine);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = __reduce_add_sync(0xffffffffu, v[i]);
+    __shared__ int gred[4];
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) red[warp][i] = v[i];
+        gred[warp] = mine;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = red[0][i] + red[1][i] + red[2][i] + red[3][i];
+    mine = max(max(gred[0], gred[1]), max(gred[2], gred[3]));
+    // prefix items: CTAs c0 .. c1 of the row's unit, one or two streams each
+    int np = 0, c0 = 0, streams = 1, prow = 0, unit = 0;
+    if (mine >= 0) {
+        const PfxGroup r = pfx_group(P, mine);
+        if (r.blocks > 0) {
+            const int row = (b - r.seq0) * P.G + h % P.G, tile = row / P.unit_rows;
+            prow = row - tile * P.unit_rows;
+            const int ui = kvh * r.tiles + tile, W = v[5], C = min(P.grid, W);
+            const int first = v[4] + ui * r.blocks, last = first + r.blocks - 1;
+            unit = v[3] + ui;
+            c0 = (int)((int64_t)first * C / W);
+            streams = P.unit_rows == 128 ? 2 : 1;
+            np = ((int)((int64_t)last * C / W) - c0 + 1) * streams;
+        }
+    }
+    // own items: CTAs of the split kernel that hold pages of (b, kvh)
+    const int64_t T = (int64_t)P.hkv * v[2], AC = A.grid;
+    int ns = 0, a0 = 0;
+    if (v[1] > 0) {
+        const int64_t first = (int64_t)P.hkv * v[0] + (int64_t)kvh * v[1];
+        a0 = (int)(first * AC / T);
+        ns = (int)((first + v[1] - 1) * AC / T) - a0 + 1;
+    }
+    const int heads = P.G > 4 ? 8 : 4;  // heads of a slot of the split kernel
+    auto row_of = [&](int i, const float *&o, const float *&m) {  // partial i of the row
+        if (i < np) {
+            const int s = P.unit_rows == 128 ? i & 1 : prow >> 7, cc = c0 + i / streams;
+            const int64_t row = ((int64_t)(unit + cc) * 2 + s) * 128 + (prow & 127);
+            o = P.part_o + row * kDim;
+            m = P.part_ml + row * 2;
+        } else {
+            const int64_t row = ((int64_t)(b * P.hkv + kvh) + a0 + (i - np)) * heads + h % P.G;
+            o = A.part_o + row * kDim;
+            m = A.part_ml + row * 2;
+        }
+    };
+    pdl_wait_primary();  // both kernels' partials are complete
+    const int items = np + ns;
+    float M = -INFINITY;
+    for (int i = tid; i < items; i += kMergeThreads) {
+        float2 e = make_float2(-INFINITY, 0.f);
+        const int64_t cc = a0 + (i - np);
+        // (a CTA of the split kernel without pages wrote nothing)
+        if (i < np || T >= AC || (cc * T + AC - 1) / AC < ((cc + 1) * T + AC - 1) / AC) {
+            const float *o, *m;
+            row_of(i, o, m);
+            e = *reinterpret_cast<const float2 *>(m);
+        }
+        ml[i] = e;
+        M = fmaxf(M, e.x);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (lane == 0) fred[warp][0] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(fred[0][0], fred[1][0]), fmaxf(fred[2][0], fred[3][0]));
+    float L = 0.f;
+    for (int i = tid; i < items; i += kMergeThreads) {
+        const float2 e = ml[i];
+        const float w = e.x == -INFINITY ? 0.f : exp2f(e.x - M);
+        L += e.x == -INFINITY ? 0.f : w * e.y;
+        ml[i].x = e.x == -INFINITY ? -1.f : w;  // -1: a partial without tokens has no output
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if (lane == 0) fred[warp][1] = L;
+    __syncthreads();
+    L = (fred[0][1] + fred[1][1]) + (fred[2][1] + fred[3][1]);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = warp; i < items; i += 4) {
+        const float w = ml[i].x;
+        if (!(w < 0.f)) {
+            const float *o, *m;
+            row_of(i, o, m);
+            const float4 x = *reinterpret_cast<const float4 *>(o + 4 * lane);
+            sum.x += w * x.x;
+            sum.y += w * x.y;
+            sum.z += w * x.z;
+            sum.w += w * x.w;
+        }
+    }
+    acc[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        const float4 x0 = acc[0][lane], x1 = acc[1][lane], x2 = acc[2][lane], x3 = acc[3][lane];
+        const float k = L == 0.f ? 0.f : 1.f / L;  // no token: zero
+        float4 y = make_float4(((x0.x + x1.x) + (x2.x + x3.x)) * k, ((x0.y + x1.y) + (x2.y + x3.y)) * k,
+                               ((x0.z + x1.z) + (x2.z + x3.z)) * k, ((x0.w + x1.w) + (x2.w + x3.w)) * k);
+        const int64_t at = (int64_t)blockIdx.x * kDim + 4 * lane;
+        if (P.out_bf16)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) =
+                make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + at) = y;
+    }
+}
+
+// ---------------------------------------------------------------------------------
+// launcher
+// ---------------------------------------------------------------------------------
+template <int kTiles>
+static cudaError_t launch_prefix_impl(const PrefixParams &P, const CUtensorMap &map, cudaStream_t stream)
+{
+    const int bytes = PfxSmem<kTiles>::bytes(P.num_groups);
+    // per process and device: the whole shared memory (an attribute of the function)
+    static unsigned long long done = 0;  // bit per device ordinal < 64
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(dev < 64 && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1ull)) {
+        e = cudaFuncSetAttribute(k_prefix<kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess && dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_ACQ_REL);
+    }
+    if (e != cudaSuccess) return e;
+    k_prefix<kTiles><<<P.grid, kPfxThreads, bytes, stream>>>(P, map);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_map, const AttnParams &A,
+                          const void *own_map, cudaStream_t stream)
+{
+    if (P.num_groups > 0 && P.grid > 0) {
+        CUtensorMap map;
+        memcpy(&map, prefix_map, sizeof map);
+        cudaError_t e = P.unit_rows == 256 ? launch_prefix_impl<2>(P, map, stream) : launch_prefix_impl<1>(P, map, stream);
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = launch_attention_partials(A, format, own_map, stream);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(P.batch * P.hkv * P.G);
+    cfg.blockDim = dim3(kMergeThreads);
+    // most partials of a row: every CTA of both kernels, two streams each of the prefix's
+    cfg.dynamicSmemBytes = (size_t)(2 * P.grid + A.grid) * sizeof(float2);
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_prefix_merge, P, A);
+}
+
+}  // namespace kvz

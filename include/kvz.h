@@ -253,6 +253,54 @@ int kvz_decode_attention_noalloc(kvz_dims dims, int32_t batch, int32_t num_q_hea
                                  int64_t num_raw_pages, float *out, uint32_t *status, kvz_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * kvz_prefix_attention / kvz_prefix_attention_raw -- decode attention of a batch whose
+ * sequences share prefixes: a system prompt, a document, the prompt of several samples.
+ * The prefix's pages are stored once and read once for all sequences of a group; the pages
+ * name no such call.  Everything not listed is as in kvz_decode_attention and
+ * kvz_decode_attention_raw, for the sequences' own tokens behind the prefix.
+ *
+ *  group_start  int32 [num_groups + 1] (0 <= num_groups <= 256), non-decreasing, within
+ *               [0, batch]: group g is the sequences [group_start[g], group_start[g+1]).
+ *               A sequence of no group attends to its own tokens alone.  Out of order or
+ *               range: KVZ_STATUS_BAD_ORDER, and no prefix is read
+ *  prefix_ids   int32 [num_groups][max_prefix_pages] meta page ids of each prefix's
+ *               completed pages (raw call: raw page ids of all its pages)
+ *  prefix_lens  int32 [num_groups] tokens of each prefix, any length (0: none).  A negative
+ *               length counts as 0, one beyond the table as the table's, both flagged
+ *               KVZ_STATUS_BAD_INDEX
+ *  prefix_tail  int32 [num_groups] raw page id of the last prefix_lens%16 tokens (-1 when
+ *               there are none); not in the raw call, whose table names the last page
+ *  page_ids, max_pages, seq_lens, tail_page: each sequence's own tokens, behind the prefix
+ *  out          out_type KVZ_OUT_F32: float32, KVZ_OUT_BF16: BF16 (rounded once at the
+ *               end), [batch][num_q_heads][128], 16-byte aligned:
+ *               softmax(q.K^T / sqrt(128)) V over the prefix and the own tokens
+ *  workspace    >= kvz_prefix_attention_workspace_size(dims, batch, num_q_heads,
+ *               num_groups, prefix_pages, table_pages) bytes, where the compressed call
+ *               counts the tail slots: prefix_pages = max_prefix_pages + 1, table_pages =
+ *               max_pages + 1 (raw call: without the + 1; more is never too small)
+ * Prefix pages may be pages of other sequences.  A page with unusable metadata or an index
+ * out of range is left out of the softmax and flagged; a row without any token is zero.
+ * Results depend on the data, the shapes, the lengths and the device's SM count only.
+ * --------------------------------------------------------------------------------- */
+#define KVZ_OUT_F32 0
+#define KVZ_OUT_BF16 1
+size_t kvz_prefix_attention_workspace_size(kvz_dims dims, int32_t batch, int32_t num_q_heads, int32_t num_groups,
+                                           int32_t prefix_pages, int32_t table_pages);
+int kvz_prefix_attention(kvz_dims dims, int32_t batch, int32_t num_q_heads, const void *q, int32_t num_groups,
+                         const int32_t *group_start, const int32_t *prefix_ids, int32_t max_prefix_pages,
+                         const int32_t *prefix_lens, const int32_t *prefix_tail, const int32_t *page_ids,
+                         int32_t max_pages, const int32_t *seq_lens, const int32_t *tail_page, const uint64_t *meta,
+                         int64_t num_meta_pages, const uint8_t *arena, uint64_t arena_bytes, const void *raw_pool,
+                         int64_t num_raw_pages, void *out, int32_t out_type, void *workspace, size_t workspace_bytes,
+                         uint32_t *status, kvz_stream_t stream);
+int kvz_prefix_attention_raw(kvz_dims dims, int32_t batch, int32_t num_q_heads, const void *q, int32_t num_groups,
+                             const int32_t *group_start, const int32_t *prefix_ids, int32_t max_prefix_pages,
+                             const int32_t *prefix_lens, const int32_t *page_ids, int32_t max_pages,
+                             const int32_t *seq_lens, const void *raw_pool, int64_t num_raw_pages, void *out,
+                             int32_t out_type, void *workspace, size_t workspace_bytes, uint32_t *status,
+                             kvz_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * kvz_append_tokens -- write new tokens' keys and values into raw pages (a decode step's
  * token per sequence, or a batch of prompts), with the rotary position applied to the
  * keys on the way, and rotate the tokens' queries for the attention call that follows.

@@ -256,6 +256,10 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     P.max_tokens = X.max_pages * kPage + (raw ? 0 : kPage - 1);
     P.unit_rows = pfx_unit_rows(batch, G, X.groups);
     P.grid = pgrid;
+    // blocks of 128 tokens (16 steps of a sum) between folds.  Each step drops about half of the
+    // last bit, 2^-25 of the sum: 8 blocks keep a float32 output within 2^-18 of that bias, 256
+    // keep it under a BF16 output's rounding (2^-9 a value)
+    P.fold = out_type == KVZ_OUT_BF16 ? 256 : 8;
     P.q = static_cast<const uint16_t *>(q);
     P.group_start = X.group_start;
     P.prefix_ids = X.ids;

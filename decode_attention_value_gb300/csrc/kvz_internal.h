@@ -131,6 +131,7 @@ struct PrefixParams {
     int max_tokens;  // most prefix tokens the tables can name
     int unit_rows;   // query rows of a CTA's tile: 128 or 256
     int grid;        // CTAs
+    int fold;        // blocks of a stream summed in tensor memory at a time
     const uint16_t *q;
     const int32_t *group_start, *prefix_ids, *prefix_lens, *prefix_tail;
     const uint64_t *meta;

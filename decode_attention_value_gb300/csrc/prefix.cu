@@ -21,8 +21,17 @@ constexpr int kPfxBlock = 128;                   // tokens of a block: 8 pages
 constexpr int kPfxPages = kPfxBlock / kPage;
 constexpr uint32_t kUnitBytes = kPfxBlock * kDim * 2;  // K or V of a block, BF16
 constexpr uint32_t kHalfBytes = kUnitBytes / 2;        // its 64-column halves
-constexpr int kPfxThreads = 320;  // two softmax warpgroups, the producer warp, the issuing warp
+constexpr uint32_t kQTileBytes = 128 * kDim * 2;       // 128 query rows, BF16
+constexpr uint32_t kQHalfBytes = kQTileBytes / 2;
+// Two softmax warpgroups and one with the producer and the issuing warp.  168 registers a thread
+// at launch (64512); the softmax threads take 208 of them (256 x 208 + 128 x 80 = 63488): a
+// thread's scores and weights stay in registers.
+constexpr int kPfxThreads = 384;
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 constexpr int kInfoRing = 8;
+// tensor memory, 256 columns a stream: 128 of scores, overwritten by the weights of the first and
+// of the second 64 tokens (32 columns of high, 32 of low parts each), and 128 of output
+constexpr uint32_t kColO = 256;
 
 // Two streams of softmax threads share a CTA.  kTiles = 2: 256 query rows, stream s holds rows
 // [128 s, 128 s + 128) and both see every block.  kTiles = 1: 128 rows, the streams take
@@ -31,13 +40,13 @@ template <int kTiles>
 struct PfxSmem {
     static constexpr int units = kTiles == 2 ? 5 : 6;  // ring of K and V blocks
     static constexpr int q = 0;
-    static constexpr int ring = q + kTiles * (int)kUnitBytes;
+    static constexpr int ring = q + kTiles * (int)kQTileBytes;
     static constexpr int full = ring + units * (int)kUnitBytes;
     static constexpr int empty = full + units * 8;
     static constexpr int qfull = empty + units * 8;
-    static constexpr int sfull = qfull + 8;   // [2] scores of a stream are in tensor memory
-    static constexpr int pready = sfull + 16;  // [2] its weights are
-    static constexpr int ofull = pready + 16;  // [2] its output of the segment is complete
+    static constexpr int sfull = qfull + 8;    // [2] scores of a stream are in tensor memory
+    static constexpr int pready = sfull + 16;  // [2][2] its weights of half a block are
+    static constexpr int ofull = pready + 32;  // [2] its output of the segment is complete
     static constexpr int drain = ofull + 16;
     static constexpr int info = drain + 8;  // [kInfoRing] bad pages of a block
     static constexpr int misc = info + kInfoRing * 4;  // tensor memory address, abort flag
@@ -146,7 +155,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
         mbar_init(sbase + S::qfull, 256);
         for (int s = 0; s < 2; ++s) {
             mbar_init(sbase + S::sfull + 8 * s, 1);
-            mbar_init(sbase + S::pready + 8 * s, 128);
+            mbar_init(sbase + S::pready + 16 * s, 128);
+            mbar_init(sbase + S::pready + 16 * s + 8, 128);
             mbar_init(sbase + S::ofull + 8 * s, 1);
         }
         mbar_init(sbase + S::drain, 1);
@@ -195,11 +205,13 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
     const int lo = c < C ? pfx_first(c, W, C) : 0, hi = c < C ? pfx_first(c + 1, W, C) : 0;
     PfxWait wait{P.status, misc + 1, true};
 
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
         // =============================== producer ===============================
         // One lane per page, 32 pages (four blocks) at a time; the ids of the next four
-        // blocks are fetched while these are copied.  Eight pages of 16 rows make a block's
-        // K (or V) operand: two boxes a page, one per 64-column half.
+        // blocks are fetched while these are copied.  (Calling pages into L2 four blocks ahead
+        // made a 131072-token prefix 12% slower.)  Eight pages of 16 rows make a block's K (or V) operand: two
+        // boxes a page, one per 64-column half.
         prefetch_tensormap(&tmap);
         const uint64_t keep = l2_evict_last();
         const int pages = (hi - lo) * kPfxPages;
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
                         else mbar_arrive(fullbar);
                     }
                     __syncwarp();
-                    if (lane < 16 && row >= 0) {
+                    if (lane < 2 * kPfxPages && row >= 0) {
                         const uint32_t dst =
                             sbase + S::ring + slot * kUnitBytes + (lane & 1) * kHalfBytes + (lane >> 1) * (kPage * 128);
                         tensor_copy_2d_g2s(dst, &tmap, (lane & 1) * 64, row + kv * kPage, fullbar);
@@ -254,104 +266,181 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
         }
     } else if (warp == 9) {
         // ============================ matrix products ============================
-        if (lane == 0) {
-            constexpr uint32_t kQk = mma_desc(128, kPfxBlock, false), kPv = mma_desc(128, kDim, true);
-            auto unit_addr = [&](int it) { return sbase + S::ring + (it % kUnits) * kUnitBytes; };
-            auto wait_unit = [&](int it) {
-                wait(sbase + S::full + 8 * (it % kUnits), (it / kUnits) & 1);
-                tc_fence_after();
-            };
-            auto free_unit = [&](int it) { mma_commit(sbase + S::empty + 8 * (it % kUnits)); };
-            // scores of stream s over K block n
-            auto qk = [&](int s, int n) {
-                const uint64_t a = smem_desc(sbase + S::q + (kTiles == 2 ? s * kUnitBytes : 0), 16, 1024);
-                const uint64_t b = smem_desc(unit_addr(2 * n), 16, 1024);
+        // One warp issues for both streams in turn, which keeps them half a block apart: one
+        // stream's softmax runs while the other's products do.  (A warp per stream let them fall
+        // into step: 368 us against 313 for 128 x 8 heads over 65536 tokens.)
+        constexpr uint32_t kQk = mma_desc(128, kPfxBlock, false), kPv = mma_desc(128, kDim, true);
+        auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+        const uint32_t tm = uniform(tmem);
+        bool ok = true;
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+            if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity));
+            tc_fence_after();
+        };
+        auto unit_addr = [&](int it) { return uniform(sbase + S::ring + (it % kUnits) * kUnitBytes); };
+        auto wait_unit = [&](int it) { wait_all(sbase + S::full + 8 * (it % kUnits), (it / kUnits) & 1); };
+        // scores of stream s over K block n; give_back: the last product that reads the block
+        auto qk = [&](int s, int n, bool give_back) {
+            const uint64_t a = smem_desc(sbase + S::q + (kTiles == 2 ? s * kQTileBytes : 0), 16, 1024);
+            const uint64_t b = smem_desc(unit_addr(2 * n), 16, 1024);
+            const uint32_t freebar = uniform(sbase + S::empty + 8 * (2 * n % kUnits));
+            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {  // 16 of the 128 dims: 32 bytes within a half's rows
-                    const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-                    mma_ss(tmem + s * 128, a + off, b + off, kQk, k > 0);
-                }
+                for (int k = 0; k < 8; ++k)  // 16 of the 128 dims: 32 bytes within a half's rows
+                    mma_ss(tm + s * 128, a + (((k >> 2) * kQHalfBytes + (k & 3) * 32) >> 4),
+                           b + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4), kQk, k > 0);
                 mma_commit(sbase + S::sfull + 8 * s);
-            };
-            // output of stream s: its weights (high and low parts) times V block n
-            auto pv = [&](int s, int n, bool add) {
-                const uint64_t b = smem_desc(unit_addr(2 * n + 1), kHalfBytes, 1024);
+                if (give_back) mma_commit(freebar);
+            }
+            __syncwarp();
+        };
+        // output of stream s: its weights (high and low parts) of 64 tokens times half of V block n
+        auto pv = [&](int s, int n, int half, bool add, bool last, bool give_back) {
+            const uint64_t b = smem_desc(unit_addr(2 * n + 1) + half * 8192, kHalfBytes, 1024);
+            const uint32_t freebar = uniform(sbase + S::empty + 8 * ((2 * n + 1) % kUnits));
+            if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)  // 16 tokens: two atoms of V rows, eight columns of weights
-                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * 64 + k * 8, b + ((k * 2048) >> 4), kPv,
-                               add || part || k);
-            };
-            uint32_t pphase[2] = {0, 0};
-            int seg = 0;
-            for (int x = lo; x < hi && wait.ok; ++seg) {
-                const PfxSeg sg = pfx_locate(P, plan, x, hi);
-                const int n0 = x - lo, nb = sg.blocks;
-                wait(sbase + S::qfull, seg & 1);
-                constexpr int step = kTiles == 2 ? 1 : 2;  // blocks between a stream's blocks
-                for (int s = 0; s < 2; ++s) {
-                    const int j = kTiles == 2 ? 0 : s;
-                    if (j >= nb) break;
-                    if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j));
-                    if (!wait.ok) break;
-                    qk(s, n0 + j);
-                    if (kTiles == 1 || s == 1) free_unit(2 * (n0 + j));
-                }
-                for (int i = 0; i < (kTiles == 2 ? 2 * nb : nb) && wait.ok; ++i) {
-                    const int s = i & 1, j = kTiles == 2 ? i >> 1 : i;
-                    wait(sbase + S::pready + 8 * s, pphase[s]);
-                    pphase[s] ^= 1;
-                    if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j) + 1);
-                    else tc_fence_after();
-                    if (!wait.ok) break;
-                    pv(s, n0 + j, j >= step);
-                    if (j + step >= nb) mma_commit(sbase + S::ofull + 8 * s);
-                    if (kTiles == 1 || s == 1) free_unit(2 * (n0 + j) + 1);
-                    if (j + step < nb) {
-                        if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j + step));
-                        if (!wait.ok) break;
-                        qk(s, n0 + j + step);
-                        if (kTiles == 1 || s == 1) free_unit(2 * (n0 + j + step));
-                    }
-                }
-                x += nb;
+                    for (int k = 0; k < 4; ++k)  // 16 tokens: two atoms of V rows, eight columns of weights
+                        mma_ts(tm + kColO + s * 128, tm + s * 128 + half * 64 + part * 32 + k * 8, b + ((k * 2048) >> 4),
+                               kPv, part || k ? true : add);
+                if (last) mma_commit(sbase + S::ofull + 8 * s);
+                if (give_back) mma_commit(freebar);
             }
-            if (!wait.ok) {  // no product in flight when tensor memory is given back
-                mma_commit(sbase + S::drain);
-                mbar_wait(sbase + S::drain, 0, P.status);
-            }
-        }
-        __syncwarp();
-    } else {
-        // ================================ softmax ================================
-        // Thread = query row.  Its 128 scores of a block come from tensor memory at once; the
-        // weights go back over them as two BF16 parts, p = high + low (16 bits of p).  The
-        // running maximum moves, and the output is rescaled, only when it grows by more than
-        // 2^8: weights up to 2^8 lose nothing in floating point.
-        const int s = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + 256 + s * 128 + lanes;
-        uint32_t sphase = 0, ophase = 0;
-        for (int x = lo; x < hi;) {  // (after a wait that gave up, every segment's barrier still)
+            __syncwarp();
+        };
+        constexpr int step = kTiles == 2 ? 1 : 2;  // blocks between a stream's blocks
+        uint32_t pphase = 0;                       // bit s
+        int seg = 0;
+        for (int x = lo; x < hi && ok; ++seg) {
             const PfxSeg sg = pfx_locate(P, plan, x, hi);
             const int n0 = x - lo, nb = sg.blocks;
-            // ---- queries to shared memory (every product of the last segment is complete) ----
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            for (int i = tid; i < kTiles * 128 * 16; i += 256) {
-                const int row = i >> 4, ch = i & 15, grow = sg.tile * P.unit_rows + row;
-                uint4 v = make_uint4(0, 0, 0, 0);
+            wait_all(sbase + S::qfull, seg & 1);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int j = kTiles == 2 ? 0 : s;
+                if (j >= nb || !ok) break;
+                if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j));
+                if (ok) qk(s, n0 + j, kTiles == 1 || s == 1);
+            }
+            for (int i = 0; i < (kTiles == 2 ? nb : (nb + 1) / 2) && ok; ++i) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {  // the streams in turn
+                    const int j = kTiles == 2 ? i : 2 * i + s;
+                    if (j >= nb || !ok) break;
+                    if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j) + 1);
+                    wait_all(sbase + S::pready + 16 * s, pphase >> s & 1);
+                    if (!ok) break;
+                    pv(s, n0 + j, 0, i % P.fold != 0, false, false);
+                    if (j + step < nb && (kTiles == 1 || s == 0)) wait_unit(2 * (n0 + j + step));
+                    wait_all(sbase + S::pready + 16 * s + 8, pphase >> s & 1);
+                    if (!ok) break;
+                    pphase ^= 1u << s;
+                    pv(s, n0 + j, 1, true, j + step >= nb, kTiles == 1 || s == 1);
+                    if (j + step < nb) qk(s, n0 + j + step, kTiles == 1 || s == 1);
+                }
+            }
+            x += nb;
+        }
+        if (!ok) {  // no product in flight when tensor memory is given back
+            if (elect_one()) mma_commit(sbase + S::drain);
+            __syncwarp();
+            mbar_wait(sbase + S::drain, 0, P.status);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ================================ softmax ================================
+        // Thread = query row.  Its 128 scores of a block come from tensor memory at once;
+        // the weights go back over them, 64 tokens at a time, as two BF16 parts, p = high + low (16
+        // bits of p); the product with the first half of V runs while the second half is made.  The
+        // running maximum moves, and the output is rescaled, only when it grows by more than
+        // 2^8: weights up to 2^8 lose nothing in floating point.  Every P.fold blocks the output
+        // is added to the partial in memory and begins anew: the tensor cores' fp32 sums drop
+        // the bits below the accumulator's last, a bias that grows with the steps of a sum.
+        const int s = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + kColO + s * 128 + lanes;
+        const uint64_t scale = pack2(P.scale_log2, P.scale_log2), minus = pack2(-1.f, -1.f);
+        uint32_t sphase = 0, ophase = 0;
+        for (int x = lo; x < hi;) {  // (after a wait that gave up, every segment's barriers still)
+            const PfxSeg sg = pfx_locate(P, plan, x, hi);
+            const int n0 = x - lo, nb = sg.blocks;
+            // ---- queries to shared memory: sixteen threads a row; all loads in flight at once, and
+            // before the barrier (behind it every product of the last segment is complete) ----
+            const int ch = tid & 15;
+            uint4 qv[8 * kTiles];
+#pragma unroll
+            for (int i = 0; i < 8 * kTiles; ++i) {
+                const int row = (tid >> 4) + 16 * i, grow = sg.tile * P.unit_rows + row;
+                qv[i] = make_uint4(0, 0, 0, 0);
                 if (row < sg.rows)
-                    v = *reinterpret_cast<const uint4 *>(
+                    qv[i] = *reinterpret_cast<const uint4 *>(
                         P.q + ((int64_t)(sg.seq0 + grow / P.G) * P.hkv * P.G + sg.kvh * P.G + grow % P.G) * kDim + ch * 8);
-                *reinterpret_cast<uint4 *>(smem + S::q + (row >> 7) * kUnitBytes + (ch >> 3) * kHalfBytes +
-                                           (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4)) = v;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 8 * kTiles; ++i) {
+                const int row = (tid >> 4) + 16 * i;
+                *reinterpret_cast<uint4 *>(smem + S::q + (row >> 7) * kQTileBytes + (ch >> 3) * kQHalfBytes +
+                                           (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4)) = qv[i];
             }
             fence_async_shared();
             mbar_arrive(sbase + S::qfull);
             const int row0 = kTiles == 2 ? s * 128 : 0;
             const bool active = row0 + quad * 32 < sg.rows;  // a warp without rows only keeps step
+            const int64_t slot0 = ((int64_t)(sg.unit + c) * 2 + s) * 128 + quad * 32;  // the warp's first row
+            const int rows = min(32, sg.rows - row0 - quad * 32);
             float m = -INFINITY, l = 0.f;
+            // The warp's 32 rows of output, complete in tensor memory and relative to maximum ref,
+            // added to their partials, 32 columns at a time.
+            float fm = 0.f;  // the partials' maximum
+            bool folded = false;
+            auto fold = [&](float ref, uint8_t *stage) {
+                const float f = !folded || fm == -INFINITY ? 0.f : ex2(fm - ref);
+#pragma unroll 1
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * w, o);
+                    tmem_wait_ld(o);
+                    if (!stage) {  // within a segment: each lane its row
+                        if (lane >= rows) continue;
+                        float *at = P.part_o + (slot0 + lane) * kDim + 32 * w;
+                        if (folded)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(fmaf(at[i], f, __uint_as_float(o[i])));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) st_global_32b(at + 8 * i, o + 8 * i);
+                        continue;
+                    }
+                    // at its end: through 4 KB of the queries' shared memory, so that memory sees
+                    // whole lines (32-byte stores to 32 rows an instruction took 2.5 us a tile)
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + (lane >> 3), col = lane & 7;
+                        float4 y = *reinterpret_cast<const float4 *>(stage + row * 128 + ((col ^ (row & 7)) << 4));
+                        const float fr = __shfl_sync(0xffffffffu, f, row);
+                        if (row < rows) {
+                            float4 *at = reinterpret_cast<float4 *>(P.part_o + (slot0 + row) * kDim + 32 * w) + col;
+                            if (folded) {
+                                const float4 z = *at;
+                                y = make_float4(fmaf(z.x, fr, y.x), fmaf(z.y, fr, y.y), fmaf(z.z, fr, y.z),
+                                                fmaf(z.w, fr, y.w));
+                            }
+                            *at = y;
+                        }
+                    }
+                }
+                fm = ref;
+                folded = true;
+            };
             int mine = 0;
             for (int j = kTiles == 2 ? 0 : s; j < nb; j += kTiles == 2 ? 1 : 2, ++mine) {
                 const int n = n0 + j;
@@ -359,6 +448,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
                 sphase ^= 1;
                 if (!__all_sync(0xffffffffu, wait.ok)) break;
                 tc_fence_after();
+                // (the products behind these scores were issued after every earlier product of the
+                // stream, so its output is complete)
+                const bool fresh = mine % P.fold == 0;  // the output begins anew
+                if (fresh && mine > 0 && active) fold(m, nullptr);
                 const int left = sg.len - (sg.block0 + j) * kPfxBlock;
                 const uint32_t bad = info[n % kInfoRing];
                 const bool whole = left >= kPfxBlock && bad == 0;
@@ -382,6 +475,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
                     fence_async_shared();
                     if (!__all_sync(0xffffffffu, wait.ok)) break;
                 }
+                float u = 0.f;
                 if (active) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) tmem_wait_ld(v[w]);
@@ -399,17 +493,18 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
                     for (int w = 0; w < 4; ++w) {
                         top[w] = __uint_as_float(v[w][0]);
 #pragma unroll
-                        for (int i = 1; i < 32; ++i) top[w] = fmaxf(top[w], __uint_as_float(v[w][i]));
+                        for (int i = 1; i < 31; i += 2)
+                            top[w] = max3(top[w], __uint_as_float(v[w][i]), __uint_as_float(v[w][i + 1]));
                     }
-                    const float bm = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * P.scale_log2;
-                    const bool grow = mine == 0 ? true : bm > m + 8.f;
+                    top[0] = max3(top[0], __uint_as_float(v[0][31]), __uint_as_float(v[1][31]));
+                    top[1] = max3(top[1], __uint_as_float(v[2][31]), __uint_as_float(v[3][31]));
+                    const float bm = fmaxf(max3(top[0], top[1], top[2]), top[3]) * P.scale_log2;
+                    const bool grow = mine == 0 || bm > m + 8.f;
                     if (mine > 0 && __any_sync(0xffffffffu, grow)) {
-                        // (the products behind these scores were issued after every earlier
-                        // product of the stream, so the output is complete)
                         const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - bm)) : 1.f;
                         l *= f;
 #pragma unroll 1
-                        for (int w = 0; w < 4; ++w) {
+                        for (int w = 0; w < 4 && !fresh; ++w) {
                             uint32_t o[32];
                             tmem_ld32(tO + 32 * w, o);
                             tmem_wait_ld(o);
@@ -419,52 +514,59 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
                         }
                     }
                     if (grow) m = bm;
-                    const float u = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t hi2[16], lo2[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float p0 = ex2(fmaf(__uint_as_float(v[w][2 * i]), P.scale_log2, -u));
-                            const float p1 = ex2(fmaf(__uint_as_float(v[w][2 * i + 1]), P.scale_log2, -u));
-                            sum[i & 3] += p0 + p1;
-                            hi2[i] = pack_bf16x2(p0, p1);
-                            lo2[i] = pack_bf16x2(p0 - __uint_as_float(hi2[i] << 16),
-                                                 p1 - __uint_as_float(hi2[i] & 0xFFFF0000u));
-                        }
-                        tmem_st16(tS + 16 * w, hi2);
-                        tmem_st16(tS + 64 + 16 * w, lo2);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_wait_st();
+                    u = m == -INFINITY ? 0.f : m;
                 }
-                tc_fence_before();
-                mbar_arrive(sbase + S::pready + 8 * s);
+                const uint64_t shift = pack2(-u, -u);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (active) {
+#pragma unroll
+                        for (int w = 2 * half; w < 2 * half + 2; ++w) {
+                            uint32_t hi2[16], lo2[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float p0, p1;
+                                unpack2(fma2(pack2(__uint_as_float(v[w][2 * i]), __uint_as_float(v[w][2 * i + 1])), scale,
+                                             shift),
+                                        p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                const uint64_t p = pack2(p0, p1);
+                                sum[i & 1] = add2(sum[i & 1], p);
+                                hi2[i] = pack_bf16x2(p0, p1);
+                                float r0, r1;
+                                unpack2(fma2(pack2(__uint_as_float(hi2[i] << 16), __uint_as_float(hi2[i] & 0xFFFF0000u)),
+                                             minus, p),
+                                        r0, r1);
+                                lo2[i] = pack_bf16x2(r0, r1);
+                            }
+                            tmem_st16(tS + 64 * half + 16 * (w & 1), hi2);
+                            tmem_st16(tS + 64 * half + 32 + 16 * (w & 1), lo2);
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(sbase + S::pready + 16 * s + 8 * half);
+                }
+                if (active) {
+                    float s0, s1;
+                    unpack2(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
+                }
             }
             // ---- the segment's partial ----
-            const int64_t slot = ((int64_t)(sg.unit + c) * 2 + s) * 128 + r;
-            const bool live = row0 + r < sg.rows;
             if (mine > 0) {
                 wait(sbase + S::ofull + 8 * s, ophase);
                 ophase ^= 1;
                 tc_fence_after();
-                if (__all_sync(0xffffffffu, wait.ok) && active) {
-#pragma unroll 1
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + 32 * w, o);
-                        tmem_wait_ld(o);
-                        if (live) {
-                            uint4 *at = reinterpret_cast<uint4 *>(P.part_o + slot * kDim + 32 * w);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) at[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        }
-                    }
-                }
-                tc_fence_before();
             }
-            if (live) *reinterpret_cast<float2 *>(P.part_ml + slot * 2) = make_float2(m, l);
+            // (one tile: the other stream's last scores have read the queries too)
+            if (kTiles == 1) asm volatile("bar.sync 2, 256;" ::: "memory");
+            if (mine > 0 && active && __all_sync(0xffffffffu, wait.ok))
+                fold(m, smem + S::q + (kTiles == 2 ? s * kQTileBytes : 0) + (kTiles == 2 ? quad : warp) * 4096);
+            tc_fence_before();
+            if (lane < rows) *reinterpret_cast<float2 *>(P.part_ml + (slot0 + lane) * 2) = make_float2(m, l);
             x += nb;
         }
     }

@@ -23,11 +23,11 @@ constexpr uint32_t kUnitBytes = kPfxBlock * kDim * 2;  // K or V of a block, BF1
 constexpr uint32_t kHalfBytes = kUnitBytes / 2;        // its 64-column halves
 constexpr uint32_t kQTileBytes = 128 * kDim * 2;       // 128 query rows, BF16
 constexpr uint32_t kQHalfBytes = kQTileBytes / 2;
-// Two softmax warpgroups and one with the producer and the issuing warp.  168 registers a thread
-// at launch (64512); the softmax threads take 208 of them (256 x 208 + 128 x 80 = 63488): a
-// thread's scores and weights stay in registers.
-constexpr int kPfxThreads = 384;
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+constexpr int kExpWarps = 4;   // 12-bit pages: warps that restore BF16 operands (warps 10 to 13)
+constexpr int kPageStages = 8;  // 12-bit pages: ring of coded pages, one block
+constexpr uint32_t kPageBytes = 2 * kPage * kDim * 2;  // most bytes of a coded (or raw) K and V page
+static_assert(kPageStages == kPfxPages, "a page's stage is its place in its block");
+static_assert(kPageStages % kExpWarps == 0, "a stage's pages all go to one warp, which sees each of its phases");
 constexpr int kInfoRing = 8;
 // tensor memory, 256 columns a stream: 128 of scores, overwritten by the weights of the first and
 // of the second 64 tokens (32 columns of high, 32 of low parts each), and 128 of output
@@ -36,19 +36,34 @@ constexpr uint32_t kColO = 256;
 // Two streams of softmax threads share a CTA.  kTiles = 2: 256 query rows, stream s holds rows
 // [128 s, 128 s + 128) and both see every block.  kTiles = 1: 128 rows, the streams take
 // alternate blocks and leave separate partials.
-template <int kTiles>
+//
+// Raw pages are copied by TMA into the operands' layout; 12-bit pages are copied as they are into
+// a ring of page stages, and four warps restore them into the operands' blocks.  The softmax
+// threads take most registers, so that a thread's scores and weights stay in them: 168 a thread at
+// launch (64512) become 256 x 208 + 128 x 80 = 63488 for raw pages; 128 (65536) become
+// 256 x 200 + 256 x 56 = 65536 for 12-bit pages.
+template <int kFmt, int kTiles>
 struct PfxSmem {
-    static constexpr int units = kTiles == 2 ? 5 : 6;  // ring of K and V blocks
+    static constexpr bool coded = kFmt != kFmtRaw;
+    static constexpr int threads = coded ? 512 : 384;
+    static constexpr int softmax_regs = coded ? 200 : 208, other_regs = coded ? 56 : 80;
+    // ring of K and V blocks
+    static constexpr int units = coded ? (kTiles == 2 ? 3 : 4) : (kTiles == 2 ? 5 : 6);
+    static constexpr int arrivals = coded ? kPfxPages : 1;  // that fill a block
     static constexpr int q = 0;
     static constexpr int ring = q + kTiles * (int)kQTileBytes;
-    static constexpr int full = ring + units * (int)kUnitBytes;
+    static constexpr int stage = ring + units * (int)kUnitBytes;
+    static constexpr int full = stage + (coded ? kPageStages * (int)kPageBytes : 0);
     static constexpr int empty = full + units * 8;
     static constexpr int qfull = empty + units * 8;
     static constexpr int sfull = qfull + 8;    // [2] scores of a stream are in tensor memory
     static constexpr int pready = sfull + 16;  // [2][2] its weights of half a block are
     static constexpr int ofull = pready + 32;  // [2] its output of the segment is complete
     static constexpr int drain = ofull + 16;
-    static constexpr int info = drain + 8;  // [kInfoRing] bad pages of a block
+    static constexpr int sempty = drain + 8;                               // page stages
+    static constexpr int sarrived = sempty + (coded ? kPageStages * 8 : 0);
+    static constexpr int sinfo = (sarrived + (coded ? kPageStages * 8 : 0) + 15) & ~15;
+    static constexpr int info = sinfo + (coded ? kPageStages * 16 : 0);  // [kInfoRing] bad pages of a block
     static constexpr int misc = info + kInfoRing * 4;  // tensor memory address, abort flag
     static constexpr int plan = misc + 16;  // [groups + 1] {first unit, first block}
     static int bytes(int groups) { return plan + (groups + 1) * 8; }
@@ -130,10 +145,34 @@ struct PfxWait {
     }
 };
 
-template <int kTiles>
-__global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P, const __grid_constant__ CUtensorMap tmap)
+// A page in its stage.
+struct __align__(16) PageInfo {
+    uint32_t kind, valid, tagsK, tagsV;  // valid: tokens of a raw page
+};
+enum : uint32_t { kPageNone = 0, kPageCoded = 1, kPageRaw = 2 };
+
+// One 512-value block of a 12-bit group -> two 16 x 16 fragments of four 8 x 8 matrices.
+__device__ __forceinline__ void pfx_restore(const uint8_t *blk, uint32_t tag, int lane, uint32_t (&a0)[4], uint32_t (&a1)[4])
 {
-    using S = PfxSmem<kTiles>;
+    if (tag == 0xFFu) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(blk + 32 * lane);
+        const uint4 y = *reinterpret_cast<const uint4 *>(blk + 32 * lane + 16);
+        a0[0] = x.x; a0[1] = x.y; a0[2] = x.z; a0[3] = x.w;
+        a1[0] = y.x; a1[1] = y.y; a1[2] = y.z; a1[3] = y.w;
+    } else {
+        const uint4 low = *reinterpret_cast<const uint4 *>(blk + 16 * lane);
+        const uint2 code = *reinterpret_cast<const uint2 *>(blk + 512 + 8 * lane);
+        restore_fragment(low.x, low.y, code.x, tag * 0x01010101u, a0);
+        restore_fragment(low.z, low.w, code.y, tag * 0x01010101u, a1);
+    }
+}
+
+template <int kFmt, int kTiles>
+__global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
+    k_prefix(const PrefixParams P, const __grid_constant__ CUtensorMap tmap)
+{
+    using S = PfxSmem<kFmt, kTiles>;
+    constexpr bool kCoded = S::coded;
     constexpr int kUnits = S::units;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
@@ -149,7 +188,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
 
     if (tid == 0) {
         for (int s = 0; s < kUnits; ++s) {
-            mbar_init(sbase + S::full + 8 * s, 1);
+            mbar_init(sbase + S::full + 8 * s, S::arrivals);
             mbar_init(sbase + S::empty + 8 * s, 1);
         }
         mbar_init(sbase + S::qfull, 256);
@@ -160,6 +199,11 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
             mbar_init(sbase + S::ofull + 8 * s, 1);
         }
         mbar_init(sbase + S::drain, 1);
+        if (kCoded)
+            for (int s = 0; s < kPageStages; ++s) {
+                mbar_init(sbase + S::sempty + 8 * s, 1);
+                mbar_init(sbase + S::sarrived + 8 * s, 1);
+            }
         misc[1] = 0;
         fence_barrier_init();
     }
@@ -205,8 +249,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
     const int lo = c < C ? pfx_first(c, W, C) : 0, hi = c < C ? pfx_first(c + 1, W, C) : 0;
     PfxWait wait{P.status, misc + 1, true};
 
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8) {
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::other_regs));
+    if (warp == 8 && !kCoded) {
         // =============================== producer ===============================
         // One lane per page, 32 pages (four blocks) at a time; the ids of the next four
         // blocks are fetched while these are copied.  (Calling pages into L2 four blocks ahead
@@ -263,6 +307,167 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
         if (!ok) {
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 1000000) {}
+        }
+    } else if (warp == 8) {
+        // ========================= producer, 12-bit pages =========================
+        // One lane per page, 32 pages (four blocks) at a time: the metadata of the next four
+        // blocks and the ids of the four behind them are fetched while these are copied.  Eight
+        // lanes, a block's pages, wait for their stages and issue together.
+        const uint64_t keep = l2_evict_last();
+        const int pages = (hi - lo) * kPfxPages;
+        struct Pre {
+            int32_t id, kvh;
+            int kind, valid;
+        };
+        auto prep = [&](int y) -> Pre {
+            Pre r{-1, 0, kPageNone, 0};
+            if (y >= pages) return r;
+            const PfxSeg s = pfx_locate(P, plan, lo + y / kPfxPages, hi);
+            const int p = s.block0 * kPfxPages + y % kPfxPages;
+            if (p * kPage >= s.len) return r;
+            r.kvh = s.kvh;
+            r.kind = p < s.len / kPage ? kPageCoded : kPageRaw;  // the raw tail is the last page
+            r.valid = min(kPage, s.len - p * kPage);
+            r.id = r.kind == kPageCoded ? ld_keep_s32(P.prefix_ids + (int64_t)s.g * P.max_pages + p, keep)
+                                        : ld_keep_s32(P.prefix_tail + s.g, keep);
+            return r;
+        };
+        auto load_meta = [&](const Pre &r, uint64_t &k, uint64_t &v) {
+            k = v = 0;
+            if (r.kind == kPageCoded && r.id >= 0 && r.id < P.num_meta_pages)
+                ld_keep_u64x2(P.meta + ((int64_t)r.id * P.hkv + r.kvh) * 2, keep, k, v);
+        };
+        Pre cur = prep(lane), nxt = prep(32 + lane);
+        uint64_t mk, mv;
+        load_meta(cur, mk, mv);
+        bool ok = true;
+        for (int base = 0; base < pages && ok; base += 32) {
+            uint32_t kind = kPageNone, flag = 0, bk = 0, bv = 0;
+            uint64_t srck = 0, srcv = 0;
+            const uint32_t tk = (uint32_t)(mk >> 32), tv = (uint32_t)(mv >> 32);
+            if (cur.kind == kPageCoded) {
+                const uint32_t ok_ = (uint32_t)mk, ov_ = (uint32_t)mv;
+                if (cur.id < 0 || cur.id >= P.num_meta_pages) {
+                    flag = KVZ_STATUS_BAD_INDEX;
+                } else if (!tags_valid(tk) || !tags_valid(tv) || ok_ == KVZ_OFFSET_INVALID || ov_ == KVZ_OFFSET_INVALID ||
+                           ((uint64_t)ok_ + group_granules(tk)) * kGranule > P.arena_bytes ||
+                           ((uint64_t)ov_ + group_granules(tv)) * kGranule > P.arena_bytes) {
+                    flag = KVZ_STATUS_BAD_META;
+                } else {
+                    kind = kPageCoded;
+                    bk = group_granules(tk) * kGranule;
+                    bv = group_granules(tv) * kGranule;
+                    srck = (uint64_t)ok_ * kGranule;
+                    srcv = (uint64_t)ov_ * kGranule;
+                }
+            } else if (cur.kind == kPageRaw) {
+                if (cur.id < 0 || cur.id >= P.num_raw_pages) {
+                    flag = cur.id == -1 ? KVZ_STATUS_BAD_TAIL : KVZ_STATUS_BAD_INDEX;
+                } else {
+                    kind = kPageRaw;
+                    srck = ((uint64_t)cur.id * P.hkv + cur.kvh) * kPageBytes;
+                }
+            }
+            if (flag) atomicOr(P.status, flag);
+            const uint32_t bad = __ballot_sync(0xffffffffu, flag != 0);
+            const int valid = cur.valid;
+            cur = nxt;
+            load_meta(cur, mk, mv);
+            nxt = prep(base + 64 + lane);
+            for (int i = 0; i < 32 / kPfxPages && ok; ++i) {
+                const int n = base / kPfxPages + i;
+                if (n >= hi - lo) break;
+                if (lane / kPfxPages == i) {
+                    const int st = lane % kPfxPages;
+                    if (wait(sbase + S::sempty + 8 * st, (n & 1) ^ 1)) {
+                        const uint32_t bar = sbase + S::sarrived + 8 * st, dst = sbase + S::stage + st * kPageBytes;
+                        if (st == 0) info[n % kInfoRing] = (bad >> (kPfxPages * i)) & 0xFFu;
+                        *reinterpret_cast<PageInfo *>(smem + S::sinfo + 16 * st) = PageInfo{kind, (uint32_t)valid, tk, tv};
+                        if (kind == kPageCoded) {
+                            mbar_arrive_expect_tx(bar, bk + bv);
+                            if (srcv == srck + bk) {  // pages encoded together: one copy
+                                bulk_copy_g2s(dst, P.arena + srck, bk + bv, bar);
+                            } else {
+                                bulk_copy_g2s(dst, P.arena + srck, bk, bar);
+                                bulk_copy_g2s(dst + bk, P.arena + srcv, bv, bar);
+                            }
+                        } else if (kind == kPageRaw) {
+                            mbar_arrive_expect_tx(bar, kPageBytes);
+                            bulk_copy_g2s(dst, reinterpret_cast<const uint8_t *>(P.raw_pool) + srck, kPageBytes, bar);
+                        } else {
+                            mbar_arrive(bar);
+                        }
+                    }
+                }
+                ok = __all_sync(0xffffffffu, wait.ok);
+            }
+        }
+        if (!ok) {  // (as above: no copies in flight at the end)
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000) {}
+        }
+    } else if (kCoded && warp >= 10 && warp < 10 + kExpWarps) {
+        // ================== 12-bit pages to BF16 operands ==================
+        // A warp takes two pages of each block, K of both before V of either: K's block must not
+        // wait for the room that V's does.  A block's fragments are 8 x 8 matrices in the storage
+        // order's lanes: stmatrix puts their rows where the swizzled operand wants them (V's
+        // fragments are transposed, dims x tokens, and are stored back as tokens x dims).
+        constexpr int kMine = kPfxPages / kExpWarps;
+        const int mi = lane >> 3, rr = lane & 7;
+        bool ok = true;
+        for (int n = 0; n < hi - lo && ok; ++n) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int it = 2 * n + kv, slot = it % kUnits;
+                if (ok) ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, ((it / kUnits) & 1) ^ 1));
+                const uint32_t unit = sbase + S::ring + slot * kUnitBytes;
+#pragma unroll 1
+                for (int q = 0; q < kMine && ok; ++q) {
+                    const int st = warp - 10 + q * kExpWarps;
+                    const uint8_t *src = smem + S::stage + st * kPageBytes;
+                    if (kv == 0) ok = __all_sync(0xffffffffu, wait(sbase + S::sarrived + 8 * st, n & 1));
+                    if (!ok) break;
+                    const PageInfo pi = *reinterpret_cast<const PageInfo *>(smem + S::sinfo + 16 * st);
+                    if (pi.kind == kPageCoded) {
+                        const uint32_t tags = kv ? pi.tagsV : pi.tagsK;
+                        const int row = 16 * st + rr + 8 * (kv ? mi >> 1 : mi & 1), c8 = kv ? mi & 1 : mi >> 1;
+                        uint32_t off = kv ? group_granules(pi.tagsK) * kGranule : 0;  // V right after K
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t tag = (tags >> (8 * j)) & 0xFFu;
+                            uint32_t a[2][4];
+                            pfx_restore(src + off, tag, lane, a[0], a[1]);
+#pragma unroll
+                            for (int f = 0; f < 2; ++f) {
+                                const int ch = 4 * (j & 1) + 2 * f + c8;  // 16-byte column within the half's rows
+                                const uint32_t at = unit + (j >> 1) * kHalfBytes + row * 128 + ((ch ^ (row & 7)) << 4);
+                                if (kv) stmatrix_x4_trans(at, a[f]);
+                                else stmatrix_x4(at, a[f]);
+                            }
+                            off += tag_granules(tag) * kGranule;
+                        }
+                    } else if (kv || pi.kind == kPageRaw) {
+                        // a raw tail as it is; rows of V without a token are zero, so that weight 0
+                        // times them is 0 (scores of K rows without one are not used)
+                        const uint32_t have = pi.kind == kPageRaw ? pi.valid : 0;
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {
+                            const int tok = 2 * i + (lane >> 4), ch = lane & 15, row = 16 * st + tok;
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            if ((uint32_t)tok < have)
+                                x = *reinterpret_cast<const uint4 *>(src + kv * (kPageBytes / 2) + tok * 256 + ch * 16);
+                            *reinterpret_cast<uint4 *>(smem + S::ring + slot * kUnitBytes + (ch >> 3) * kHalfBytes +
+                                                       row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = x;
+                        }
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(sbase + S::full + 8 * slot);
+                        if (kv) mbar_arrive(sbase + S::sempty + 8 * st);
+                    }
+                }
+            }
         }
     } else if (warp == 9) {
         // ============================ matrix products ============================
@@ -350,7 +555,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
         }
         __syncwarp();
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::softmax_regs));
         // ================================ softmax ================================
         // Thread = query row.  Its 128 scores of a block come from tensor memory at once;
         // the weights go back over them, 64 tokens at a time, as two BF16 parts, p = high + low (16
@@ -460,7 +665,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1) k_prefix(const PrefixParams P,
 #pragma unroll
                     for (int w = 0; w < 4; ++w) tmem_ld32(tS + 32 * w, v[w]);
                 }
-                if (!whole) {
+                if (!kCoded && !whole) {
                     // rows of V that hold no token: zero, so that weight 0 times them is 0
                     const int it = 2 * n + 1;
                     wait(sbase + S::full + 8 * (it % kUnits), (it / kUnits) & 1);
@@ -730,20 +935,20 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
 // ---------------------------------------------------------------------------------
 // launcher
 // ---------------------------------------------------------------------------------
-template <int kTiles>
+template <int kFmt, int kTiles>
 static cudaError_t launch_prefix_impl(const PrefixParams &P, const CUtensorMap &map, cudaStream_t stream)
 {
-    const int bytes = PfxSmem<kTiles>::bytes(P.num_groups);
+    const int bytes = PfxSmem<kFmt, kTiles>::bytes(P.num_groups);
     // per process and device: the whole shared memory (an attribute of the function)
     static unsigned long long done = 0;  // bit per device ordinal < 64
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(dev < 64 && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1ull)) {
-        e = cudaFuncSetAttribute(k_prefix<kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        e = cudaFuncSetAttribute(k_prefix<kFmt, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e == cudaSuccess && dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_ACQ_REL);
     }
     if (e != cudaSuccess) return e;
-    k_prefix<kTiles><<<P.grid, kPfxThreads, bytes, stream>>>(P, map);
+    k_prefix<kFmt, kTiles><<<P.grid, PfxSmem<kFmt, kTiles>::threads, bytes, stream>>>(P, map);
     return cudaGetLastError();
 }
 
@@ -753,7 +958,11 @@ cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_
     if (P.num_groups > 0 && P.grid > 0) {
         CUtensorMap map;
         memcpy(&map, prefix_map, sizeof map);
-        cudaError_t e = P.unit_rows == 256 ? launch_prefix_impl<2>(P, map, stream) : launch_prefix_impl<1>(P, map, stream);
+        cudaError_t e;
+        if (format == kFmtRaw)
+            e = P.unit_rows == 256 ? launch_prefix_impl<kFmtRaw, 2>(P, map, stream) : launch_prefix_impl<kFmtRaw, 1>(P, map, stream);
+        else
+            e = P.unit_rows == 256 ? launch_prefix_impl<kFmtZf, 2>(P, map, stream) : launch_prefix_impl<kFmtZf, 1>(P, map, stream);
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_attention_partials(A, format, own_map, stream);

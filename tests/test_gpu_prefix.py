@@ -13,6 +13,7 @@ BOTH = ["raw", "coded"]
 def run(case, kind, **kw):
     out = case.run_raw(**kw) if kind == "raw" else case.run_coded(**kw)
     torch.cuda.synchronize()
+    assert not int(case.status.item()) & case.kvz.STATUS_TIMEOUT
     return out
 
 
@@ -34,6 +35,20 @@ def test_prefix_lengths(kind, prefix):
 def test_head_layouts(kind, G, hkv, n):
     c = PrefixCase([(n, 700)], own_lens(n, 70, G), G * hkv, hkv, seed=G)
     c.check(run(c, kind, dtype=torch.bfloat16))
+    assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("kind", BOTH)
+@pytest.mark.parametrize("n,G", [(16, 4), (50, 4)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_blocks_a_cta(kind, n, G, dtype):
+    """Long prefixes over many KV heads: every ring of the kernel wraps several times."""
+    c = PrefixCase([(n, 40003), (2, 9000)], own_lens(n + 2, 20), 8 * G, 8, seed=n)
+    ref = c.reference()
+    c.check(run(c, kind, dtype=dtype), ref)
+    first = run(c, kind, dtype=dtype)
+    for _ in range(4):
+        assert torch.equal(first, run(c, kind, dtype=dtype))
     assert int(c.status.item()) == 0
 
 

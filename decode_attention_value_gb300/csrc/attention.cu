@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
                         pending = false;
                         // overlapped launch: the kernel before this one may still be writing the
                         // sequence's last page; everything else was complete before it started
-                        if (P.overlap && d_last) pdl_wait_primary();
+                        if (P.overlap == 1 && d_last) pdl_wait_primary();
                         info[s] = StageInfo{d_kind, d_valid, d_tK, d_tV};
                         const uint32_t dst = sbase + Smem::stage + s * kStageBytes;
                         if (d_kind == kKindPair) {
@@ -443,6 +443,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
                 mbar_wait(sbase + Smem::full + 8 * s, (uint32_t)(last & 1), P.status);
             }
         }
+        // beside a kernel that shares nothing with this one: complete after it, for the kernel
+        // that waits for this one and reads the results of both
+        if (P.overlap == 2) pdl_wait_primary();
         return;
     }
 
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
     bool ok = true;
     // overlapped launch: q, the workspace and the outputs belong to the kernel before this
     // one until it has finished
-    if (P.overlap) pdl_wait_primary();
+    if (P.overlap == 1) pdl_wait_primary();
     int64_t x = lo, ibase = 0;
     while (x < hi) {
         const PageLoc L = locate(pref, B, hkv, x);

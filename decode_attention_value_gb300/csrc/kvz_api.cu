@@ -33,12 +33,31 @@ int sm_count()
     return n;
 }
 
+// attn_ctas_per_sm, asked once per device and batch size (ten occupancy queries, 2.5 us)
+cudaError_t ctas_per_sm(int batch, int *out)
+{
+    static std::mutex mu;
+    static int8_t known[8][kMaxBatch + 1];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < 8 && batch >= 0 && batch <= kMaxBatch;
+    std::lock_guard<std::mutex> lock(mu);
+    if (keep && known[dev][batch] > 0) {
+        *out = known[dev][batch];
+        return cudaSuccess;
+    }
+    e = attn_ctas_per_sm(batch, out);
+    if (e == cudaSuccess && keep && *out > 0 && *out < 128) known[dev][batch] = (int8_t)*out;
+    return e;
+}
+
 // Number of attention CTAs: one wave of the CTAs the device holds, but at least
 // kMinPagesPerCta pages each.  Depends only on shapes and the device.
 int attention_grid(int batch, int hkv, int table_pages, int *grid)
 {
     int per_sm = 0;
-    cudaError_t e = attn_ctas_per_sm(batch, &per_sm);
+    cudaError_t e = ctas_per_sm(batch, &per_sm);
     if (e != cudaSuccess) return fail_cuda(e);
     if (per_sm < 1) return KVZ_ERR_UNSUPPORTED;
     const int sms = sm_count();
@@ -242,10 +261,10 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     if (!rc) rc = prefix_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &pmap);
     if (rc) return rc;
     AttnParams A;
-    // the own pages' kernel follows the prefix kernel as its programmatic dependent
+    // the own pages' kernel runs beside the prefix kernel as its programmatic dependent
     attention_params(&A, F, d, batch, hq, grid, q, page_ids, max_pages, seq_lens, tail_page, num_meta_pages, arena,
-                     arena_bytes, num_raw_pages, nullptr, static_cast<uint8_t *>(ws) + prefix_bytes, status,
-                     pgrid > 0 ? KVZ_ATTN_OVERLAP_PREVIOUS : 0u);
+                     arena_bytes, num_raw_pages, nullptr, static_cast<uint8_t *>(ws) + prefix_bytes, status, 0u);
+    A.overlap = pgrid > 0 ? 2 : 0;
     PrefixParams P;
     memset(&P, 0, sizeof P);
     P.batch = batch;

@@ -93,7 +93,9 @@ struct AttnParams {
     float *part_ml;    // [slots][4 or 8][2]
     uint32_t *status;
     float scale_log2;  // log2(e) / sqrt(128)
-    int overlap;       // 1: launched as programmatic dependents (KVZ_ATTN_OVERLAP_PREVIOUS)
+    // 1: launched as programmatic dependents (KVZ_ATTN_OVERLAP_PREVIOUS); 2: the same, after a
+    // kernel that writes nothing this one reads or writes (the prefix kernel)
+    int overlap;
 };
 
 inline size_t attn_slots(int batch, int hkv, int grid) { return (size_t)batch * hkv + grid - 1; }

@@ -24,10 +24,7 @@ constexpr uint32_t kHalfBytes = kUnitBytes / 2;        // its 64-column halves
 constexpr uint32_t kQTileBytes = 128 * kDim * 2;       // 128 query rows, BF16
 constexpr uint32_t kQHalfBytes = kQTileBytes / 2;
 constexpr int kExpWarps = 4;   // 12-bit pages: warps that restore BF16 operands (warps 10 to 13)
-constexpr int kPageStages = 8;  // 12-bit pages: ring of coded pages, one block
 constexpr uint32_t kPageBytes = 2 * kPage * kDim * 2;  // most bytes of a coded (or raw) K and V page
-static_assert(kPageStages == kPfxPages, "a page's stage is its place in its block");
-static_assert(kPageStages % kExpWarps == 0, "a stage's pages all go to one warp, which sees each of its phases");
 constexpr int kInfoRing = 8;
 // tensor memory, 256 columns a stream: 128 of scores, overwritten by the weights of the first and
 // of the second 64 tokens (32 columns of high, 32 of low parts each), and 128 of output
@@ -47,13 +44,20 @@ struct PfxSmem {
     static constexpr bool coded = kFmt != kFmtRaw;
     static constexpr int threads = coded ? 512 : 384;
     static constexpr int softmax_regs = coded ? 200 : 208, other_regs = coded ? 56 : 80;
-    // ring of K and V blocks
-    static constexpr int units = coded ? (kTiles == 2 ? 3 : 4) : (kTiles == 2 ? 5 : 6);
+    // rings of K blocks and of V blocks: K's are given back as soon as the scores are made, V's
+    // when the weights have been used
+    static constexpr int ku = coded ? 1 : (kTiles == 2 ? 2 : 3), vu = coded ? 2 : 3, units = ku + vu;
+    // ring of coded pages; a stage's pages all go to one of the restoring warps, which sees each
+    // of its phases
+    static constexpr int stages = coded ? (kTiles == 2 ? 8 : 12) : 0;
+    static_assert(stages % kExpWarps == 0, "a page's warp follows from its stage");
+    __host__ __device__ static constexpr int slot(int n, int kv) { return kv ? ku + n % vu : n % ku; }
+    __host__ __device__ static constexpr uint32_t phase(int n, int kv) { return (kv ? n / vu : n / ku) & 1; }
     static constexpr int arrivals = coded ? kPfxPages : 1;  // that fill a block
     static constexpr int q = 0;
     static constexpr int ring = q + kTiles * (int)kQTileBytes;
     static constexpr int stage = ring + units * (int)kUnitBytes;
-    static constexpr int full = stage + (coded ? kPageStages * (int)kPageBytes : 0);
+    static constexpr int full = stage + stages * (int)kPageBytes;
     static constexpr int empty = full + units * 8;
     static constexpr int qfull = empty + units * 8;
     static constexpr int sfull = qfull + 8;    // [2] scores of a stream are in tensor memory
@@ -61,9 +65,9 @@ struct PfxSmem {
     static constexpr int ofull = pready + 32;  // [2] its output of the segment is complete
     static constexpr int drain = ofull + 16;
     static constexpr int sempty = drain + 8;                               // page stages
-    static constexpr int sarrived = sempty + (coded ? kPageStages * 8 : 0);
-    static constexpr int sinfo = (sarrived + (coded ? kPageStages * 8 : 0) + 15) & ~15;
-    static constexpr int info = sinfo + (coded ? kPageStages * 16 : 0);  // [kInfoRing] bad pages of a block
+    static constexpr int sarrived = sempty + stages * 8;
+    static constexpr int sinfo = (sarrived + stages * 8 + 15) & ~15;
+    static constexpr int info = sinfo + stages * 16;  // [kInfoRing] bad pages of a block
     static constexpr int misc = info + kInfoRing * 4;  // tensor memory address, abort flag
     static constexpr int plan = misc + 16;  // [groups + 1] {first unit, first block}
     static int bytes(int groups) { return plan + (groups + 1) * 8; }
@@ -173,7 +177,6 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
 {
     using S = PfxSmem<kFmt, kTiles>;
     constexpr bool kCoded = S::coded;
-    constexpr int kUnits = S::units;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
     if (sbase & 1023u) {  // swizzled operands need 1024-byte alignment
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + S::misc);
 
     if (tid == 0) {
-        for (int s = 0; s < kUnits; ++s) {
+        for (int s = 0; s < S::units; ++s) {
             mbar_init(sbase + S::full + 8 * s, S::arrivals);
             mbar_init(sbase + S::empty + 8 * s, 1);
         }
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         }
         mbar_init(sbase + S::drain, 1);
         if (kCoded)
-            for (int s = 0; s < kPageStages; ++s) {
+            for (int s = 0; s < S::stages; ++s) {
                 mbar_init(sbase + S::sempty + 8 * s, 1);
                 mbar_init(sbase + S::sarrived + 8 * s, 1);
             }
@@ -281,9 +284,9 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 const int row = __shfl_sync(0xffffffffu, cur, kPfxPages * i + ((lane >> 1) & 7));
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int it = 2 * n + kv, slot = it % kUnits;
+                    const int slot = S::slot(n, kv);
                     const uint32_t fullbar = sbase + S::full + 8 * slot;
-                    ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, ((it / kUnits) & 1) ^ 1));
+                    ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, kv) ^ 1));
                     if (!ok) break;
                     if (lane == 0) {
                         if (kv == 0) info[n % kInfoRing] = (bad >> (kPfxPages * i)) & 0xFFu;
@@ -378,10 +381,11 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 const int n = base / kPfxPages + i;
                 if (n >= hi - lo) break;
                 if (lane / kPfxPages == i) {
-                    const int st = lane % kPfxPages;
-                    if (wait(sbase + S::sempty + 8 * st, (n & 1) ^ 1)) {
+                    constexpr int kStages = kCoded ? S::stages : 1;
+                    const int st = (base + lane) % kStages;
+                    if (wait(sbase + S::sempty + 8 * st, (((base + lane) / kStages) & 1) ^ 1)) {
                         const uint32_t bar = sbase + S::sarrived + 8 * st, dst = sbase + S::stage + st * kPageBytes;
-                        if (st == 0) info[n % kInfoRing] = (bad >> (kPfxPages * i)) & 0xFFu;
+                        if (lane % kPfxPages == 0) info[n % kInfoRing] = (bad >> (kPfxPages * i)) & 0xFFu;
                         *reinterpret_cast<PageInfo *>(smem + S::sinfo + 16 * st) = PageInfo{kind, (uint32_t)valid, tk, tv};
                         if (kind == kPageCoded) {
                             mbar_arrive_expect_tx(bar, bk + bv);
@@ -418,19 +422,20 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         for (int n = 0; n < hi - lo && ok; ++n) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-                const int it = 2 * n + kv, slot = it % kUnits;
-                if (ok) ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, ((it / kUnits) & 1) ^ 1));
+                const int slot = S::slot(n, kv);
+                if (ok) ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, kv) ^ 1));
                 const uint32_t unit = sbase + S::ring + slot * kUnitBytes;
 #pragma unroll 1
                 for (int q = 0; q < kMine && ok; ++q) {
-                    const int st = warp - 10 + q * kExpWarps;
+                    constexpr int kStages = kCoded ? S::stages : 1;
+                    const int page = warp - 10 + q * kExpWarps, y = n * kPfxPages + page, st = y % kStages;
                     const uint8_t *src = smem + S::stage + st * kPageBytes;
-                    if (kv == 0) ok = __all_sync(0xffffffffu, wait(sbase + S::sarrived + 8 * st, n & 1));
+                    if (kv == 0) ok = __all_sync(0xffffffffu, wait(sbase + S::sarrived + 8 * st, (y / kStages) & 1));
                     if (!ok) break;
                     const PageInfo pi = *reinterpret_cast<const PageInfo *>(smem + S::sinfo + 16 * st);
                     if (pi.kind == kPageCoded) {
                         const uint32_t tags = kv ? pi.tagsV : pi.tagsK;
-                        const int row = 16 * st + rr + 8 * (kv ? mi >> 1 : mi & 1), c8 = kv ? mi & 1 : mi >> 1;
+                        const int row = 16 * page + rr + 8 * (kv ? mi >> 1 : mi & 1), c8 = kv ? mi & 1 : mi >> 1;
                         uint32_t off = kv ? group_granules(pi.tagsK) * kGranule : 0;  // V right after K
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                         const uint32_t have = pi.kind == kPageRaw ? pi.valid : 0;
 #pragma unroll 1
                         for (int i = 0; i < 8; ++i) {
-                            const int tok = 2 * i + (lane >> 4), ch = lane & 15, row = 16 * st + tok;
+                            const int tok = 2 * i + (lane >> 4), ch = lane & 15, row = 16 * page + tok;
                             uint4 x = make_uint4(0, 0, 0, 0);
                             if ((uint32_t)tok < have)
                                 x = *reinterpret_cast<const uint4 *>(src + kv * (kPageBytes / 2) + tok * 256 + ch * 16);
@@ -482,13 +487,13 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
             if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity));
             tc_fence_after();
         };
-        auto unit_addr = [&](int it) { return uniform(sbase + S::ring + (it % kUnits) * kUnitBytes); };
-        auto wait_unit = [&](int it) { wait_all(sbase + S::full + 8 * (it % kUnits), (it / kUnits) & 1); };
+        auto unit_addr = [&](int n, int kv) { return uniform(sbase + S::ring + S::slot(n, kv) * kUnitBytes); };
+        auto wait_unit = [&](int n, int kv) { wait_all(sbase + S::full + 8 * S::slot(n, kv), S::phase(n, kv)); };
         // scores of stream s over K block n; give_back: the last product that reads the block
         auto qk = [&](int s, int n, bool give_back) {
             const uint64_t a = smem_desc(sbase + S::q + (kTiles == 2 ? s * kQTileBytes : 0), 16, 1024);
-            const uint64_t b = smem_desc(unit_addr(2 * n), 16, 1024);
-            const uint32_t freebar = uniform(sbase + S::empty + 8 * (2 * n % kUnits));
+            const uint64_t b = smem_desc(unit_addr(n, 0), 16, 1024);
+            const uint32_t freebar = uniform(sbase + S::empty + 8 * S::slot(n, 0));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // 16 of the 128 dims: 32 bytes within a half's rows
@@ -501,8 +506,8 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         };
         // output of stream s: its weights (high and low parts) of 64 tokens times half of V block n
         auto pv = [&](int s, int n, int half, bool add, bool last, bool give_back) {
-            const uint64_t b = smem_desc(unit_addr(2 * n + 1) + half * 8192, kHalfBytes, 1024);
-            const uint32_t freebar = uniform(sbase + S::empty + 8 * ((2 * n + 1) % kUnits));
+            const uint64_t b = smem_desc(unit_addr(n, 1) + half * 8192, kHalfBytes, 1024);
+            const uint32_t freebar = uniform(sbase + S::empty + 8 * S::slot(n, 1));
             if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
             for (int s = 0; s < 2; ++s) {
                 const int j = kTiles == 2 ? 0 : s;
                 if (j >= nb || !ok) break;
-                if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j));
+                if (kTiles == 1 || s == 0) wait_unit(n0 + j, 0);
                 if (ok) qk(s, n0 + j, kTiles == 1 || s == 1);
             }
             for (int i = 0; i < (kTiles == 2 ? nb : (nb + 1) / 2) && ok; ++i) {
@@ -534,11 +539,11 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 for (int s = 0; s < 2; ++s) {  // the streams in turn
                     const int j = kTiles == 2 ? i : 2 * i + s;
                     if (j >= nb || !ok) break;
-                    if (kTiles == 1 || s == 0) wait_unit(2 * (n0 + j) + 1);
+                    if (kTiles == 1 || s == 0) wait_unit(n0 + j, 1);
                     wait_all(sbase + S::pready + 16 * s, pphase >> s & 1);
                     if (!ok) break;
                     pv(s, n0 + j, 0, i % P.fold != 0, false, false);
-                    if (j + step < nb && (kTiles == 1 || s == 0)) wait_unit(2 * (n0 + j + step));
+                    if (j + step < nb && (kTiles == 1 || s == 0)) wait_unit(n0 + j + step, 0);
                     wait_all(sbase + S::pready + 16 * s + 8, pphase >> s & 1);
                     if (!ok) break;
                     pphase ^= 1u << s;
@@ -667,10 +672,10 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 }
                 if (!kCoded && !whole) {
                     // rows of V that hold no token: zero, so that weight 0 times them is 0
-                    const int it = 2 * n + 1;
-                    wait(sbase + S::full + 8 * (it % kUnits), (it / kUnits) & 1);
+                    const int slot = S::slot(n, 1);
+                    wait(sbase + S::full + 8 * slot, S::phase(n, 1));
                     if (r >= left || (bad >> (r >> 4) & 1)) {
-                        uint8_t *at = smem + S::ring + (it % kUnits) * kUnitBytes + r * 128;
+                        uint8_t *at = smem + S::ring + slot * kUnitBytes + r * 128;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             *reinterpret_cast<uint4 *>(at + 16 * i) = make_uint4(0, 0, 0, 0);
@@ -784,32 +789,32 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
 }
 
 // ---------------------------------------------------------------------------------
-// merge: one block per (sequence, query head).  The partials of its row, prefix CTAs in order
-// and then own-page CTAs in order, are weighted by 2^(m - max) and added: each warp every
-// fourth one, then the four warps in order.
+// merge: one block per (sequence, KV head), one to eight of its eight warps per query head.  The
+// partials of a head's row, the prefix's CTAs in order and then the own pages' CTAs in order, are
+// dealt to the head's warps in turn; a warp takes 32 at a time (a lane each for the maxima and
+// sums, all lanes for the outputs) into a running maximum, sum and output, and the warps of a head
+// are added in order.
 // ---------------------------------------------------------------------------------
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 
 __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixParams P, const AttnParams A)
 {
-    extern __shared__ float2 ml[];  // [items]: (m, l), then weight in .x
-    __shared__ int red[4][6];
-    __shared__ float fred[4][2];
-    __shared__ float4 acc[4][32];
-    const int b = blockIdx.x / (P.hkv * P.G), h = blockIdx.x % (P.hkv * P.G), kvh = h / P.G, tid = threadIdx.x;
+    __shared__ int red[kMergeWarps][8];
+    __shared__ float2 wml[kMergeWarps];
+    __shared__ float4 acc[kMergeWarps][32];
+    const int b = blockIdx.x / P.hkv, kvh = blockIdx.x % P.hkv, tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
     // ---- before the wait: what the lengths say (they were complete before the call) ----
     // own pages of the sequences before b, of b, of all; prefix units and blocks before b's
-    // group and in all; b's group
-    int v[6] = {0, 0, 0, 0, 0, 0}, mine = -1;
+    // group and blocks in all; b's group
+    int v[7] = {0, 0, 0, 0, 0, 0, -1};
     for (int i = tid; i < P.batch; i += kMergeThreads) {
         const int L = A.seq_lens[i], pages = L > 0 ? (L + kPage - 1) / kPage : 0;
         v[0] += i < b ? pages : 0;
         v[1] += i == b ? pages : 0;
         v[2] += pages;
     }
-    const bool ok = P.num_groups > 0 && pfx_groups_ok(P, lane);
-    if (ok)
+    if (P.num_groups > 0 && pfx_groups_ok(P, lane))
         for (int g = tid; g < P.num_groups; g += kMergeThreads) {
             const PfxGroup r = pfx_group(P, g);
             const int n = P.hkv * r.tiles;
@@ -817,35 +822,40 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
                 v[3] += n;
                 v[4] += n * r.blocks;
             } else if (r.seq0 <= b) {
-                mine = g;
+                v[6] = g;
             }
             v[5] += n * r.blocks;
         }
-    mine = __reduce_max_sync(0xffffffffu, mine);
 #pragma unroll
     for (int i = 0; i < 6; ++i) v[i] = __reduce_add_sync(0xffffffffu, v[i]);
-    __shared__ int gred[4];
+    v[6] = __reduce_max_sync(0xffffffffu, v[6]);
     if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < 6; ++i) red[warp][i] = v[i];
-        gred[warp] = mine;
+        for (int i = 0; i < 7; ++i) red[warp][i] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 6; ++i) v[i] = red[0][i] + red[1][i] + red[2][i] + red[3][i];
-    mine = max(max(gred[0], gred[1]), max(gred[2], gred[3]));
+    for (int i = 0; i < 7; ++i) v[i] = red[0][i];
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) v[i] += red[w][i];
+        v[6] = max(v[6], red[w][6]);
+    }
+    const int share = P.G > 4 ? 1 : P.G > 2 ? 2 : P.G > 1 ? 4 : 8;  // warps of a head
+    const int hg = warp / share, part = warp % share;
     // prefix items: CTAs c0 .. c1 of the row's unit, one or two streams each
-    int np = 0, c0 = 0, streams = 1, prow = 0, unit = 0;
-    if (mine >= 0) {
-        const PfxGroup r = pfx_group(P, mine);
+    int np = 0, c0 = 0, row = 0, unit = 0;
+    const int streams = P.unit_rows == 128 ? 2 : 1;
+    if (v[6] >= 0 && hg < P.G) {
+        const PfxGroup r = pfx_group(P, v[6]);
         if (r.blocks > 0) {
-            const int row = (b - r.seq0) * P.G + h % P.G, tile = row / P.unit_rows;
-            prow = row - tile * P.unit_rows;
+            const int all = (b - r.seq0) * P.G + hg, tile = all / P.unit_rows;
+            row = all - tile * P.unit_rows;
             const int ui = kvh * r.tiles + tile, W = v[5], C = min(P.grid, W);
             const int first = v[4] + ui * r.blocks, last = first + r.blocks - 1;
             unit = v[3] + ui;
             c0 = (int)((int64_t)first * C / W);
-            streams = P.unit_rows == 128 ? 2 : 1;
             np = ((int)((int64_t)last * C / W) - c0 + 1) * streams;
         }
     }
@@ -857,79 +867,90 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
         a0 = (int)(first * AC / T);
         ns = (int)((first + v[1] - 1) * AC / T) - a0 + 1;
     }
-    const int heads = P.G > 4 ? 8 : 4;  // heads of a slot of the split kernel
-    auto row_of = [&](int i, const float *&o, const float *&m) {  // partial i of the row
+    const int items = hg < P.G ? np + ns : 0, heads = P.G > 4 ? 8 : 4;  // heads: of a slot of the split kernel
+    // partial i of the row
+    auto row_of = [&](int i) -> int64_t {
         if (i < np) {
-            const int s = P.unit_rows == 128 ? i & 1 : prow >> 7, cc = c0 + i / streams;
-            const int64_t row = ((int64_t)(unit + cc) * 2 + s) * 128 + (prow & 127);
-            o = P.part_o + row * kDim;
-            m = P.part_ml + row * 2;
-        } else {
-            const int64_t row = ((int64_t)(b * P.hkv + kvh) + a0 + (i - np)) * heads + h % P.G;
-            o = A.part_o + row * kDim;
-            m = A.part_ml + row * 2;
+            const int s = streams == 2 ? i & 1 : row >> 7, cc = c0 + i / streams;
+            return ((int64_t)(unit + cc) * 2 + s) * 128 + (row & 127);
         }
+        return ((int64_t)(b * P.hkv + kvh) + a0 + (i - np)) * heads + hg;
     };
     pdl_wait_primary();  // both kernels' partials are complete
-    const int items = np + ns;
-    float M = -INFINITY;
-    for (int i = tid; i < items; i += kMergeThreads) {
+    float M = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = part; i0 < items; i0 += 32 * share) {
+        const int mine = i0 + lane * share;
         float2 e = make_float2(-INFINITY, 0.f);
-        const int64_t cc = a0 + (i - np);
-        // (a CTA of the split kernel without pages wrote nothing)
-        if (i < np || T >= AC || (cc * T + AC - 1) / AC < ((cc + 1) * T + AC - 1) / AC) {
-            const float *o, *m;
-            row_of(i, o, m);
-            e = *reinterpret_cast<const float2 *>(m);
+        if (mine < items) {
+            const int64_t cc = a0 + (mine - np);
+            // (a CTA of the split kernel without pages wrote nothing)
+            if (mine < np || T >= AC || (cc * T + AC - 1) / AC < ((cc + 1) * T + AC - 1) / AC)
+                e = *reinterpret_cast<const float2 *>((mine < np ? P.part_ml : A.part_ml) + row_of(mine) * 2);
         }
-        ml[i] = e;
-        M = fmaxf(M, e.x);
-    }
+        float top = e.x;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    if (lane == 0) fred[warp][0] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(fred[0][0], fred[1][0]), fmaxf(fred[2][0], fred[3][0]));
-    float L = 0.f;
-    for (int i = tid; i < items; i += kMergeThreads) {
-        const float2 e = ml[i];
-        const float w = e.x == -INFINITY ? 0.f : exp2f(e.x - M);
-        L += e.x == -INFINITY ? 0.f : w * e.y;
-        ml[i].x = e.x == -INFINITY ? -1.f : w;  // -1: a partial without tokens has no output
-    }
+        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = fmaxf(top, M);
+        const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+        const bool none = e.x == -INFINITY;  // a partial without tokens has no output
+        const float w = none ? 0.f : exp2f(e.x - top);
+        float sum = none ? 0.f : w * e.y;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    if (lane == 0) fred[warp][1] = L;
-    __syncthreads();
-    L = (fred[0][1] + fred[1][1]) + (fred[2][1] + fred[3][1]);
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = warp; i < items; i += 4) {
-        const float w = ml[i].x;
-        if (!(w < 0.f)) {
-            const float *o, *m;
-            row_of(i, o, m);
-            const float4 x = *reinterpret_cast<const float4 *>(o + 4 * lane);
-            sum.x += w * x.x;
-            sum.y += w * x.y;
-            sum.z += w * x.z;
-            sum.w += w * x.w;
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const uint32_t have = __ballot_sync(0xffffffffu, !none);
+        L = L * f + sum;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        M = top;
+        const int n = min(32, (items - i0 + share - 1) / share);
+        for (int k0 = 0; k0 < n; k0 += 8) {  // eight loads in flight
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + (k0 + k) * share;
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (have >> (k0 + k) & 1)
+                    x[k] = reinterpret_cast<const float4 *>((i < np ? P.part_o : A.part_o) + row_of(i) * kDim)[lane];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+                o.x += wk * x[k].x;
+                o.y += wk * x[k].y;
+                o.z += wk * x[k].z;
+                o.w += wk * x[k].w;
+            }
         }
     }
-    acc[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0) {
-        const float4 x0 = acc[0][lane], x1 = acc[1][lane], x2 = acc[2][lane], x3 = acc[3][lane];
-        const float k = L == 0.f ? 0.f : 1.f / L;  // no token: zero
-        float4 y = make_float4(((x0.x + x1.x) + (x2.x + x3.x)) * k, ((x0.y + x1.y) + (x2.y + x3.y)) * k,
-                               ((x0.z + x1.z) + (x2.z + x3.z)) * k, ((x0.w + x1.w) + (x2.w + x3.w)) * k);
-        const int64_t at = (int64_t)blockIdx.x * kDim + 4 * lane;
-        if (P.out_bf16)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) =
-                make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-        else
-            *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + at) = y;
+    if (share > 1) {
+        acc[warp][lane] = o;
+        if (lane == 0) wml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (part > 0) return;
+        for (int k = 1; k < share; ++k) M = fmaxf(M, wml[warp + k].x);
+        const float f0 = wml[warp].x == -INFINITY ? 0.f : exp2f(wml[warp].x - M);
+        L *= f0;
+        o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+        for (int k = 1; k < share; ++k) {
+            const float2 e = wml[warp + k];
+            const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - M);
+            const float4 x = acc[warp + k][lane];
+            L += f * e.y;
+            o.x += f * x.x;
+            o.y += f * x.y;
+            o.z += f * x.z;
+            o.w += f * x.w;
+        }
     }
+    if (hg >= P.G) return;
+    const float k = L == 0.f ? 0.f : 1.f / L;  // no token: zero
+    const float4 y = make_float4(o.x * k, o.y * k, o.z * k, o.w * k);
+    const int64_t at = ((int64_t)blockIdx.x * P.G + hg) * kDim + 4 * lane;
+    if (P.out_bf16)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) =
+            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + at) = y;
 }
 
 // ---------------------------------------------------------------------------------
@@ -971,10 +992,8 @@ cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(P.batch * P.hkv * P.G);
+    cfg.gridDim = dim3(P.batch * P.hkv);
     cfg.blockDim = dim3(kMergeThreads);
-    // most partials of a row: every CTA of both kernels, two streams each of the prefix's
-    cfg.dynamicSmemBytes = (size_t)(2 * P.grid + A.grid) * sizeof(float2);
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;

@@ -23,8 +23,8 @@ constexpr uint32_t kUnitBytes = kPfxBlock * kDim * 2;  // K or V of a block, BF1
 constexpr uint32_t kHalfBytes = kUnitBytes / 2;        // its 64-column halves
 constexpr uint32_t kQTileBytes = 128 * kDim * 2;       // 128 query rows, BF16
 constexpr uint32_t kQHalfBytes = kQTileBytes / 2;
-constexpr int kExpWarps = 4;   // 12-bit pages: warps that restore BF16 operands (warps 10 to 13)
-constexpr uint32_t kPageBytes = 2 * kPage * kDim * 2;  // most bytes of a coded (or raw) K and V page
+constexpr int kExpWarps = 3;  // 12-bit pages: warps that restore K (warps 10 to 12) and V (13 to 15)
+constexpr uint32_t kGroupBytes = kPage * kDim * 2;  // most bytes of a coded (or raw) K or V group
 constexpr int kInfoRing = 8;
 // tensor memory, 256 columns a stream: 128 of scores, overwritten by the weights of the first and
 // of the second 64 tokens (32 columns of high, 32 of low parts each), and 128 of output
@@ -34,8 +34,10 @@ constexpr uint32_t kColO = 256;
 // [128 s, 128 s + 128) and both see every block.  kTiles = 1: 128 rows, the streams take
 // alternate blocks and leave separate partials.
 //
-// Raw pages are copied by TMA into the operands' layout; 12-bit pages are copied as they are into
-// a ring of page stages, and four warps restore them into the operands' blocks.  The softmax
+// Raw pages are copied by TMA into the operands' layout.  12-bit pages are copied as they are, a
+// block's eight K groups and eight V groups into stages of their own, and restored by six warps,
+// three for K and three for V: K of the next blocks is read and restored while V waits for room.
+// The softmax
 // threads take most registers, so that a thread's scores and weights stay in them: 168 a thread at
 // launch (64512) become 256 x 208 + 128 x 80 = 63488 for raw pages; 128 (65536) become
 // 256 x 200 + 256 x 56 = 65536 for 12-bit pages.
@@ -46,29 +48,26 @@ struct PfxSmem {
     static constexpr int softmax_regs = coded ? 200 : 208, other_regs = coded ? 56 : 80;
     // rings of K blocks and of V blocks: K's are given back as soon as the scores are made, V's
     // when the weights have been used
-    static constexpr int ku = coded ? 1 : (kTiles == 2 ? 2 : 3), vu = coded ? 2 : 3, units = ku + vu;
-    // ring of coded pages; a stage's pages all go to one of the restoring warps, which sees each
-    // of its phases
-    static constexpr int stages = coded ? (kTiles == 2 ? 8 : 12) : 0;
-    static_assert(stages % kExpWarps == 0, "a page's warp follows from its stage");
+    static constexpr int ku = kTiles == 2 ? (coded ? 1 : 2) : (coded ? 2 : 3), vu = coded ? 2 : 3, units = ku + vu;
+    static constexpr int stages = coded ? 2 * kPfxPages : 0;  // coded groups of a block
     __host__ __device__ static constexpr int slot(int n, int kv) { return kv ? ku + n % vu : n % ku; }
     __host__ __device__ static constexpr uint32_t phase(int n, int kv) { return (kv ? n / vu : n / ku) & 1; }
-    static constexpr int arrivals = coded ? kPfxPages : 1;  // that fill a block
+    static constexpr int arrivals = coded ? kExpWarps : 1;  // that fill a block
     static constexpr int q = 0;
     static constexpr int ring = q + kTiles * (int)kQTileBytes;
     static constexpr int stage = ring + units * (int)kUnitBytes;
-    static constexpr int full = stage + stages * (int)kPageBytes;
+    static constexpr int full = stage + stages * (int)kGroupBytes;
     static constexpr int empty = full + units * 8;
     static constexpr int qfull = empty + units * 8;
     static constexpr int sfull = qfull + 8;    // [2] scores of a stream are in tensor memory
     static constexpr int pready = sfull + 16;  // [2][2] its weights of half a block are
     static constexpr int ofull = pready + 32;  // [2] its output of the segment is complete
     static constexpr int drain = ofull + 16;
-    static constexpr int sempty = drain + 8;                               // page stages
-    static constexpr int sarrived = sempty + stages * 8;
-    static constexpr int sinfo = (sarrived + stages * 8 + 15) & ~15;
-    static constexpr int info = sinfo + stages * 16;  // [kInfoRing] bad pages of a block
-    static constexpr int misc = info + kInfoRing * 4;  // tensor memory address, abort flag
+    static constexpr int sarrived = drain + 8;  // [stages] coded groups
+    static constexpr int sempty = sarrived + stages * 8;
+    static constexpr int sinfo = sempty + stages * 8;
+    static constexpr int info = sinfo + stages * 8;   // [kInfoRing][8] bad pages of a block
+    static constexpr int misc = info + kInfoRing * 8;  // tensor memory address, abort flag
     static constexpr int plan = misc + 16;  // [groups + 1] {first unit, first block}
     static int bytes(int groups) { return plan + (groups + 1) * 8; }
 };
@@ -149,27 +148,65 @@ struct PfxWait {
     }
 };
 
-// A page in its stage.
-struct __align__(16) PageInfo {
-    uint32_t kind, valid, tagsK, tagsV;  // valid: tokens of a raw page
-};
-enum : uint32_t { kPageNone = 0, kPageCoded = 1, kPageRaw = 2 };
+// A K or V group in its stage: {kind | valid tokens of a raw one << 8, tags}.
+enum : uint32_t { kGroupNone = 0, kGroupCoded = 1, kGroupRaw = 2, kGroupBad = 3 };
 
-// One 512-value block of a 12-bit group -> two 16 x 16 fragments of four 8 x 8 matrices.
-__device__ __forceinline__ void pfx_restore(const uint8_t *blk, uint32_t tag, int lane, uint32_t (&a0)[4], uint32_t (&a1)[4])
+// A coded group (four blocks of 512 values) -> rows 16 page .. 16 page + 15 of an operand's block.
+// A block's fragments are 8 x 8 matrices in the storage order's lanes: stmatrix puts their rows
+// where the swizzled operand wants them (V's are dims x tokens and are stored back transposed).
+// Two blocks a turn, their loads issued before either is used; K and V share the code: the
+// kernel's roles run side by side and their loops have to fit the instruction caches together
+// (unrolled by four and by role, a third of the stalls were for instructions).
+__device__ __forceinline__ void pfx_restore_group(const uint8_t *src, uint32_t tags, uint32_t unit, int page, int lane,
+                                                  bool is_v)
 {
-    if (tag == 0xFFu) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(blk + 32 * lane);
-        const uint4 y = *reinterpret_cast<const uint4 *>(blk + 32 * lane + 16);
-        a0[0] = x.x; a0[1] = x.y; a0[2] = x.z; a0[3] = x.w;
-        a1[0] = y.x; a1[1] = y.y; a1[2] = y.z; a1[3] = y.w;
-    } else {
-        const uint4 low = *reinterpret_cast<const uint4 *>(blk + 16 * lane);
-        const uint2 code = *reinterpret_cast<const uint2 *>(blk + 512 + 8 * lane);
-        restore_fragment(low.x, low.y, code.x, tag * 0x01010101u, a0);
-        restore_fragment(low.z, low.w, code.y, tag * 0x01010101u, a1);
+    const int mi = lane >> 3, rr = lane & 7;
+    const int row = 16 * page + rr + 8 * (is_v ? mi >> 1 : mi & 1), c8 = is_v ? mi & 1 : mi >> 1;
+    // 16-byte column 4 (j % 2) + 2 f + c8 of the rows of half j / 2, swizzled by the row
+    uint32_t at = unit + row * 128;
+    const uint32_t col = (uint32_t)((c8 ^ rr) << 4);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        uint4 x[2];
+        uint2 y[2], z[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const bool raw = (tags >> (8 * j) & 0x80u) != 0;
+            const uint8_t *lo = src + (raw ? 32 : 16) * lane, *hi = src + (raw ? 32 * lane + 16 : 512 + 8 * lane);
+            x[j] = *reinterpret_cast<const uint4 *>(lo);
+            y[j] = *reinterpret_cast<const uint2 *>(hi);
+            z[j] = raw ? *reinterpret_cast<const uint2 *>(hi + 8) : make_uint2(0, 0);
+            src += raw ? KVZ_BLOCK_BYTES_RAW : KVZ_BLOCK_BYTES_ELIGIBLE;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t bb = __byte_perm(tags, 0, 0x1111 * j);  // the block's tag in every byte
+            uint32_t a[2][4] = {{x[j].x, x[j].y, x[j].z, x[j].w}, {y[j].x, y[j].y, z[j].x, z[j].y}};
+            if (!(bb & 0x80u)) {
+                restore_fragment(x[j].x, x[j].y, y[j].x, bb, a[0]);
+                restore_fragment(x[j].z, x[j].w, y[j].y, bb, a[1]);
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const uint32_t to = at + (col ^ (64u * j + 32u * f));
+                if (is_v) stmatrix_x4_trans(to, a[f]);
+                else stmatrix_x4(to, a[f]);
+            }
+        }
+        tags >>= 16;
+        at += kHalfBytes;
     }
 }
+
+// Eight flags as bytes and back.
+__device__ __forceinline__ uint64_t spread_bits(uint32_t bits)
+{
+    uint64_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r |= (uint64_t)(bits >> i & 1) << (8 * i);
+    return r;
+}
+__device__ __forceinline__ uint32_t gather_bits(uint64_t bytes) { return (uint32_t)((bytes * 0x0102040810204080ull) >> 56); }
 
 template <int kFmt, int kTiles>
 __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
@@ -186,7 +223,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
     pdl_launch_dependents();  // the own-pages kernel may be placed as CTAs here finish
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int2 *plan = reinterpret_cast<int2 *>(smem + S::plan);
-    uint32_t *info = reinterpret_cast<uint32_t *>(smem + S::info);
+    uint64_t *info = reinterpret_cast<uint64_t *>(smem + S::info);  // a byte per page
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(smem + S::misc);
 
     if (tid == 0) {
@@ -204,8 +241,8 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         mbar_init(sbase + S::drain, 1);
         if (kCoded)
             for (int s = 0; s < S::stages; ++s) {
-                mbar_init(sbase + S::sempty + 8 * s, 1);
                 mbar_init(sbase + S::sarrived + 8 * s, 1);
+                mbar_init(sbase + S::sempty + 8 * s, 1);
             }
         misc[1] = 0;
         fence_barrier_init();
@@ -289,7 +326,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                     ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, kv) ^ 1));
                     if (!ok) break;
                     if (lane == 0) {
-                        if (kv == 0) info[n % kInfoRing] = (bad >> (kPfxPages * i)) & 0xFFu;
+                        if (kv == 0) info[n % kInfoRing] = spread_bits((bad >> (kPfxPages * i)) & 0xFFu);
                         if (live) mbar_arrive_expect_tx(fullbar, __popc(live) * (kPage * kDim * 2));
                         else mbar_arrive(fullbar);
                     }
@@ -313,166 +350,168 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         }
     } else if (warp == 8) {
         // ========================= producer, 12-bit pages =========================
-        // One lane per page, 32 pages (four blocks) at a time: the metadata of the next four
-        // blocks and the ids of the four behind them are fetched while these are copied.  Eight
-        // lanes, a block's pages, wait for their stages and issue together.
+        // Lane p copies the K group of every block's page p, lane 8 + p its V group, each as soon
+        // as its stage is free.  Places and sizes are worked out by the whole warp, 32 pages (four
+        // blocks) at a time, two batches on hand, and handed to the copying lanes by shuffles; the
+        // metadata of the third batch and the ids of the fourth are fetched ahead.  (A lane working
+        // out its own group while the others wait took 600 clocks a group.)
         const uint64_t keep = l2_evict_last();
-        const int pages = (hi - lo) * kPfxPages;
+        const int nb = hi - lo, page = lane & 7, st = lane & 15;
+        const bool is_v = (lane & 8) != 0, copies = lane < 2 * kPfxPages;
         struct Pre {
-            int32_t id, kvh;
-            int kind, valid;
+            int32_t id;
+            uint32_t what;  // KV head << 16 | valid tokens << 8 | kind
         };
         auto prep = [&](int y) -> Pre {
-            Pre r{-1, 0, kPageNone, 0};
-            if (y >= pages) return r;
+            if (y >= nb * kPfxPages) return Pre{-1, kGroupNone};
             const PfxSeg s = pfx_locate(P, plan, lo + y / kPfxPages, hi);
             const int p = s.block0 * kPfxPages + y % kPfxPages;
-            if (p * kPage >= s.len) return r;
-            r.kvh = s.kvh;
-            r.kind = p < s.len / kPage ? kPageCoded : kPageRaw;  // the raw tail is the last page
-            r.valid = min(kPage, s.len - p * kPage);
-            r.id = r.kind == kPageCoded ? ld_keep_s32(P.prefix_ids + (int64_t)s.g * P.max_pages + p, keep)
-                                        : ld_keep_s32(P.prefix_tail + s.g, keep);
-            return r;
+            if (p * kPage >= s.len) return Pre{-1, kGroupNone};
+            const bool coded = p < s.len / kPage;  // the raw tail is the last page
+            return Pre{coded ? ld_keep_s32(P.prefix_ids + (int64_t)s.g * P.max_pages + p, keep)
+                             : ld_keep_s32(P.prefix_tail + s.g, keep),
+                       (uint32_t)s.kvh << 16 | (uint32_t)min(kPage, s.len - p * kPage) << 8 |
+                           (coded ? kGroupCoded : kGroupRaw)};
         };
-        auto load_meta = [&](const Pre &r, uint64_t &k, uint64_t &v) {
-            k = v = 0;
-            if (r.kind == kPageCoded && r.id >= 0 && r.id < P.num_meta_pages)
-                ld_keep_u64x2(P.meta + ((int64_t)r.id * P.hkv + r.kvh) * 2, keep, k, v);
+        uint64_t mk = 0, mv = 0;
+        auto load_meta = [&](const Pre &r) {
+            if ((r.what & 0xFFu) == kGroupCoded && r.id >= 0 && r.id < P.num_meta_pages)
+                ld_keep_u64x2(P.meta + ((int64_t)r.id * P.hkv + (r.what >> 16)) * 2, keep, mk, mv);
         };
-        Pre cur = prep(lane), nxt = prep(32 + lane);
-        uint64_t mk, mv;
-        load_meta(cur, mk, mv);
-        bool ok = true;
-        for (int base = 0; base < pages && ok; base += 32) {
-            uint32_t kind = kPageNone, flag = 0, bk = 0, bv = 0;
-            uint64_t srck = 0, srcv = 0;
-            const uint32_t tk = (uint32_t)(mk >> 32), tv = (uint32_t)(mv >> 32);
-            if (cur.kind == kPageCoded) {
-                const uint32_t ok_ = (uint32_t)mk, ov_ = (uint32_t)mv;
-                if (cur.id < 0 || cur.id >= P.num_meta_pages) {
+        struct Place {
+            uint32_t what, offk, offv, tk, tv;  // raw: offk = index of the K and V pair
+        };
+        auto resolve = [&](const Pre &r) -> Place {  // from the metadata in mk, mv
+            Place q{r.what & 0xFFFFu, (uint32_t)mk, (uint32_t)mv, (uint32_t)(mk >> 32), (uint32_t)(mv >> 32)};
+            uint32_t flag = 0;
+            if ((q.what & 0xFFu) == kGroupCoded) {
+                if (r.id < 0 || r.id >= P.num_meta_pages)
                     flag = KVZ_STATUS_BAD_INDEX;
-                } else if (!tags_valid(tk) || !tags_valid(tv) || ok_ == KVZ_OFFSET_INVALID || ov_ == KVZ_OFFSET_INVALID ||
-                           ((uint64_t)ok_ + group_granules(tk)) * kGranule > P.arena_bytes ||
-                           ((uint64_t)ov_ + group_granules(tv)) * kGranule > P.arena_bytes) {
+                else if (!tags_valid(q.tk) || !tags_valid(q.tv) || q.offk == KVZ_OFFSET_INVALID || q.offv == KVZ_OFFSET_INVALID ||
+                         ((uint64_t)q.offk + group_granules(q.tk)) * kGranule > P.arena_bytes ||
+                         ((uint64_t)q.offv + group_granules(q.tv)) * kGranule > P.arena_bytes)
                     flag = KVZ_STATUS_BAD_META;
-                } else {
-                    kind = kPageCoded;
-                    bk = group_granules(tk) * kGranule;
-                    bv = group_granules(tv) * kGranule;
-                    srck = (uint64_t)ok_ * kGranule;
-                    srcv = (uint64_t)ov_ * kGranule;
-                }
-            } else if (cur.kind == kPageRaw) {
-                if (cur.id < 0 || cur.id >= P.num_raw_pages) {
-                    flag = cur.id == -1 ? KVZ_STATUS_BAD_TAIL : KVZ_STATUS_BAD_INDEX;
-                } else {
-                    kind = kPageRaw;
-                    srck = ((uint64_t)cur.id * P.hkv + cur.kvh) * kPageBytes;
-                }
+            } else if ((q.what & 0xFFu) == kGroupRaw) {
+                if (r.id < 0 || r.id >= P.num_raw_pages) flag = r.id == -1 ? KVZ_STATUS_BAD_TAIL : KVZ_STATUS_BAD_INDEX;
+                q.offk = (uint32_t)r.id * (uint32_t)P.hkv + (r.what >> 16);
             }
-            if (flag) atomicOr(P.status, flag);
-            const uint32_t bad = __ballot_sync(0xffffffffu, flag != 0);
-            const int valid = cur.valid;
-            cur = nxt;
-            load_meta(cur, mk, mv);
-            nxt = prep(base + 64 + lane);
-            for (int i = 0; i < 32 / kPfxPages && ok; ++i) {
-                const int n = base / kPfxPages + i;
-                if (n >= hi - lo) break;
-                if (lane / kPfxPages == i) {
-                    constexpr int kStages = kCoded ? S::stages : 1;
-                    const int st = (base + lane) % kStages;
-                    if (wait(sbase + S::sempty + 8 * st, (((base + lane) / kStages) & 1) ^ 1)) {
-                        const uint32_t bar = sbase + S::sarrived + 8 * st, dst = sbase + S::stage + st * kPageBytes;
-                        if (lane % kPfxPages == 0) info[n % kInfoRing] = (bad >> (kPfxPages * i)) & 0xFFu;
-                        *reinterpret_cast<PageInfo *>(smem + S::sinfo + 16 * st) = PageInfo{kind, (uint32_t)valid, tk, tv};
-                        if (kind == kPageCoded) {
-                            mbar_arrive_expect_tx(bar, bk + bv);
-                            if (srcv == srck + bk) {  // pages encoded together: one copy
-                                bulk_copy_g2s(dst, P.arena + srck, bk + bv, bar);
-                            } else {
-                                bulk_copy_g2s(dst, P.arena + srck, bk, bar);
-                                bulk_copy_g2s(dst + bk, P.arena + srcv, bv, bar);
-                            }
-                        } else if (kind == kPageRaw) {
-                            mbar_arrive_expect_tx(bar, kPageBytes);
-                            bulk_copy_g2s(dst, reinterpret_cast<const uint8_t *>(P.raw_pool) + srck, kPageBytes, bar);
-                        } else {
-                            mbar_arrive(bar);
-                        }
+            if (flag) {
+                q.what = kGroupBad;
+                atomicOr(P.status, flag);
+            }
+            return q;
+        };
+        Pre third = prep(lane), fourth = prep(32 + lane);
+        load_meta(third);
+        Place a = resolve(third);
+        third = fourth;
+        load_meta(third);
+        fourth = prep(64 + lane);
+        Place b = resolve(third);
+        third = fourth;
+        load_meta(third);
+        fourth = prep(96 + lane);
+        const uint32_t emptybar = sbase + S::sempty + 8 * st, bar = sbase + S::sarrived + 8 * st;
+        uint64_t since = 0;
+        bool ok = true;
+        int batch = 0;  // of `a`
+        for (int n = copies ? 0 : nb, idle = 0; ok && __any_sync(0xffffffffu, n < nb);) {
+            const bool ready = n < nb && n / 4 <= batch + 1 && mbar_test_wait(emptybar, (n & 1) ^ 1);
+            if (__any_sync(0xffffffffu, ready)) {
+                const int from = 8 * (n & 3) + page;
+                const bool later = n / 4 != batch;
+                auto get = [&](uint32_t x, uint32_t y) {
+                    const uint32_t u = __shfl_sync(0xffffffffu, x, from), v = __shfl_sync(0xffffffffu, y, from);
+                    return later ? v : u;
+                };
+                const uint32_t what = get(a.what, b.what), offk = get(a.offk, b.offk), offv = get(a.offv, b.offv);
+                const uint32_t tk = get(a.tk, b.tk), tv = get(a.tv, b.tv), kind = what & 0xFFu;
+                if (ready) {
+                    const uint32_t tags = is_v ? tv : tk;
+                    *reinterpret_cast<uint2 *>(smem + S::sinfo + 8 * st) = make_uint2(what, tags);
+                    if (kind == kGroupCoded) {
+                        const uint32_t bytes = group_granules(tags) * kGranule;
+                        mbar_arrive_expect_tx(bar, bytes);
+                        bulk_copy_g2s(sbase + S::stage + st * kGroupBytes, P.arena + (uint64_t)(is_v ? offv : offk) * kGranule,
+                                      bytes, bar);
+                    } else if (kind == kGroupRaw) {
+                        mbar_arrive_expect_tx(bar, kGroupBytes);
+                        bulk_copy_g2s(sbase + S::stage + st * kGroupBytes,
+                                      reinterpret_cast<const uint8_t *>(P.raw_pool) +
+                                          ((uint64_t)offk * 2 + (is_v ? 1 : 0)) * kGroupBytes,
+                                      kGroupBytes, bar);
+                    } else {
+                        mbar_arrive(bar);
                     }
+                    ++n;
                 }
-                ok = __all_sync(0xffffffffu, wait.ok);
+                __syncwarp();
+                idle = 0;
+                if (__all_sync(0xffffffffu, n >= min(nb, 4 * (batch + 1)))) {  // every lane is done with `a`
+                    ++batch;
+                    a = b;
+                    b = resolve(third);
+                    third = fourth;
+                    load_meta(third);
+                    fourth = prep(32 * (batch + 3) + lane);
+                }
+            } else if ((++idle & 1023) == 0) {  // bounded: give up after kWaitLimitNs without a step
+                const uint64_t now = globaltimer_ns();
+                if (idle == 1024) since = now;
+                if (misc[1] || now - since > kWaitLimitNs) {
+                    if (lane == 0) atomicOr(P.status, KVZ_STATUS_TIMEOUT);
+                    misc[1] = 1;
+                    ok = false;
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            } else {
+                __nanosleep(64);  // polling takes issue slots from the softmax warps of its scheduler
             }
         }
         if (!ok) {  // (as above: no copies in flight at the end)
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 1000000) {}
         }
-    } else if (kCoded && warp >= 10 && warp < 10 + kExpWarps) {
+    } else if (kCoded && warp >= 10) {
         // ================== 12-bit pages to BF16 operands ==================
-        // A warp takes two pages of each block, K of both before V of either: K's block must not
-        // wait for the room that V's does.  A block's fragments are 8 x 8 matrices in the storage
-        // order's lanes: stmatrix puts their rows where the swizzled operand wants them (V's
-        // fragments are transposed, dims x tokens, and are stored back as tokens x dims).
-        constexpr int kMine = kPfxPages / kExpWarps;
-        const int mi = lane >> 3, rr = lane & 7;
+        const bool is_v = warp >= 10 + kExpWarps;
+        const int w = (warp - 10) % kExpWarps;
         bool ok = true;
         for (int n = 0; n < hi - lo && ok; ++n) {
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const int slot = S::slot(n, kv);
-                if (ok) ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, kv) ^ 1));
-                const uint32_t unit = sbase + S::ring + slot * kUnitBytes;
+            const int slot = S::slot(n, is_v);
+            ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, is_v) ^ 1));
+            const uint32_t unit = sbase + S::ring + slot * kUnitBytes;
+            for (int page = w; page < kPfxPages && ok; page += kExpWarps) {  // every third page
+                const int st = (is_v ? kPfxPages : 0) + page;
+                const uint8_t *stage = smem + S::stage + st * kGroupBytes;
+                ok = __all_sync(0xffffffffu, wait(sbase + S::sarrived + 8 * st, n & 1));
+                if (!ok) break;
+                const uint2 gi = *reinterpret_cast<const uint2 *>(smem + S::sinfo + 8 * st);
+                const uint32_t kind = gi.x & 0xFFu;
+                if (kind == kGroupCoded) {
+                    pfx_restore_group(stage, gi.y, unit, page, lane, is_v);
+                } else if (is_v || kind == kGroupRaw) {
+                    // a raw tail as it is; rows of V without a token are zero, so that weight 0
+                    // times them is 0 (scores of K rows without one are not used)
+                    const uint32_t have = kind == kGroupRaw ? gi.x >> 8 : 0;
 #pragma unroll 1
-                for (int q = 0; q < kMine && ok; ++q) {
-                    constexpr int kStages = kCoded ? S::stages : 1;
-                    const int page = warp - 10 + q * kExpWarps, y = n * kPfxPages + page, st = y % kStages;
-                    const uint8_t *src = smem + S::stage + st * kPageBytes;
-                    if (kv == 0) ok = __all_sync(0xffffffffu, wait(sbase + S::sarrived + 8 * st, (y / kStages) & 1));
-                    if (!ok) break;
-                    const PageInfo pi = *reinterpret_cast<const PageInfo *>(smem + S::sinfo + 16 * st);
-                    if (pi.kind == kPageCoded) {
-                        const uint32_t tags = kv ? pi.tagsV : pi.tagsK;
-                        const int row = 16 * page + rr + 8 * (kv ? mi >> 1 : mi & 1), c8 = kv ? mi & 1 : mi >> 1;
-                        uint32_t off = kv ? group_granules(pi.tagsK) * kGranule : 0;  // V right after K
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t tag = (tags >> (8 * j)) & 0xFFu;
-                            uint32_t a[2][4];
-                            pfx_restore(src + off, tag, lane, a[0], a[1]);
-#pragma unroll
-                            for (int f = 0; f < 2; ++f) {
-                                const int ch = 4 * (j & 1) + 2 * f + c8;  // 16-byte column within the half's rows
-                                const uint32_t at = unit + (j >> 1) * kHalfBytes + row * 128 + ((ch ^ (row & 7)) << 4);
-                                if (kv) stmatrix_x4_trans(at, a[f]);
-                                else stmatrix_x4(at, a[f]);
-                            }
-                            off += tag_granules(tag) * kGranule;
-                        }
-                    } else if (kv || pi.kind == kPageRaw) {
-                        // a raw tail as it is; rows of V without a token are zero, so that weight 0
-                        // times them is 0 (scores of K rows without one are not used)
-                        const uint32_t have = pi.kind == kPageRaw ? pi.valid : 0;
-#pragma unroll 1
-                        for (int i = 0; i < 8; ++i) {
-                            const int tok = 2 * i + (lane >> 4), ch = lane & 15, row = 16 * page + tok;
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if ((uint32_t)tok < have)
-                                x = *reinterpret_cast<const uint4 *>(src + kv * (kPageBytes / 2) + tok * 256 + ch * 16);
-                            *reinterpret_cast<uint4 *>(smem + S::ring + slot * kUnitBytes + (ch >> 3) * kHalfBytes +
-                                                       row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = x;
-                        }
-                    }
-                    fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(sbase + S::full + 8 * slot);
-                        if (kv) mbar_arrive(sbase + S::sempty + 8 * st);
+                    for (int i = 0; i < 8; ++i) {
+                        const int tok = 2 * i + (lane >> 4), ch = lane & 15, row = 16 * page + tok;
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if ((uint32_t)tok < have) x = *reinterpret_cast<const uint4 *>(stage + tok * 256 + ch * 16);
+                        *reinterpret_cast<uint4 *>(smem + S::ring + slot * kUnitBytes + (ch >> 3) * kHalfBytes + row * 128 +
+                                                   (((ch & 7) ^ (row & 7)) << 4)) = x;
                     }
                 }
+                __syncwarp();
+                if (lane == 0) {
+                    if (!is_v) reinterpret_cast<uint8_t *>(info + n % kInfoRing)[page] = kind == kGroupBad;
+                    mbar_arrive(sbase + S::sempty + 8 * st);
+                }
             }
+            fence_async_shared();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(sbase + S::full + 8 * slot);
         }
     } else if (warp == 9) {
         // ============================ matrix products ============================
@@ -663,7 +702,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 const bool fresh = mine % P.fold == 0;  // the output begins anew
                 if (fresh && mine > 0 && active) fold(m, nullptr);
                 const int left = sg.len - (sg.block0 + j) * kPfxBlock;
-                const uint32_t bad = info[n % kInfoRing];
+                const uint32_t bad = gather_bits(info[n % kInfoRing]);
                 const bool whole = left >= kPfxBlock && bad == 0;
                 uint32_t v[4][32];
                 if (active) {

@@ -154,47 +154,58 @@ enum : uint32_t { kGroupNone = 0, kGroupCoded = 1, kGroupRaw = 2, kGroupBad = 3 
 // A coded group (four blocks of 512 values) -> rows 16 page .. 16 page + 15 of an operand's block.
 // A block's fragments are 8 x 8 matrices in the storage order's lanes: stmatrix puts their rows
 // where the swizzled operand wants them (V's are dims x tokens and are stored back transposed).
-// Two blocks a turn, their loads issued before either is used; K and V share the code: the
-// kernel's roles run side by side and their loops have to fit the instruction caches together
-// (unrolled by four and by role, a third of the stalls were for instructions).
+// A group without raw blocks, the common one, has its blocks at fixed places: all loads are issued
+// before any is used.  K and V share the code: the kernel's roles run side by side and their loops
+// have to fit the instruction caches together (unrolled by role as well, a third of the stalls were
+// for instructions).
 __device__ __forceinline__ void pfx_restore_group(const uint8_t *src, uint32_t tags, uint32_t unit, int page, int lane,
                                                   bool is_v)
 {
     const int mi = lane >> 3, rr = lane & 7;
     const int row = 16 * page + rr + 8 * (is_v ? mi >> 1 : mi & 1), c8 = is_v ? mi & 1 : mi >> 1;
     // 16-byte column 4 (j % 2) + 2 f + c8 of the rows of half j / 2, swizzled by the row
-    uint32_t at = unit + row * 128;
-    const uint32_t col = (uint32_t)((c8 ^ rr) << 4);
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-        uint4 x[2];
-        uint2 y[2], z[2];
+    const uint32_t at = unit + row * 128, col = (uint32_t)((c8 ^ rr) << 4);
+    auto put = [&](uint32_t to, const uint32_t (&a)[4]) {
+        if (is_v) stmatrix_x4_trans(to, a);
+        else stmatrix_x4(to, a);
+    };
+    if (!(tags & 0x80808080u)) {
+        uint4 low[4];
+        uint2 code[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const bool raw = (tags >> (8 * j) & 0x80u) != 0;
-            const uint8_t *lo = src + (raw ? 32 : 16) * lane, *hi = src + (raw ? 32 * lane + 16 : 512 + 8 * lane);
-            x[j] = *reinterpret_cast<const uint4 *>(lo);
-            y[j] = *reinterpret_cast<const uint2 *>(hi);
-            z[j] = raw ? *reinterpret_cast<const uint2 *>(hi + 8) : make_uint2(0, 0);
-            src += raw ? KVZ_BLOCK_BYTES_RAW : KVZ_BLOCK_BYTES_ELIGIBLE;
+        for (int j = 0; j < 4; ++j) {
+            low[j] = *reinterpret_cast<const uint4 *>(src + 768 * j + 16 * lane);
+            code[j] = *reinterpret_cast<const uint2 *>(src + 768 * j + 512 + 8 * lane);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const uint32_t bb = __byte_perm(tags, 0, 0x1111 * j);  // the block's tag in every byte
-            uint32_t a[2][4] = {{x[j].x, x[j].y, x[j].z, x[j].w}, {y[j].x, y[j].y, z[j].x, z[j].y}};
-            if (!(bb & 0x80u)) {
-                restore_fragment(x[j].x, x[j].y, y[j].x, bb, a[0]);
-                restore_fragment(x[j].z, x[j].w, y[j].y, bb, a[1]);
-            }
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const uint32_t to = at + (col ^ (64u * j + 32u * f));
-                if (is_v) stmatrix_x4_trans(to, a[f]);
-                else stmatrix_x4(to, a[f]);
-            }
+            const uint32_t to = at + (j >> 1) * kHalfBytes + (col ^ (64u * (j & 1)));
+            uint32_t a[4];
+            restore_fragment(low[j].x, low[j].y, code[j].x, bb, a);
+            put(to, a);
+            restore_fragment(low[j].z, low[j].w, code[j].y, bb, a);
+            put(to ^ 32u, a);
         }
-        tags >>= 16;
-        at += kHalfBytes;
+        return;
+    }
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+        const bool raw = (tags & 0x80u) != 0;
+        const uint8_t *lo = src + (raw ? 32 : 16) * lane, *hi = src + (raw ? 32 * lane + 16 : 512 + 8 * lane);
+        const uint4 x = *reinterpret_cast<const uint4 *>(lo);
+        const uint2 y = *reinterpret_cast<const uint2 *>(hi), z = raw ? *reinterpret_cast<const uint2 *>(hi + 8) : make_uint2(0, 0);
+        uint32_t a[2][4] = {{x.x, x.y, x.z, x.w}, {y.x, y.y, z.x, z.y}};
+        if (!raw) {
+            const uint32_t bb = __byte_perm(tags, 0, 0x0000);
+            restore_fragment(x.x, x.y, y.x, bb, a[0]);
+            restore_fragment(x.z, x.w, y.y, bb, a[1]);
+        }
+        const uint32_t to = at + (j >> 1) * kHalfBytes + (col ^ (64u * (j & 1)));
+        put(to, a[0]);
+        put(to ^ 32u, a[1]);
+        src += raw ? KVZ_BLOCK_BYTES_RAW : KVZ_BLOCK_BYTES_ELIGIBLE;
+        tags >>= 8;
     }
 }
 
@@ -290,13 +301,15 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
     PfxWait wait{P.status, misc + 1, true};
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::other_regs));
-    if (warp == 8 && !kCoded) {
+    if ((warp == 8 || warp == 10) && !kCoded) {
         // =============================== producer ===============================
         // One lane per page, 32 pages (four blocks) at a time; the ids of the next four
         // blocks are fetched while these are copied.  (Calling pages into L2 four blocks ahead
         // made a 131072-token prefix 12% slower.)  Eight pages of 16 rows make a block's K (or V) operand: two
-        // boxes a page, one per 64-column half.
+        // boxes a page, one per 64-column half.  One warp copies K, one V: a copy takes its issuing warp
+        // about 100 clocks, and a block has 32 of them.
         prefetch_tensormap(&tmap);
+        const int kv = warp == 8 ? 0 : 1;
         const uint64_t keep = l2_evict_last();
         const int pages = (hi - lo) * kPfxPages;
         auto prep = [&](int y) -> int {  // the page's first row in the raw pool, -1: none, -2: bad
@@ -319,25 +332,21 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 if (n >= hi - lo) break;
                 const uint32_t live = (good >> (kPfxPages * i)) & 0xFFu;
                 const int row = __shfl_sync(0xffffffffu, cur, kPfxPages * i + ((lane >> 1) & 7));
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int slot = S::slot(n, kv);
-                    const uint32_t fullbar = sbase + S::full + 8 * slot;
-                    ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, kv) ^ 1));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (kv == 0) info[n % kInfoRing] = spread_bits((bad >> (kPfxPages * i)) & 0xFFu);
-                        if (live) mbar_arrive_expect_tx(fullbar, __popc(live) * (kPage * kDim * 2));
-                        else mbar_arrive(fullbar);
-                    }
-                    __syncwarp();
-                    if (lane < 2 * kPfxPages && row >= 0) {
-                        const uint32_t dst =
-                            sbase + S::ring + slot * kUnitBytes + (lane & 1) * kHalfBytes + (lane >> 1) * (kPage * 128);
-                        tensor_copy_2d_g2s(dst, &tmap, (lane & 1) * 64, row + kv * kPage, fullbar);
-                    }
-                }
+                const int slot = S::slot(n, kv);
+                const uint32_t fullbar = sbase + S::full + 8 * slot;
+                ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, kv) ^ 1));
                 if (!ok) break;
+                if (lane == 0) {
+                    if (kv == 0) info[n % kInfoRing] = spread_bits((bad >> (kPfxPages * i)) & 0xFFu);
+                    if (live) mbar_arrive_expect_tx(fullbar, __popc(live) * (kPage * kDim * 2));
+                    else mbar_arrive(fullbar);
+                }
+                __syncwarp();
+                if (lane < 2 * kPfxPages && row >= 0) {
+                    const uint32_t dst =
+                        sbase + S::ring + slot * kUnitBytes + (lane & 1) * kHalfBytes + (lane >> 1) * (kPage * 128);
+                    tensor_copy_2d_g2s(dst, &tmap, (lane & 1) * 64, row + kv * kPage, fullbar);
+                }
             }
             cur = nxt;
             nxt = nn;

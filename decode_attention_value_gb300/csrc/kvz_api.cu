@@ -248,14 +248,14 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
 {
     const int hkv = d.num_kv_heads, G = hq / hkv;
     const bool raw = F.format == kFmtRaw;
-    int grid = 0, pgrid = 0;
-    int rc = attention_grid(batch, hkv, raw ? max_pages : max_pages + 1, &grid);
+    int grid = 0, pgrid = 0, rc = 0;
+    if (max_pages > kOwnPages) rc = attention_grid(batch, hkv, raw ? max_pages : max_pages + 1, &grid);
     if (rc) return rc;
     rc = prefix_grid(batch, hkv, G, X.groups, raw ? X.max_pages : X.max_pages + 1, &pgrid);
     if (rc) return rc;
     const size_t rows = pfx_part_rows(pfx_max_units(batch, hkv, G, X.groups), pgrid);
     const size_t prefix_bytes = rows * (kDim + 2) * 4;
-    if (prefix_bytes + attn_ws_bytes(batch, hkv, grid, G) > ws_bytes) return KVZ_ERR_WORKSPACE;
+    if (prefix_bytes + (grid > 0 ? attn_ws_bytes(batch, hkv, grid, G) : 0) > ws_bytes) return KVZ_ERR_WORKSPACE;
     CUtensorMap map, pmap;
     rc = raw_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &map);
     if (!rc) rc = prefix_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &pmap);
@@ -813,8 +813,9 @@ size_t kvz_prefix_attention_workspace_size(kvz_dims dims, int32_t batch, int32_t
 {
     if (num_groups < 0 || num_groups > kPfxMaxGroups || prefix_pages < 0) return 0;
     if (dims_ok(dims) && num_q_heads >= 1 && num_q_heads % dims.num_kv_heads != 0) return 0;
-    const size_t own = kvz_attention_workspace_size(dims, batch, num_q_heads, table_pages);
+    size_t own = kvz_attention_workspace_size(dims, batch, num_q_heads, table_pages);
     if (own == 0 || batch == 0) return own;
+    if (table_pages <= kOwnPages) own = 16;  // (merged where they are computed)
     const int G = num_q_heads / dims.num_kv_heads;
     int grid = 0;
     if (prefix_grid(batch, dims.num_kv_heads, G, num_groups, prefix_pages, &grid) != KVZ_OK) return 0;

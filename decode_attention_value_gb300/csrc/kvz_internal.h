@@ -159,6 +159,11 @@ inline int64_t pfx_max_units(int batch, int hkv, int G, int groups)
 }
 inline size_t pfx_part_rows(int64_t units, int grid) { return grid > 0 ? (size_t)(units + grid - 1) * 2 * 128 : 0; }
 
+// Own tokens up to this many pages a sequence go through one block per (sequence, KV head), which
+// merges the prefix partials too (own.cu); longer ones are split over CTAs (A.grid > 0).
+constexpr int kOwnPages = 64;
+cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, const void *map, bool after_prefix,
+                       cudaStream_t stream);
 // prefix_map: tensor map of the raw pool with one page's 16 K or V rows x 64 columns a box
 cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_map, const AttnParams &A,
                           const void *own_map, cudaStream_t stream);

@@ -1,0 +1,341 @@
+// own.cu -- the own tokens of sequences that share prefixes, when there are few: one block per
+// (sequence, KV head) computes their attention and merges the prefix's partials into the output.
+//
+// The split kernel of attention.cu deals pages out evenly, which long sequences need; for a
+// hundred own tokens a sequence its segments are a few pages each, and their partials, written
+// and merged by a third kernel, cost more than the pages: 128 sequences x 8 query heads a KV head
+// with 0..200 own tokens took 56 us behind the prefix kernel, 52 MB of pages at 8 us.  Here the
+// partials never leave the block.
+//
+// A warp takes every fourth page, two in flight in its own shared-memory stages, and runs the
+// m16n8k16 products of attention.cu on it: S^T = K Q^T with the query heads in the columns, a
+// running softmax, O^T += V^T P^T with P as two BF16 parts.  The block's warps leave their states
+// in shared memory; then each head's warp adds the states and the prefix partials, in order.
+#include <cuda.h>
+
+#include <cstring>
+
+#include "frags.cuh"
+#include "prefix.cuh"
+
+namespace kvz {
+
+constexpr int kOwnWarps = 4, kOwnThreads = kOwnWarps * 32, kOwnStages = 2;
+constexpr int kOwnPageBytes = 2 * kPage * kDim * 2;
+constexpr int kOwnRing = kOwnWarps * kOwnStages * kOwnPageBytes;  // 64 KB; holds the warps' states afterwards
+constexpr int kOwnSmem = kOwnRing + kOwnWarps * kOwnStages * 8;
+
+template <int kFmt, bool kG8>
+__global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, const PrefixParams P, const int after,
+                                                        const __grid_constant__ CUtensorMap tmap)
+{
+    constexpr bool kCoded = kFmt != kFmtRaw;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ float2 wml[kOwnWarps][8];  // a warp's (maximum, sum) of each head
+    const uint32_t sbase = smem_addr(smem);
+    if (sbase & 1023u) {  // the swizzled TMA destinations need 1024-byte alignment
+        if (threadIdx.x == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int b = blockIdx.x / A.hkv, kvh = blockIdx.x % A.hkv, G = A.G;
+    const uint32_t bar0 = sbase + kOwnRing + warp * kOwnStages * 8;
+    if (lane == 0) {  // a warp's barriers are its own
+        for (int s = 0; s < kOwnStages; ++s) mbar_init(bar0 + 8 * s, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    const int L = A.seq_lens[b], n = L > 0 ? (L + kPage - 1) / kPage : 0;
+    if (L < 0 && tid == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
+    const int mine = (n - warp + kOwnWarps - 1) / kOwnWarps;  // pages warp, warp + 4, ...
+
+    // queries: B operand of QK^T, column = head (n % 4 when G <= 4)
+    uint32_t qf[8][2];
+    const int qhead = kG8 ? g : (g & 3);
+    const bool qhas = qhead < G;
+    const uint32_t *qg = reinterpret_cast<const uint32_t *>(
+        A.q + ((int64_t)b * A.hkv * G + (int64_t)kvh * G + (qhas ? qhead : 0)) * kDim);
+#pragma unroll
+    for (int kt = 0; kt < 8; ++kt) {
+        qf[kt][0] = qhas ? __ldg(qg + 8 * kt + t) : 0u;
+        qf[kt][1] = qhas ? __ldg(qg + 8 * kt + t + 4) : 0u;
+    }
+    float o[8][4];
+#pragma unroll
+    for (int a = 0; a < 8; ++a) o[a][0] = o[a][1] = o[a][2] = o[a][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    // lane i % 32 resolves the warp's i-th page, 32 at a time
+    enum : uint32_t { kSkip = 0, kPair = 1, kPlain = 2 };
+    uint32_t kind = kSkip, tk = 0, tv = 0;
+    const uint8_t *srck = nullptr, *srcv = nullptr;
+    int row = 0;
+    auto resolve = [&](int i0) {
+        kind = kSkip;
+        const int p = warp + kOwnWarps * (i0 + lane);
+        if (p >= n) return;
+        uint32_t flag = 0;
+        if (kCoded && p < L / kPage) {
+            const int32_t id = p < A.max_pages ? A.page_ids[(int64_t)b * A.max_pages + p] : INT32_MIN;
+            if (id < 0 || id >= A.num_meta_pages) {
+                flag = KVZ_STATUS_BAD_INDEX;
+            } else {
+                const uint64_t *m = A.meta + ((int64_t)id * A.hkv + kvh) * 2;
+                const uint64_t mk = m[0], mv = m[1];
+                const uint32_t ofk = (uint32_t)mk, ofv = (uint32_t)mv;
+                tk = (uint32_t)(mk >> 32);
+                tv = (uint32_t)(mv >> 32);
+                if (!tags_valid(tk) || !tags_valid(tv) || ofk == KVZ_OFFSET_INVALID || ofv == KVZ_OFFSET_INVALID ||
+                    ((uint64_t)ofk + group_granules(tk)) * kGranule > A.arena_bytes ||
+                    ((uint64_t)ofv + group_granules(tv)) * kGranule > A.arena_bytes)
+                    flag = KVZ_STATUS_BAD_META;
+                else
+                    kind = kPair;
+                srck = A.arena + (uint64_t)ofk * kGranule;
+                srcv = A.arena + (uint64_t)ofv * kGranule;
+            }
+        } else {
+            const int32_t id = kCoded ? A.tail_page[b] : p < A.max_pages ? A.page_ids[(int64_t)b * A.max_pages + p] : INT32_MIN;
+            if (id < 0 || id >= A.num_raw_pages) {
+                flag = kCoded && id == -1 ? KVZ_STATUS_BAD_TAIL : KVZ_STATUS_BAD_INDEX;
+            } else {
+                kind = kPlain;
+                row = (id * A.hkv + kvh) * 32;
+            }
+        }
+        if (flag) atomicOr(A.status, flag);
+    };
+    auto issue = [&](int i) {  // the warp's i-th page into its stage
+        if (lane != (i & 31)) return;
+        const uint32_t bar = bar0 + 8 * (i % kOwnStages);
+        const uint32_t dst = sbase + (warp * kOwnStages + i % kOwnStages) * kOwnPageBytes;
+        if (kind == kPair) {
+            const uint32_t bk = group_granules(tk) * kGranule, bv = group_granules(tv) * kGranule;
+            mbar_arrive_expect_tx(bar, bk + bv);
+            bulk_copy_g2s(dst, srck, bk, bar);
+            bulk_copy_g2s(dst + bk, srcv, bv, bar);
+        } else if (kind == kPlain) {
+            mbar_arrive_expect_tx(bar, kOwnPageBytes);
+            tensor_copy_2d_g2s(dst, &tmap, 0, row, bar);
+            tensor_copy_2d_g2s(dst + 4096, &tmap, 64, row, bar);
+        } else {
+            mbar_arrive(bar);
+        }
+    };
+    bool ok = true;
+    for (int i0 = 0; i0 < mine && ok; i0 += 32) {
+        const int cnt = min(32, mine - i0);
+        resolve(i0);
+        for (int i = 0; i < kOwnStages && i < cnt; ++i) issue(i0 + i);
+        for (int i = i0; i < i0 + cnt && ok; ++i) {
+            const int s = i % kOwnStages;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * s, (i / kOwnStages) & 1, A.status));
+            const uint32_t what = __shfl_sync(0xffffffffu, kind, i & 31);
+            if (ok && what != kSkip) {
+                const uint8_t *st = smem + (warp * kOwnStages + s) * kOwnPageBytes;
+                const uint32_t sta = sbase + (warp * kOwnStages + s) * kOwnPageBytes;
+                const uint32_t tagk = __shfl_sync(0xffffffffu, tk, i & 31), tagv = __shfl_sync(0xffffffffu, tv, i & 31);
+                const int valid = min(kPage, L - (warp + kOwnWarps * i) * kPage);
+                // ---- S^T = K Q^T over the page's 16 tokens ----
+                float sc[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t off = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t a0[4], a1[4];
+                    if (kCoded && what == kPair) {
+                        const uint32_t tag = (tagk >> (8 * j)) & 0xFFu;
+                        block_frags(st + off, tag, lane, a0, a1);
+                        off += tag_granules(tag) * kGranule;
+                    } else {
+                        raw_k_frag(sta, j, 0, lane, a0);
+                        raw_k_frag(sta, j, 1, lane, a1);
+                    }
+                    mma_bf16_16816(sc, a0, qf[2 * j][0], qf[2 * j][1]);
+                    mma_bf16_16816(sc, a1, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[e] *= A.scale_log2;
+                if (valid < kPage) {
+                    if (g >= valid) sc[0] = sc[1] = -INFINITY;
+                    if (g + 8 >= valid) sc[2] = sc[3] = -INFINITY;
+                }
+                // ---- running softmax (a column's 16 tokens: lanes with equal t) ----
+                float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+                }
+                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+                if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+                    const float f0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0), f1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
+#pragma unroll
+                    for (int a = 0; a < 8; ++a) {
+                        o[a][0] *= f0;
+                        o[a][2] *= f0;
+                        o[a][1] *= f1;
+                        o[a][3] *= f1;
+                    }
+                    l0 *= f0;
+                    l1 *= f1;
+                    m0 = n0;
+                    m1 = n1;
+                }
+                const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+                const float p0 = exp2f(sc[0] - u0), p1 = exp2f(sc[1] - u1), p2 = exp2f(sc[2] - u0), p3 = exp2f(sc[3] - u1);
+                l0 += p0 + p2;
+                l1 += p1 + p3;
+                // P as high and low BF16 parts: for G <= 4 in columns h and h + 4 of one product, else
+                // in two products
+                const float r0 = p0 - bf16_round(p0), r1 = p1 - bf16_round(p1);
+                const float r2 = p2 - bf16_round(p2), r3 = p3 - bf16_round(p3);
+                const bool low = !kG8 && t >= 2;
+                const uint32_t pb0 = movmatrix_trans(low ? pack_bf16x2(r0, r1) : pack_bf16x2(p0, p1));
+                const uint32_t pb1 = movmatrix_trans(low ? pack_bf16x2(r2, r3) : pack_bf16x2(p2, p3));
+                uint32_t pl0 = 0, pl1 = 0;
+                if (kG8) {
+                    pl0 = movmatrix_trans(pack_bf16x2(r0, r1));
+                    pl1 = movmatrix_trans(pack_bf16x2(r2, r3));
+                }
+                // ---- O^T += V^T P^T ----
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t a[2][4];
+                    if (kCoded && what == kPair) {
+                        const uint32_t tag = (tagv >> (8 * j)) & 0xFFu;
+                        block_frags(st + off, tag, lane, a[0], a[1]);  // V right after K
+                        off += tag_granules(tag) * kGranule;
+                    } else {
+                        raw_v_frag(sta, j, 0, lane, a[0]);
+                        raw_v_frag(sta, j, 1, lane, a[1]);
+                        if (valid < kPage) {
+                            mask_v_frag(a[0], lane, valid);
+                            mask_v_frag(a[1], lane, valid);
+                        }
+                    }
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        mma_bf16_16816(o[2 * j + f], a[f], pb0, pb1);
+                        if (kG8) mma_bf16_16816(o[2 * j + f], a[f], pl0, pl1);
+                    }
+                }
+            }
+            __syncwarp();
+            if (ok && i + kOwnStages < i0 + cnt) issue(i + kOwnStages);
+        }
+    }
+    // (after a wait that gave up, the copy it waited for may land late: microseconds)
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000) {}
+    }
+
+    // ---- the warp's state to shared memory ----
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    if (!kG8) {  // columns h and h + 4: the high and low parts of P
+#pragma unroll
+        for (int a = 0; a < 8; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[a][e] += __shfl_xor_sync(0xffffffffu, o[a][e], 2);
+    }
+    __syncthreads();  // every page has been read: the ring holds the states now
+    float *states = reinterpret_cast<float *>(smem);  // [warp][8 heads][128]
+    if (kG8 || t < 2) {
+        const int h0 = 2 * t, h1 = 2 * t + 1;
+        if (g == 0) {
+            wml[warp][h0] = make_float2(m0, l0);
+            wml[warp][h1] = make_float2(m1, l1);
+        }
+#pragma unroll
+        for (int a = 0; a < 8; ++a) {
+            float *to = states + (warp * 8 + h0) * kDim + 16 * a + g;
+            to[0] = o[a][0];
+            to[kDim] = o[a][1];
+            to[8] = o[a][2];
+            to[kDim + 8] = o[a][3];
+        }
+    }
+    __syncthreads();
+
+    // ---- a head at a time: the states, then the prefix's partials ----
+    const int share = G == 1 ? 4 : G == 2 ? 2 : 1;  // warps of a head
+    const int part = warp % share;
+    const PfxPlace where = pfx_place(P, b, lane);
+    if (after) pdl_wait_primary();  // the prefix partials are complete
+    for (int h0 = 0; h0 < G; h0 += kOwnWarps / share) {  // (uniform: the barrier below)
+        const int h = h0 + warp / share;
+        RowSum sum;
+        if (h < G) {
+            if (part == 0)
+                for (int w = 0; w < kOwnWarps; ++w)
+                    sum.add(wml[w][h].x, wml[w][h].y, *reinterpret_cast<const float4 *>(states + (w * 8 + h) * kDim + 4 * lane));
+            const PfxItems pre = pfx_items(P, where, b, kvh, h);
+            for (int i0 = part; i0 < pre.n; i0 += 32 * share) {
+                const int i = i0 + lane * share;
+                float2 e = make_float2(-INFINITY, 0.f);
+                if (i < pre.n) e = *reinterpret_cast<const float2 *>(P.part_ml + pre.row(i) * 2);
+                sum.add(e.x, e.y, min(32, (pre.n - i0 + share - 1) / share), [&](int k) {
+                    return reinterpret_cast<const float4 *>(P.part_o + pre.row(i0 + k * share) * kDim)[lane];
+                });
+            }
+        }
+        if (share > 1) {  // (one turn: G <= 2)
+            __syncthreads();
+            if (part > 0 && h < G) {
+                *reinterpret_cast<float4 *>(states + warp * 8 * kDim + 4 * lane) = sum.o;
+                if (lane == 0) wml[warp][0] = make_float2(sum.m, sum.l);
+            }
+            __syncthreads();
+            if (part > 0) continue;
+            for (int w = warp + 1; w < warp + share; ++w)
+                sum.add(wml[w][0].x, wml[w][0].y, *reinterpret_cast<const float4 *>(states + w * 8 * kDim + 4 * lane));
+        }
+        if (h < G) sum.store(P, (int64_t)blockIdx.x * G + h, lane);
+    }
+}
+
+template <int kFmt, bool kG8>
+static cudaError_t launch_own_impl(const AttnParams &A, const PrefixParams &P, const void *map, bool after,
+                                   cudaStream_t stream)
+{
+    // per process and device: more shared memory than the default (an attribute of the function)
+    static unsigned long long done = 0;  // bit per device ordinal < 64
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(dev < 64 && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1ull)) {
+        e = cudaFuncSetAttribute(k_own<kFmt, kG8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k_own<kFmt, kG8>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        if (e == cudaSuccess && dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_ACQ_REL);
+    }
+    if (e != cudaSuccess) return e;
+    CUtensorMap m;
+    memcpy(&m, map, sizeof m);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(A.batch * A.hkv);
+    cfg.blockDim = dim3(kOwnThreads);
+    cfg.dynamicSmemBytes = kOwnSmem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_own<kFmt, kG8>, A, P, after ? 1 : 0, m);
+}
+
+cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, const void *map, bool after_prefix,
+                       cudaStream_t stream)
+{
+    if (format == kFmtRaw)
+        return A.G > 4 ? launch_own_impl<kFmtRaw, true>(A, P, map, after_prefix, stream)
+                       : launch_own_impl<kFmtRaw, false>(A, P, map, after_prefix, stream);
+    return A.G > 4 ? launch_own_impl<kFmtZf, true>(A, P, map, after_prefix, stream)
+                   : launch_own_impl<kFmtZf, false>(A, P, map, after_prefix, stream);
+}
+
+}  // namespace kvz

@@ -12,12 +12,11 @@
 
 #include <cstring>
 
-#include "kvz_internal.h"
+#include "prefix.cuh"
 #include "tc.cuh"
 
 namespace kvz {
 
-constexpr int kPfxBlock = 128;                   // tokens of a block: 8 pages
 constexpr int kPfxPages = kPfxBlock / kPage;
 constexpr uint32_t kUnitBytes = kPfxBlock * kDim * 2;  // K or V of a block, BF16
 constexpr uint32_t kHalfBytes = kUnitBytes / 2;        // its 64-column halves
@@ -71,34 +70,6 @@ struct PfxSmem {
     static constexpr int plan = misc + 16;  // [groups + 1] {first unit, first block}
     static int bytes(int groups) { return plan + (groups + 1) * 8; }
 };
-
-// Units and blocks of group g (0, 0 when it has no sequence or no prefix).
-struct PfxGroup {
-    int seq0, seqs, len, blocks, tiles;
-};
-
-__device__ __forceinline__ PfxGroup pfx_group(const PrefixParams &P, int g)
-{
-    PfxGroup r;
-    r.seq0 = P.group_start[g];
-    r.seqs = P.group_start[g + 1] - r.seq0;
-    r.len = min(max(P.prefix_lens[g], 0), P.max_tokens);
-    r.blocks = (r.len + kPfxBlock - 1) / kPfxBlock;
-    r.tiles = r.blocks > 0 ? (r.seqs * P.G + P.unit_rows - 1) / P.unit_rows : 0;
-    return r;
-}
-
-// One warp: group starts ordered and in range?
-__device__ __forceinline__ bool pfx_groups_ok(const PrefixParams &P, int lane)
-{
-    bool ok = true;
-    for (int g = lane; g < P.num_groups; g += 32) ok &= P.group_start[g] <= P.group_start[g + 1];
-    ok &= P.group_start[0] >= 0 && P.group_start[P.num_groups] <= P.batch;
-    return __all_sync(0xffffffffu, ok);
-}
-
-// First block of CTA c's range of W blocks over C CTAs.
-__device__ __forceinline__ int pfx_first(int c, int W, int C) { return (int)(((int64_t)c * W + C - 1) / C); }
 
 struct PfxSeg {
     int g, kvh, tile, unit, block0, blocks, len, seq0, rows;  // rows of this unit's tile
@@ -847,158 +818,74 @@ constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 
 __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixParams P, const AttnParams A)
 {
-    __shared__ int red[kMergeWarps][8];
+    __shared__ int red[kMergeWarps][3];
     __shared__ float2 wml[kMergeWarps];
     __shared__ float4 acc[kMergeWarps][32];
     const int b = blockIdx.x / P.hkv, kvh = blockIdx.x % P.hkv, tid = threadIdx.x;
     const int warp = tid >> 5, lane = tid & 31;
     // ---- before the wait: what the lengths say (they were complete before the call) ----
-    // own pages of the sequences before b, of b, of all; prefix units and blocks before b's
-    // group and blocks in all; b's group
-    int v[7] = {0, 0, 0, 0, 0, 0, -1};
+    int v[3] = {0, 0, 0};  // own pages of the sequences before b, of b, of all
     for (int i = tid; i < P.batch; i += kMergeThreads) {
         const int L = A.seq_lens[i], pages = L > 0 ? (L + kPage - 1) / kPage : 0;
         v[0] += i < b ? pages : 0;
         v[1] += i == b ? pages : 0;
         v[2] += pages;
     }
-    if (P.num_groups > 0 && pfx_groups_ok(P, lane))
-        for (int g = tid; g < P.num_groups; g += kMergeThreads) {
-            const PfxGroup r = pfx_group(P, g);
-            const int n = P.hkv * r.tiles;
-            if (r.seq0 + r.seqs <= b) {  // groups before b's
-                v[3] += n;
-                v[4] += n * r.blocks;
-            } else if (r.seq0 <= b) {
-                v[6] = g;
-            }
-            v[5] += n * r.blocks;
-        }
 #pragma unroll
-    for (int i = 0; i < 6; ++i) v[i] = __reduce_add_sync(0xffffffffu, v[i]);
-    v[6] = __reduce_max_sync(0xffffffffu, v[6]);
+    for (int i = 0; i < 3; ++i) v[i] = __reduce_add_sync(0xffffffffu, v[i]);
     if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < 7; ++i) red[warp][i] = v[i];
+        for (int i = 0; i < 3; ++i) red[warp][i] = v[i];
     }
+    const PfxPlace where = pfx_place(P, b, lane);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 7; ++i) v[i] = red[0][i];
+    for (int i = 0; i < 3; ++i) {
+        v[i] = 0;
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) v[i] += red[w][i];
-        v[6] = max(v[6], red[w][6]);
+        for (int w = 0; w < kMergeWarps; ++w) v[i] += red[w][i];
     }
     const int share = P.G > 4 ? 1 : P.G > 2 ? 2 : P.G > 1 ? 4 : 8;  // warps of a head
     const int hg = warp / share, part = warp % share;
-    // prefix items: CTAs c0 .. c1 of the row's unit, one or two streams each
-    int np = 0, c0 = 0, row = 0, unit = 0;
-    const int streams = P.unit_rows == 128 ? 2 : 1;
-    if (v[6] >= 0 && hg < P.G) {
-        const PfxGroup r = pfx_group(P, v[6]);
-        if (r.blocks > 0) {
-            const int all = (b - r.seq0) * P.G + hg, tile = all / P.unit_rows;
-            row = all - tile * P.unit_rows;
-            const int ui = kvh * r.tiles + tile, W = v[5], C = min(P.grid, W);
-            const int first = v[4] + ui * r.blocks, last = first + r.blocks - 1;
-            unit = v[3] + ui;
-            c0 = (int)((int64_t)first * C / W);
-            np = ((int)((int64_t)last * C / W) - c0 + 1) * streams;
-        }
-    }
+    PfxItems pre{0, 1, 0, 0};
+    if (hg < P.G) pre = pfx_items(P, where, b, kvh, hg);
     // own items: CTAs of the split kernel that hold pages of (b, kvh)
     const int64_t T = (int64_t)P.hkv * v[2], AC = A.grid;
     int ns = 0, a0 = 0;
-    if (v[1] > 0) {
+    if (v[1] > 0 && hg < P.G) {
         const int64_t first = (int64_t)P.hkv * v[0] + (int64_t)kvh * v[1];
         a0 = (int)(first * AC / T);
         ns = (int)((first + v[1] - 1) * AC / T) - a0 + 1;
     }
-    const int items = hg < P.G ? np + ns : 0, heads = P.G > 4 ? 8 : 4;  // heads: of a slot of the split kernel
-    // partial i of the row
-    auto row_of = [&](int i) -> int64_t {
-        if (i < np) {
-            const int s = streams == 2 ? i & 1 : row >> 7, cc = c0 + i / streams;
-            return ((int64_t)(unit + cc) * 2 + s) * 128 + (row & 127);
-        }
-        return ((int64_t)(b * P.hkv + kvh) + a0 + (i - np)) * heads + hg;
-    };
+    const int items = pre.n + ns, heads = P.G > 4 ? 8 : 4;  // heads: of a slot of the split kernel
+    auto own_row = [&](int i) { return ((int64_t)(b * P.hkv + kvh) + a0 + i) * heads + hg; };
     pdl_wait_primary();  // both kernels' partials are complete
-    float M = -INFINITY, L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    RowSum sum;
     for (int i0 = part; i0 < items; i0 += 32 * share) {
         const int mine = i0 + lane * share;
         float2 e = make_float2(-INFINITY, 0.f);
         if (mine < items) {
-            const int64_t cc = a0 + (mine - np);
+            const int64_t cc = a0 + (mine - pre.n);
             // (a CTA of the split kernel without pages wrote nothing)
-            if (mine < np || T >= AC || (cc * T + AC - 1) / AC < ((cc + 1) * T + AC - 1) / AC)
-                e = *reinterpret_cast<const float2 *>((mine < np ? P.part_ml : A.part_ml) + row_of(mine) * 2);
+            if (mine < pre.n)
+                e = *reinterpret_cast<const float2 *>(P.part_ml + pre.row(mine) * 2);
+            else if (T >= AC || (cc * T + AC - 1) / AC < ((cc + 1) * T + AC - 1) / AC)
+                e = *reinterpret_cast<const float2 *>(A.part_ml + own_row(mine - pre.n) * 2);
         }
-        float top = e.x;
-#pragma unroll
-        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        top = fmaxf(top, M);
-        const float f = M == -INFINITY ? 0.f : exp2f(M - top);
-        const bool none = e.x == -INFINITY;  // a partial without tokens has no output
-        const float w = none ? 0.f : exp2f(e.x - top);
-        float sum = none ? 0.f : w * e.y;
-#pragma unroll
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const uint32_t have = __ballot_sync(0xffffffffu, !none);
-        L = L * f + sum;
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-        M = top;
-        const int n = min(32, (items - i0 + share - 1) / share);
-        for (int k0 = 0; k0 < n; k0 += 8) {  // eight loads in flight
-            float4 x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int i = i0 + (k0 + k) * share;
-                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (have >> (k0 + k) & 1)
-                    x[k] = reinterpret_cast<const float4 *>((i < np ? P.part_o : A.part_o) + row_of(i) * kDim)[lane];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
-                o.x += wk * x[k].x;
-                o.y += wk * x[k].y;
-                o.z += wk * x[k].z;
-                o.w += wk * x[k].w;
-            }
-        }
+        sum.add(e.x, e.y, min(32, (items - i0 + share - 1) / share), [&](int k) {
+            const int i = i0 + k * share;
+            const float *o = i < pre.n ? P.part_o + pre.row(i) * kDim : A.part_o + own_row(i - pre.n) * kDim;
+            return reinterpret_cast<const float4 *>(o)[lane];
+        });
     }
     if (share > 1) {
-        acc[warp][lane] = o;
-        if (lane == 0) wml[warp] = make_float2(M, L);
+        acc[warp][lane] = sum.o;
+        if (lane == 0) wml[warp] = make_float2(sum.m, sum.l);
         __syncthreads();
         if (part > 0) return;
-        for (int k = 1; k < share; ++k) M = fmaxf(M, wml[warp + k].x);
-        const float f0 = wml[warp].x == -INFINITY ? 0.f : exp2f(wml[warp].x - M);
-        L *= f0;
-        o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
-        for (int k = 1; k < share; ++k) {
-            const float2 e = wml[warp + k];
-            const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - M);
-            const float4 x = acc[warp + k][lane];
-            L += f * e.y;
-            o.x += f * x.x;
-            o.y += f * x.y;
-            o.z += f * x.z;
-            o.w += f * x.w;
-        }
+        for (int k = 1; k < share; ++k) sum.add(wml[warp + k].x, wml[warp + k].y, acc[warp + k][lane]);
     }
-    if (hg >= P.G) return;
-    const float k = L == 0.f ? 0.f : 1.f / L;  // no token: zero
-    const float4 y = make_float4(o.x * k, o.y * k, o.z * k, o.w * k);
-    const int64_t at = ((int64_t)blockIdx.x * P.G + hg) * kDim + 4 * lane;
-    if (P.out_bf16)
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) =
-            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-    else
-        *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + at) = y;
+    if (hg < P.G) sum.store(P, (int64_t)blockIdx.x * P.G + hg, lane);
 }
 
 // ---------------------------------------------------------------------------------
@@ -1024,7 +911,8 @@ static cudaError_t launch_prefix_impl(const PrefixParams &P, const CUtensorMap &
 cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_map, const AttnParams &A,
                           const void *own_map, cudaStream_t stream)
 {
-    if (P.num_groups > 0 && P.grid > 0) {
+    const bool after = P.num_groups > 0 && P.grid > 0;
+    if (after) {
         CUtensorMap map;
         memcpy(&map, prefix_map, sizeof map);
         cudaError_t e;
@@ -1034,6 +922,7 @@ cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_
             e = P.unit_rows == 256 ? launch_prefix_impl<kFmtZf, 2>(P, map, stream) : launch_prefix_impl<kFmtZf, 1>(P, map, stream);
         if (e != cudaSuccess) return e;
     }
+    if (A.grid == 0) return launch_own(A, P, format, own_map, after, stream);
     cudaError_t e = launch_attention_partials(A, format, own_map, stream);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];

@@ -62,6 +62,20 @@ def test_group_sizes(kind, n):
 
 
 @pytest.mark.parametrize("kind", BOTH)
+@pytest.mark.parametrize("G", [1, 2, 4, 7])
+@pytest.mark.parametrize("top", [1023, 1024, 1040, 2100])
+def test_long_own_tokens(kind, G, top):
+    """Own tokens on both sides of where they are split over CTAs, ragged, with empty ones."""
+    own = own_lens(9, top, G)
+    own[2], own[5], own[8] = top, 0, 1
+    c = PrefixCase([(3, 200), (4, 0), (1, 31)], own, 2 * G, 2, seed=top + G)
+    ref = c.reference()
+    c.check(run(c, kind), ref)
+    c.check(run(c, kind, dtype=torch.bfloat16), ref)
+    assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("kind", BOTH)
 @pytest.mark.parametrize("groups", [[(3, 400), (1, 17), (9, 1300), (2, 128)], [(70, 300), (2, 900), (40, 1)],
                                     [(4, 0), (0, 500), (5, 260), (0, 0)], [(1, 50)] * 40])
 def test_groups_of_different_sizes(kind, groups):

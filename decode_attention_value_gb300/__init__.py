@@ -163,17 +163,43 @@ def _ptr(t: torch.Tensor | None, dtype=None, name: str = "") -> int | None:
     return t.data_ptr()
 
 
-def _ptr_on(t: torch.Tensor, dtype, name: str, dev: int) -> int:
-    """_ptr for a tensor that has to be on CUDA device dev."""
-    p = _ptr(t, dtype, name)
+def _refuse(t: torch.Tensor, dtypes, name: str, dev: int):
+    """What is wrong with a tensor that _ptr_on does not take."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on CUDA device {dev}, got {t.device}")
-    return p
+    if dtypes and t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {dtypes[0]}, got {t.dtype}")
+    raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _ptr_on(t: torch.Tensor, dtypes, name: str, dev: int) -> int:
+    """_ptr for a tensor that has to be on CUDA device dev (a few hundred nanoseconds: the
+    calls that take many tensors are launched once a layer)."""
+    if (dtypes and t.dtype not in dtypes) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtypes, name, dev)
+    return t.data_ptr()
+
+
+# torch.cuda.current_stream() and current_device() build objects (3 us a call on the GB300's host);
+# these return the numbers they wrap
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int | None:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(_current_device())
+
+
+def _device_of(status: torch.Tensor) -> int:
+    """The device of a call: its status tensor's, which has to be the current one."""
+    dev = status.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"status: expected a tensor on the current CUDA device, got {status.device}")
+    return dev
 
 
 def _check(fn: str, rc: int):
@@ -185,6 +211,10 @@ _U64 = (torch.uint64, torch.int64) if hasattr(torch, "uint64") else (torch.int64
 _U32 = (torch.int32,) + ((torch.uint32,) if hasattr(torch, "uint32") else ())
 _U8 = (torch.uint8,)
 _BF16 = (torch.bfloat16, torch.int16)
+_BF16_ONLY = (torch.bfloat16,)
+_I32 = (torch.int32,)
+_I64 = (torch.int64,)
+_OUT_TYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 
 
 def _pages_of(pool: torch.Tensor) -> int:
@@ -323,32 +353,34 @@ def prefix_attention_workspace_size(hkv: int, batch: int, num_q_heads: int, grou
 def _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens, out, status, workspace, stream):
     """Checks shared by the two prefix attention calls: (device, batch, query heads, groups,
     prefix columns, own columns, output type, workspace)."""
-    dev = status.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"status: expected a tensor on the current CUDA device, got {status.device}")
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
-        raise ValueError(f"q: expected [batch][heads][{HEAD_DIM}], got {tuple(q.shape)}")
-    B, hq = q.shape[0], q.shape[1]
-    n = prefix_lens.numel()
-    if prefix_lens.dim() != 1 or group_start.shape != (n + 1,):
+    dev = _device_of(status)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != HEAD_DIM:
+        raise ValueError(f"q: expected [batch][heads][{HEAD_DIM}], got {tuple(shape)}")
+    B, hq, _ = shape
+    if prefix_lens.dim() != 1:
+        raise ValueError(f"prefix_lens: expected [groups], got {tuple(prefix_lens.shape)}")
+    n = prefix_lens.shape[0]
+    if group_start.shape != (n + 1,):
         raise ValueError(f"group_start: expected [{n + 1}] for {n} groups, got {tuple(group_start.shape)}")
-    if prefix_ids.dim() != 2 or prefix_ids.shape[0] != n:
-        raise ValueError(f"prefix_ids: expected [{n}][pages], got {tuple(prefix_ids.shape)}")
-    if page_ids.dim() != 2 or page_ids.shape[0] != B:
-        raise ValueError(f"page_ids: expected [{B}][pages], got {tuple(page_ids.shape)}")
+    pre, own = prefix_ids.shape, page_ids.shape
+    if len(pre) != 2 or pre[0] != n:
+        raise ValueError(f"prefix_ids: expected [{n}][pages], got {tuple(pre)}")
+    if len(own) != 2 or own[0] != B:
+        raise ValueError(f"page_ids: expected [{B}][pages], got {tuple(own)}")
     if seq_lens.shape != (B,):
         raise ValueError(f"seq_lens: expected [{B}], got {tuple(seq_lens.shape)}")
-    if out.shape != q.shape:
-        raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
-    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+    if out.shape != shape:
+        raise ValueError(f"out: expected {tuple(shape)}, got {tuple(out.shape)}")
+    kind = _OUT_TYPES.get(out.dtype)
+    if kind is None:
         raise ValueError(f"out: expected torch.float32 or torch.bfloat16, got {out.dtype}")
     if workspace is None:
-        workspace = torch.empty(prefix_attention_workspace_size(hkv, B, hq, n, prefix_ids.shape[1], page_ids.shape[1]),
-                                dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(prefix_attention_workspace_size(hkv, B, hq, n, pre[1], own[1]), dtype=torch.uint8,
+                                device=q.device)
         if stream is not None:
             workspace.record_stream(stream)
-    return dev, B, hq, n, prefix_ids.shape[1], page_ids.shape[1], OUT_BF16 if out.dtype is torch.bfloat16 else OUT_F32, \
-        workspace
+    return dev, B, hq, n, pre[1], own[1], kind, workspace
 
 
 def prefix_attention(q, group_start, prefix_ids, prefix_lens, prefix_tail, page_ids, seq_lens, tail_page, meta, arena,
@@ -363,16 +395,15 @@ def prefix_attention(q, group_start, prefix_ids, prefix_lens, prefix_tail, page_
                                                         out, status, workspace, stream)
     if prefix_tail.shape != (n,) or tail_page.shape != (B,):
         raise ValueError(f"prefix_tail, tail_page: expected [{n}] and [{B}]")
-    if tuple(meta.shape[1:]) != (hkv, 2) or tuple(raw_pool.shape[1:]) != (hkv, 2, PAGE, HEAD_DIM):
+    if meta.shape[1:] != (hkv, 2) or raw_pool.shape[1:] != (hkv, 2, PAGE, HEAD_DIM):
         raise ValueError(f"meta, raw_pool: expected [pages][{hkv}][2] and [pages][{hkv}][2][{PAGE}][{HEAD_DIM}]")
-    i32 = torch.int32
     _check("kvz_prefix_attention", _lib.kvz_prefix_attention(
-        _dims(hkv), B, hq, _ptr_on(q, torch.bfloat16, "q", dev), n, _ptr_on(group_start, i32, "group_start", dev),
-        _ptr_on(prefix_ids, i32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, i32, "prefix_lens", dev),
-        _ptr_on(prefix_tail, i32, "prefix_tail", dev), _ptr_on(page_ids, i32, "page_ids", dev), op,
-        _ptr_on(seq_lens, i32, "seq_lens", dev), _ptr_on(tail_page, i32, "tail_page", dev),
+        _dims(hkv), B, hq, _ptr_on(q, _BF16_ONLY, "q", dev), n, _ptr_on(group_start, _I32, "group_start", dev),
+        _ptr_on(prefix_ids, _I32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, _I32, "prefix_lens", dev),
+        _ptr_on(prefix_tail, _I32, "prefix_tail", dev), _ptr_on(page_ids, _I32, "page_ids", dev), op,
+        _ptr_on(seq_lens, _I32, "seq_lens", dev), _ptr_on(tail_page, _I32, "tail_page", dev),
         _ptr_on(meta, _U64, "meta", dev), meta.shape[0], _ptr_on(arena, _U8, "arena", dev), arena.numel(),
-        _ptr_on(raw_pool, torch.bfloat16, "raw_pool", dev), raw_pool.shape[0], _ptr_on(out, None, "out", dev), ot,
+        _ptr_on(raw_pool, _BF16_ONLY, "raw_pool", dev), raw_pool.shape[0], _ptr_on(out, None, "out", dev), ot,
         _ptr_on(workspace, _U8, "workspace", dev), workspace.numel(), _ptr_on(status, _U32, "status", dev),
         _stream(stream)))
 
@@ -381,17 +412,17 @@ def prefix_attention_raw(q, group_start, prefix_ids, prefix_lens, page_ids, seq_
                          workspace=None, stream=None):
     """prefix_attention over plain BF16 pages: prefix_ids and page_ids name raw pages and
     cover the last, partial ones."""
-    hkv = raw_pool.shape[1]
+    pool = raw_pool.shape
+    hkv = pool[1]
     dev, B, hq, n, pp, op, ot, workspace = _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens,
                                                         out, status, workspace, stream)
-    if tuple(raw_pool.shape[1:]) != (hkv, 2, PAGE, HEAD_DIM):
-        raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(raw_pool.shape)}")
-    i32 = torch.int32
+    if pool[1:] != (hkv, 2, PAGE, HEAD_DIM):
+        raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(pool)}")
     _check("kvz_prefix_attention_raw", _lib.kvz_prefix_attention_raw(
-        _dims(hkv), B, hq, _ptr_on(q, torch.bfloat16, "q", dev), n, _ptr_on(group_start, i32, "group_start", dev),
-        _ptr_on(prefix_ids, i32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, i32, "prefix_lens", dev),
-        _ptr_on(page_ids, i32, "page_ids", dev), op, _ptr_on(seq_lens, i32, "seq_lens", dev),
-        _ptr_on(raw_pool, torch.bfloat16, "raw_pool", dev), raw_pool.shape[0], _ptr_on(out, None, "out", dev), ot,
+        _dims(hkv), B, hq, _ptr_on(q, _BF16_ONLY, "q", dev), n, _ptr_on(group_start, _I32, "group_start", dev),
+        _ptr_on(prefix_ids, _I32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, _I32, "prefix_lens", dev),
+        _ptr_on(page_ids, _I32, "page_ids", dev), op, _ptr_on(seq_lens, _I32, "seq_lens", dev),
+        _ptr_on(raw_pool, _BF16_ONLY, "raw_pool", dev), pool[0], _ptr_on(out, None, "out", dev), ot,
         _ptr_on(workspace, _U8, "workspace", dev), workspace.numel(), _ptr_on(status, _U32, "status", dev),
         _stream(stream)))
 
@@ -414,20 +445,20 @@ def rope_table(inv_freq: torch.Tensor, axis: torch.Tensor | None = None) -> torc
     return torch.stack([turns, axis], 1)
 
 
-def _heads(t: torch.Tensor, name: str, tokens: int, heads: int | None, dev: int):
-    """Pointer, token stride and head stride of a BF16 [tokens][heads][128] tensor whose
-    heads are contiguous."""
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != HEAD_DIM or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name}: expected [{tokens}][{heads or 'heads'}][{HEAD_DIM}], got {tuple(t.shape)}")
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: expected a tensor on CUDA device {dev}, got {t.device}")
+def _heads(t: torch.Tensor, name: str, tokens: int, dev: int):
+    """(heads, pointer, token stride, head stride) of a BF16 [tokens][heads][128] tensor
+    whose heads are contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name}: expected [{tokens}][heads][{HEAD_DIM}], got {tuple(shape)}")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        _refuse(t, _BF16_ONLY, name, dev)
     ts, hs, es = t.stride()
     if es != 1:
         raise ValueError(f"{name}: expected contiguous heads")
+    heads = shape[1]
     # a stride nothing steps by may be any number
-    return t.data_ptr(), ts if tokens > 1 else 0, hs if t.shape[1] > 1 else 0
+    return heads, t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0
 
 
 def append_tokens(k, v, slots, raw_pool, status, q=None, q_out=None, rope=None, positions=None,
@@ -438,52 +469,59 @@ def append_tokens(k, v, slots, raw_pool, status, q=None, q_out=None, rope=None, 
     rope_table) at positions (int32 [T] or [axes][T]).  q [T][Hq][128], when given, is
     rotated into q_out (allocated when None; may be q).  k, v, slots and raw_pool may all
     be None to rotate queries alone.  Returns q_out."""
-    dev = status.get_device()
-    first = q if k is None else k
-    if first is None:
-        raise ValueError("append_tokens: no tokens (k and q are both None)")
-    if (k is None) != (v is None) or (k is None) != (slots is None) or (k is None) != (raw_pool is None):
-        raise ValueError("append_tokens: k, v, slots and raw_pool go together")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"status: expected a tensor on the current CUDA device, got {status.device}")
-    T = first.shape[0]
-    hq = hkv = 0
-    qa = ka = va = (None, 0, 0)
-    pool = pages = sl = qo = None
+    dev = _device_of(status)
     if k is not None:
-        hkv = k.shape[1] if k.dim() == 3 else 0
-        ka, va = _heads(k, "k", T, hkv, dev), _heads(v, "v", T, hkv, dev)
-        if raw_pool.dim() != 5 or tuple(raw_pool.shape[1:]) != (hkv, 2, PAGE, HEAD_DIM):
-            raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(raw_pool.shape)}")
-        pool, pages = _ptr_on(raw_pool, torch.bfloat16, "raw_pool", dev), raw_pool.shape[0]
+        if v is None or slots is None or raw_pool is None:
+            raise ValueError("append_tokens: k, v, slots and raw_pool go together")
+        T = k.shape[0]
+        hkv, kp, kt, kh = _heads(k, "k", T, dev)
+        hv, vp, vt, vh = _heads(v, "v", T, dev)
+        pool = raw_pool.shape
+        if hv != hkv:
+            raise ValueError(f"v: expected {hkv} heads, got {hv}")
+        if pool[1:] != (hkv, 2, PAGE, HEAD_DIM):
+            raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(pool)}")
         if slots.shape != (T,):
             raise ValueError(f"slots: expected [{T}], got {tuple(slots.shape)}")
-        sl = _ptr_on(slots, torch.int32, "slots", dev)
+        pages, pool, sl = pool[0], _ptr_on(raw_pool, _BF16_ONLY, "raw_pool", dev), _ptr_on(slots, _I32, "slots", dev)
+    else:
+        if v is not None or slots is not None or raw_pool is not None:
+            raise ValueError("append_tokens: k, v, slots and raw_pool go together")
+        if q is None:
+            raise ValueError("append_tokens: no tokens (k and q are both None)")
+        T, hkv, pages = q.shape[0], 1, 0
+        kp = vp = pool = sl = None
+        kt = kh = vt = vh = 0
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        qa = _heads(q, "q", T, hq, dev)
+        hq, qp, qt, qh = _heads(q, "q", T, dev)
         if q_out is None:
             q_out = torch.empty((T, hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
         elif q_out.shape != q.shape:
             raise ValueError(f"q_out: expected {tuple(q.shape)}, got {tuple(q_out.shape)}")
-        qo = _ptr_on(q_out, torch.bfloat16, "q_out", dev)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rot = axes = 0
-    rp = pp = None
+        qo = _ptr_on(q_out, _BF16_ONLY, "q_out", dev)
+    else:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        hq = qt = qh = 0
+        qp = qo = None
     if rope is not None:
-        if rope.dim() != 2 or rope.shape[1] != 2:
-            raise ValueError(f"rope: expected a rope_table, got {tuple(rope.shape)}")
+        table = rope.shape
+        if len(table) != 2 or table[1] != 2:
+            raise ValueError(f"rope: expected a rope_table, got {tuple(table)}")
         if positions is None:
             raise ValueError("rope without positions")
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.shape[-1] != T or positions.dim() not in (1, 2):
-            raise ValueError(f"positions: expected [{T}] or [axes][{T}], got {tuple(positions.shape)}")
-        rot, rp = 2 * rope.shape[0], _ptr_on(rope, torch.int64, "rope", dev)
-        pp = _ptr_on(positions, torch.int32, "positions", dev)
+        at = positions.shape
+        if len(at) not in (1, 2) or at[-1] != T:
+            raise ValueError(f"positions: expected [{T}] or [axes][{T}], got {tuple(at)}")
+        axes = 1 if len(at) == 1 else at[0]
+        rot, rp, pp = 2 * table[0], _ptr_on(rope, _I64, "rope", dev), _ptr_on(positions, _I32, "positions", dev)
+    else:
+        axes = rot = 0
+        rp = pp = None
     _check("kvz_append_tokens", _lib.kvz_append_tokens(
-        _dims(max(hkv, 1)), T, hq, *qa, *ka, *va, sl, pp, axes, rp, rot, ROPE_INTERLEAVED if interleaved else 0,
-        rope_scale, qo, pool, pages or 0, _ptr_on(status, _U32, "status", dev), _stream(stream)))
+        _dims(hkv), T, hq, qp, qt, qh, kp, kt, kh, vp, vt, vh, sl, pp, axes, rp, rot,
+        ROPE_INTERLEAVED if interleaved else 0, rope_scale, qo, pool, pages, _ptr_on(status, _U32, "status", dev),
+        _stream(stream)))
     return q_out
 
 

@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
     const int share = G == 1 ? 4 : G == 2 ? 2 : 1;  // warps of a head
     const int part = warp % share;
     const PfxPlace where = pfx_place(P, b, lane);
+    PfxItems pre = pfx_items(P, where, b, kvh, min(warp / share, G - 1));
     if (after) pdl_wait_primary();  // the prefix partials are complete
     for (int h0 = 0; h0 < G; h0 += kOwnWarps / share) {  // (uniform: the barrier below)
         const int h = h0 + warp / share;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
             if (part == 0)
                 for (int w = 0; w < kOwnWarps; ++w)
                     sum.add(wml[w][h].x, wml[w][h].y, *reinterpret_cast<const float4 *>(states + (w * 8 + h) * kDim + 4 * lane));
-            const PfxItems pre = pfx_items(P, where, b, kvh, h);
+            if (h0 > 0) pre = pfx_items(P, where, b, kvh, h);
             for (int i0 = part; i0 < pre.n; i0 += 32 * share) {
                 const int i = i0 + lane * share;
                 float2 e = make_float2(-INFINITY, 0.f);

@@ -296,7 +296,7 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     P.out_bf16 = out_type == KVZ_OUT_BF16;
     P.status = status;
     P.scale_log2 = A.scale_log2;
-    cudaError_t e = launch_prefix(P, F.format, &pmap, A, &map, stream);
+    cudaError_t e = launch_prefix(P, F.format, &pmap, A, &map, sm_count(), stream);
     return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
 }
 

@@ -163,10 +163,10 @@ inline size_t pfx_part_rows(int64_t units, int grid) { return grid > 0 ? (size_t
 // merges the prefix partials too (own.cu); longer ones are split over CTAs (A.grid > 0).
 constexpr int kOwnPages = 64;
 cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, const void *map, bool after_prefix,
-                       cudaStream_t stream);
+                       int sms, cudaStream_t stream);
 // prefix_map: tensor map of the raw pool with one page's 16 K or V rows x 64 columns a box
 cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_map, const AttnParams &A,
-                          const void *own_map, cudaStream_t stream);
+                          const void *own_map, int sms, cudaStream_t stream);
 
 cudaError_t launch_encode(const EncodeParams &P, cudaStream_t stream);
 cudaError_t launch_enc_prepare(const EncodeParams &P, cudaStream_t stream);

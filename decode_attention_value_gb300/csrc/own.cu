@@ -7,10 +7,15 @@
 // with 0..200 own tokens took 56 us behind the prefix kernel, 52 MB of pages at 8 us.  Here the
 // partials never leave the block.
 //
-// A warp takes every fourth page, two in flight in its own shared-memory stages, and runs the
+// A warp takes every fourth page, one to four in flight in its own shared-memory stages, and runs the
 // m16n8k16 products of attention.cu on it: S^T = K Q^T with the query heads in the columns, a
-// running softmax, O^T += V^T P^T with P as two BF16 parts.  The block's warps leave their states
-// in shared memory; then each head's warp adds the states and the prefix partials, in order.
+// running softmax, O^T += V^T P^T with P as two BF16 parts (three for fp32 outputs).  The block's
+// warps leave their states in shared memory; then each head's warp adds the states and the prefix
+// partials, in order.
+//
+// Bound: the latency of a block's dependent reads (lengths and page ids, pages, partials), so those
+// of a kind are issued together, and as many blocks as fit run at once: with few blocks a warp has
+// up to four pages in flight, with many one (kOwnStages).
 #include <cuda.h>
 
 #include <cstring>
@@ -20,14 +25,17 @@
 
 namespace kvz {
 
-constexpr int kOwnWarps = 4, kOwnThreads = kOwnWarps * 32, kOwnStages = 2;
+constexpr int kOwnWarps = 4, kOwnThreads = kOwnWarps * 32;
 constexpr int kOwnPageBytes = 2 * kPage * kDim * 2;
-constexpr int kOwnRing = kOwnWarps * kOwnStages * kOwnPageBytes;  // 64 KB; holds the warps' states afterwards
-constexpr int kOwnSmem = kOwnRing + kOwnWarps * kOwnStages * 8;
+constexpr int kOwnResident = 6;  // blocks an SM holds with one stage a warp
+// The warps' stages, which hold their states afterwards, and a barrier each.
+__host__ __device__ constexpr int own_ring(int stages) { return kOwnWarps * stages * kOwnPageBytes; }
+__host__ __device__ constexpr int own_smem(int stages) { return own_ring(stages) + kOwnWarps * stages * 8; }
+static_assert(kOwnPages + 1 <= 32 * kOwnWarps, "a lane resolves one page");
 
-template <int kFmt, bool kG8>
-__global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, const PrefixParams P, const int after,
-                                                        const __grid_constant__ CUtensorMap tmap)
+template <int kFmt, bool kG8, bool kThird>
+__global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnParams A, const PrefixParams P, const int after,
+                                                                   const int log_stages, const __grid_constant__ CUtensorMap tmap)
 {
     constexpr bool kCoded = kFmt != kFmtRaw;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -39,44 +47,37 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int b = blockIdx.x / A.hkv, kvh = blockIdx.x % A.hkv, G = A.G;
-    const uint32_t bar0 = sbase + kOwnRing + warp * kOwnStages * 8;
+    // lane i holds the place of the warp's i-th page, page warp + 4 i
+    const int page = warp + kOwnWarps * lane;
+    int L = A.seq_lens[b];
+    int32_t id = page < A.max_pages ? A.page_ids[(int64_t)b * A.max_pages + page] : -1;
+    const int32_t tail = kCoded ? A.tail_page[b] : 0;
+    const int stages = 1 << log_stages;
+    const uint32_t ring = sbase + warp * stages * kOwnPageBytes, bar0 = sbase + own_ring(stages) + warp * stages * 8;
     if (lane == 0) {  // a warp's barriers are its own
-        for (int s = 0; s < kOwnStages; ++s) mbar_init(bar0 + 8 * s, 1);
+        for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8 * s, 1);
         fence_barrier_init();
     }
     __syncwarp();
-    const int L = A.seq_lens[b], n = L > 0 ? (L + kPage - 1) / kPage : 0;
-    if (L < 0 && tid == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
+    // tokens that the table cannot name are left out (12-bit: whole pages; the tail has its own id)
+    const int most = A.max_pages * kPage + (kCoded ? kPage - 1 : 0);
+    if ((L < 0 || L > most) && tid == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
+    L = L < 0 ? 0 : L <= most ? L : A.max_pages * kPage + (kCoded ? L % kPage : 0);
+    const int n = (L + kPage - 1) / kPage;
     const int mine = (n - warp + kOwnWarps - 1) / kOwnWarps;  // pages warp, warp + 4, ...
 
-    // queries: B operand of QK^T, column = head (n % 4 when G <= 4)
-    uint32_t qf[8][2];
-    const int qhead = kG8 ? g : (g & 3);
-    const bool qhas = qhead < G;
-    const uint32_t *qg = reinterpret_cast<const uint32_t *>(
-        A.q + ((int64_t)b * A.hkv * G + (int64_t)kvh * G + (qhas ? qhead : 0)) * kDim);
-#pragma unroll
-    for (int kt = 0; kt < 8; ++kt) {
-        qf[kt][0] = qhas ? __ldg(qg + 8 * kt + t) : 0u;
-        qf[kt][1] = qhas ? __ldg(qg + 8 * kt + t + 4) : 0u;
-    }
     float o[8][4];
 #pragma unroll
     for (int a = 0; a < 8; ++a) o[a][0] = o[a][1] = o[a][2] = o[a][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    // lane i % 32 resolves the warp's i-th page, 32 at a time
     enum : uint32_t { kSkip = 0, kPair = 1, kPlain = 2 };
     uint32_t kind = kSkip, tk = 0, tv = 0;
     const uint8_t *srck = nullptr, *srcv = nullptr;
     int row = 0;
-    auto resolve = [&](int i0) {
-        kind = kSkip;
-        const int p = warp + kOwnWarps * (i0 + lane);
-        if (p >= n) return;
+    if (page < n) {
         uint32_t flag = 0;
-        if (kCoded && p < L / kPage) {
-            const int32_t id = p < A.max_pages ? A.page_ids[(int64_t)b * A.max_pages + p] : INT32_MIN;
+        if (kCoded && page < L / kPage) {
             if (id < 0 || id >= A.num_meta_pages) {
                 flag = KVZ_STATUS_BAD_INDEX;
             } else {
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
                 srcv = A.arena + (uint64_t)ofv * kGranule;
             }
         } else {
-            const int32_t id = kCoded ? A.tail_page[b] : p < A.max_pages ? A.page_ids[(int64_t)b * A.max_pages + p] : INT32_MIN;
+            if (kCoded) id = tail;
             if (id < 0 || id >= A.num_raw_pages) {
                 flag = kCoded && id == -1 ? KVZ_STATUS_BAD_TAIL : KVZ_STATUS_BAD_INDEX;
             } else {
@@ -104,11 +105,10 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
             }
         }
         if (flag) atomicOr(A.status, flag);
-    };
+    }
     auto issue = [&](int i) {  // the warp's i-th page into its stage
-        if (lane != (i & 31)) return;
-        const uint32_t bar = bar0 + 8 * (i % kOwnStages);
-        const uint32_t dst = sbase + (warp * kOwnStages + i % kOwnStages) * kOwnPageBytes;
+        if (lane != i) return;
+        const uint32_t bar = bar0 + 8 * (i & (stages - 1)), dst = ring + (i & (stages - 1)) * kOwnPageBytes;
         if (kind == kPair) {
             const uint32_t bk = group_granules(tk) * kGranule, bv = group_granules(tv) * kGranule;
             mbar_arrive_expect_tx(bar, bk + bv);
@@ -122,107 +122,124 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
             mbar_arrive(bar);
         }
     };
+    for (int i = 0; i < stages && i < mine; ++i) issue(i);
+
+    // ---- while the pages come: the queries, and where the prefix's partials are ----
+    // B operand of QK^T, column = head (n % 4 when G <= 4)
+    uint32_t qf[8][2];
+    const int qhead = kG8 ? g : (g & 3);
+    const bool qhas = qhead < G;
+    const uint32_t *qg = reinterpret_cast<const uint32_t *>(
+        A.q + ((int64_t)b * A.hkv * G + (int64_t)kvh * G + (qhas ? qhead : 0)) * kDim);
+#pragma unroll
+    for (int kt = 0; kt < 8; ++kt) {
+        qf[kt][0] = qhas ? __ldg(qg + 8 * kt + t) : 0u;
+        qf[kt][1] = qhas ? __ldg(qg + 8 * kt + t + 4) : 0u;
+    }
+    const PfxPlace where = pfx_place(P, b, lane);
+
     bool ok = true;
-    for (int i0 = 0; i0 < mine && ok; i0 += 32) {
-        const int cnt = min(32, mine - i0);
-        resolve(i0);
-        for (int i = 0; i < kOwnStages && i < cnt; ++i) issue(i0 + i);
-        for (int i = i0; i < i0 + cnt && ok; ++i) {
-            const int s = i % kOwnStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * s, (i / kOwnStages) & 1, A.status));
-            const uint32_t what = __shfl_sync(0xffffffffu, kind, i & 31);
-            if (ok && what != kSkip) {
-                const uint8_t *st = smem + (warp * kOwnStages + s) * kOwnPageBytes;
-                const uint32_t sta = sbase + (warp * kOwnStages + s) * kOwnPageBytes;
-                const uint32_t tagk = __shfl_sync(0xffffffffu, tk, i & 31), tagv = __shfl_sync(0xffffffffu, tv, i & 31);
-                const int valid = min(kPage, L - (warp + kOwnWarps * i) * kPage);
-                // ---- S^T = K Q^T over the page's 16 tokens ----
-                float sc[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t off = 0;
+    for (int i = 0; i < mine && ok; ++i) {
+        const int s = i & (stages - 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * s, (i >> log_stages) & 1, A.status));
+        const uint32_t what = __shfl_sync(0xffffffffu, kind, i);
+        if (ok && what != kSkip) {
+            const uint32_t sta = ring + s * kOwnPageBytes;
+            const uint8_t *st = smem + (sta - sbase);
+            const uint32_t tagk = __shfl_sync(0xffffffffu, tk, i), tagv = __shfl_sync(0xffffffffu, tv, i);
+            const int valid = min(kPage, L - (warp + kOwnWarps * i) * kPage);
+            // ---- S^T = K Q^T over the page's 16 tokens ----
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t off = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t a0[4], a1[4];
-                    if (kCoded && what == kPair) {
-                        const uint32_t tag = (tagk >> (8 * j)) & 0xFFu;
-                        block_frags(st + off, tag, lane, a0, a1);
-                        off += tag_granules(tag) * kGranule;
-                    } else {
-                        raw_k_frag(sta, j, 0, lane, a0);
-                        raw_k_frag(sta, j, 1, lane, a1);
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a0[4], a1[4];
+                if (kCoded && what == kPair) {
+                    const uint32_t tag = (tagk >> (8 * j)) & 0xFFu;
+                    block_frags(st + off, tag, lane, a0, a1);
+                    off += tag_granules(tag) * kGranule;
+                } else {
+                    raw_k_frag(sta, j, 0, lane, a0);
+                    raw_k_frag(sta, j, 1, lane, a1);
+                }
+                mma_bf16_16816(sc, a0, qf[2 * j][0], qf[2 * j][1]);
+                mma_bf16_16816(sc, a1, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[e] *= A.scale_log2;
+            if (valid < kPage) {
+                if (g >= valid) sc[0] = sc[1] = -INFINITY;
+                if (g + 8 >= valid) sc[2] = sc[3] = -INFINITY;
+            }
+            // ---- running softmax (a column's 16 tokens: lanes with equal t) ----
+            float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+            }
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+                const float f0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0), f1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
+#pragma unroll
+                for (int a = 0; a < 8; ++a) {
+                    o[a][0] *= f0;
+                    o[a][2] *= f0;
+                    o[a][1] *= f1;
+                    o[a][3] *= f1;
+                }
+                l0 *= f0;
+                l1 *= f1;
+                m0 = n0;
+                m1 = n1;
+            }
+            const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+            const float p0 = exp2f(sc[0] - u0), p1 = exp2f(sc[1] - u1), p2 = exp2f(sc[2] - u0), p3 = exp2f(sc[3] - u1);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            // P as high and low BF16 parts: for G <= 4 in columns h and h + 4 of one product, else
+            // in two products; a product for the third part (columns h)
+            const float r0 = p0 - bf16_round(p0), r1 = p1 - bf16_round(p1);
+            const float r2 = p2 - bf16_round(p2), r3 = p3 - bf16_round(p3);
+            const bool low = !kG8 && t >= 2;
+            const uint32_t pb0 = movmatrix_trans(low ? pack_bf16x2(r0, r1) : pack_bf16x2(p0, p1));
+            const uint32_t pb1 = movmatrix_trans(low ? pack_bf16x2(r2, r3) : pack_bf16x2(p2, p3));
+            uint32_t pl0 = 0, pl1 = 0;
+            if (kG8) {
+                pl0 = movmatrix_trans(pack_bf16x2(r0, r1));
+                pl1 = movmatrix_trans(pack_bf16x2(r2, r3));
+            }
+            uint32_t pt0 = 0, pt1 = 0;
+            if (kThird) {
+                pt0 = movmatrix_trans(low ? 0u : pack_bf16x2(r0 - bf16_round(r0), r1 - bf16_round(r1)));
+                pt1 = movmatrix_trans(low ? 0u : pack_bf16x2(r2 - bf16_round(r2), r3 - bf16_round(r3)));
+            }
+            // ---- O^T += V^T P^T ----
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a[2][4];
+                if (kCoded && what == kPair) {
+                    const uint32_t tag = (tagv >> (8 * j)) & 0xFFu;
+                    block_frags(st + off, tag, lane, a[0], a[1]);  // V right after K
+                    off += tag_granules(tag) * kGranule;
+                } else {
+                    raw_v_frag(sta, j, 0, lane, a[0]);
+                    raw_v_frag(sta, j, 1, lane, a[1]);
+                    if (valid < kPage) {
+                        mask_v_frag(a[0], lane, valid);
+                        mask_v_frag(a[1], lane, valid);
                     }
-                    mma_bf16_16816(sc, a0, qf[2 * j][0], qf[2 * j][1]);
-                    mma_bf16_16816(sc, a1, qf[2 * j + 1][0], qf[2 * j + 1][1]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[e] *= A.scale_log2;
-                if (valid < kPage) {
-                    if (g >= valid) sc[0] = sc[1] = -INFINITY;
-                    if (g + 8 >= valid) sc[2] = sc[3] = -INFINITY;
-                }
-                // ---- running softmax (a column's 16 tokens: lanes with equal t) ----
-                float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-                }
-                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-                if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
-                    const float f0 = n0 == -INFINITY ? 1.f : exp2f(m0 - n0), f1 = n1 == -INFINITY ? 1.f : exp2f(m1 - n1);
-#pragma unroll
-                    for (int a = 0; a < 8; ++a) {
-                        o[a][0] *= f0;
-                        o[a][2] *= f0;
-                        o[a][1] *= f1;
-                        o[a][3] *= f1;
-                    }
-                    l0 *= f0;
-                    l1 *= f1;
-                    m0 = n0;
-                    m1 = n1;
-                }
-                const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-                const float p0 = exp2f(sc[0] - u0), p1 = exp2f(sc[1] - u1), p2 = exp2f(sc[2] - u0), p3 = exp2f(sc[3] - u1);
-                l0 += p0 + p2;
-                l1 += p1 + p3;
-                // P as high and low BF16 parts: for G <= 4 in columns h and h + 4 of one product, else
-                // in two products
-                const float r0 = p0 - bf16_round(p0), r1 = p1 - bf16_round(p1);
-                const float r2 = p2 - bf16_round(p2), r3 = p3 - bf16_round(p3);
-                const bool low = !kG8 && t >= 2;
-                const uint32_t pb0 = movmatrix_trans(low ? pack_bf16x2(r0, r1) : pack_bf16x2(p0, p1));
-                const uint32_t pb1 = movmatrix_trans(low ? pack_bf16x2(r2, r3) : pack_bf16x2(p2, p3));
-                uint32_t pl0 = 0, pl1 = 0;
-                if (kG8) {
-                    pl0 = movmatrix_trans(pack_bf16x2(r0, r1));
-                    pl1 = movmatrix_trans(pack_bf16x2(r2, r3));
-                }
-                // ---- O^T += V^T P^T ----
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t a[2][4];
-                    if (kCoded && what == kPair) {
-                        const uint32_t tag = (tagv >> (8 * j)) & 0xFFu;
-                        block_frags(st + off, tag, lane, a[0], a[1]);  // V right after K
-                        off += tag_granules(tag) * kGranule;
-                    } else {
-                        raw_v_frag(sta, j, 0, lane, a[0]);
-                        raw_v_frag(sta, j, 1, lane, a[1]);
-                        if (valid < kPage) {
-                            mask_v_frag(a[0], lane, valid);
-                            mask_v_frag(a[1], lane, valid);
-                        }
-                    }
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        mma_bf16_16816(o[2 * j + f], a[f], pb0, pb1);
-                        if (kG8) mma_bf16_16816(o[2 * j + f], a[f], pl0, pl1);
-                    }
+                for (int f = 0; f < 2; ++f) {
+                    mma_bf16_16816(o[2 * j + f], a[f], pb0, pb1);
+                    if (kG8) mma_bf16_16816(o[2 * j + f], a[f], pl0, pl1);
+                    if (kThird) mma_bf16_16816(o[2 * j + f], a[f], pt0, pt1);
                 }
             }
-            __syncwarp();
-            if (ok && i + kOwnStages < i0 + cnt) issue(i + kOwnStages);
         }
+        __syncwarp();
+        if (ok && i + stages < mine) issue(i + stages);
     }
     // (after a wait that gave up, the copy it waited for may land late: microseconds)
     if (!ok) {
@@ -264,7 +281,6 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
     // ---- a head at a time: the states, then the prefix's partials ----
     const int share = G == 1 ? 4 : G == 2 ? 2 : 1;  // warps of a head
     const int part = warp % share;
-    const PfxPlace where = pfx_place(P, b, lane);
     PfxItems pre = pfx_items(P, where, b, kvh, min(warp / share, G - 1));
     if (after) pdl_wait_primary();  // the prefix partials are complete
     for (int h0 = 0; h0 < G; h0 += kOwnWarps / share) {  // (uniform: the barrier below)
@@ -299,8 +315,8 @@ __global__ void __launch_bounds__(kOwnThreads, 3) k_own(const AttnParams A, cons
     }
 }
 
-template <int kFmt, bool kG8>
-static cudaError_t launch_own_impl(const AttnParams &A, const PrefixParams &P, const void *map, bool after,
+template <int kFmt, bool kG8, bool kThird>
+static cudaError_t launch_own_impl(const AttnParams &A, const PrefixParams &P, const CUtensorMap &map, bool after, int sms,
                                    cudaStream_t stream)
 {
     // per process and device: more shared memory than the default (an attribute of the function)
@@ -308,35 +324,46 @@ static cudaError_t launch_own_impl(const AttnParams &A, const PrefixParams &P, c
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(dev < 64 && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1ull)) {
-        e = cudaFuncSetAttribute(k_own<kFmt, kG8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOwnSmem);
+        e = cudaFuncSetAttribute(k_own<kFmt, kG8, kThird>, cudaFuncAttributeMaxDynamicSharedMemorySize, own_smem(4));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_own<kFmt, kG8>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            e = cudaFuncSetAttribute(k_own<kFmt, kG8, kThird>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e == cudaSuccess && dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_ACQ_REL);
     }
     if (e != cudaSuccess) return e;
-    CUtensorMap m;
-    memcpy(&m, map, sizeof m);
+    // pages in flight: four a warp (128 KB a block) when an SM has one block, two for up to three
+    // blocks, else one
+    const int blocks = A.batch * A.hkv, log_stages = blocks <= sms ? 2 : blocks <= 3 * sms ? 1 : 0;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(A.batch * A.hkv);
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kOwnThreads);
-    cfg.dynamicSmemBytes = kOwnSmem;
+    cfg.dynamicSmemBytes = own_smem(1 << log_stages);
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_own<kFmt, kG8>, A, P, after ? 1 : 0, m);
+    return cudaLaunchKernelEx(&cfg, k_own<kFmt, kG8, kThird>, A, P, after ? 1 : 0, log_stages, map);
 }
 
-cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, const void *map, bool after_prefix,
+template <int kFmt, bool kG8>
+static cudaError_t launch_own_of(const AttnParams &A, const PrefixParams &P, const CUtensorMap &map, bool after, int sms,
+                                 cudaStream_t stream)
+{
+    return P.out_bf16 ? launch_own_impl<kFmt, kG8, false>(A, P, map, after, sms, stream)
+                      : launch_own_impl<kFmt, kG8, true>(A, P, map, after, sms, stream);
+}
+
+cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, const void *map, bool after_prefix, int sms,
                        cudaStream_t stream)
 {
+    CUtensorMap m;
+    memcpy(&m, map, sizeof m);
     if (format == kFmtRaw)
-        return A.G > 4 ? launch_own_impl<kFmtRaw, true>(A, P, map, after_prefix, stream)
-                       : launch_own_impl<kFmtRaw, false>(A, P, map, after_prefix, stream);
-    return A.G > 4 ? launch_own_impl<kFmtZf, true>(A, P, map, after_prefix, stream)
-                   : launch_own_impl<kFmtZf, false>(A, P, map, after_prefix, stream);
+        return A.G > 4 ? launch_own_of<kFmtRaw, true>(A, P, m, after_prefix, sms, stream)
+                       : launch_own_of<kFmtRaw, false>(A, P, m, after_prefix, sms, stream);
+    return A.G > 4 ? launch_own_of<kFmtZf, true>(A, P, m, after_prefix, sms, stream)
+                   : launch_own_of<kFmtZf, false>(A, P, m, after_prefix, sms, stream);
 }
 
 }  // namespace kvz

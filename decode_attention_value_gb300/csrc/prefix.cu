@@ -25,8 +25,9 @@ constexpr uint32_t kQHalfBytes = kQTileBytes / 2;
 constexpr int kExpWarps = 3;  // 12-bit pages: warps that restore K (warps 10 to 12) and V (13 to 15)
 constexpr uint32_t kGroupBytes = kPage * kDim * 2;  // most bytes of a coded (or raw) K or V group
 constexpr int kInfoRing = 8;
-// tensor memory, 256 columns a stream: 128 of scores, overwritten by the weights of the first and
-// of the second 64 tokens (32 columns of high, 32 of low parts each), and 128 of output
+// tensor memory, 256 columns a stream: 128 of scores, each 32 tokens' overwritten by their weights (16
+// columns of high, 16 of low parts), the first 64 columns later by all tokens' third parts, and 128 of
+// output
 constexpr uint32_t kColO = 256;
 
 // Two streams of softmax threads share a CTA.  kTiles = 2: 256 query rows, stream s holds rows
@@ -48,6 +49,8 @@ struct PfxSmem {
     // rings of K blocks and of V blocks: K's are given back as soon as the scores are made, V's
     // when the weights have been used
     static constexpr int ku = kTiles == 2 ? (coded ? 1 : 2) : (coded ? 2 : 3), vu = coded ? 2 : 3, units = ku + vu;
+    // operand layout: bytes from eight rows to the next, from 64 columns to the next
+    static constexpr uint32_t rows8 = 1024, cols64 = kHalfBytes;
     static constexpr int stages = coded ? 2 * kPfxPages : 0;  // coded groups of a block
     __host__ __device__ static constexpr int slot(int n, int kv) { return kv ? ku + n % vu : n % ku; }
     __host__ __device__ static constexpr uint32_t phase(int n, int kv) { return (kv ? n / vu : n / ku) & 1; }
@@ -59,8 +62,9 @@ struct PfxSmem {
     static constexpr int empty = full + units * 8;
     static constexpr int qfull = empty + units * 8;
     static constexpr int sfull = qfull + 8;    // [2] scores of a stream are in tensor memory
-    static constexpr int pready = sfull + 16;  // [2][2] its weights of half a block are
-    static constexpr int ofull = pready + 32;  // [2] its output of the segment is complete
+    static constexpr int pready = sfull + 16;  // [2][3] its weights of half a block are, third parts
+    static constexpr int pused = pready + 48;  // [2] those of the first half have been used
+    static constexpr int ofull = pused + 16;   // [2] its output of the segment is complete
     static constexpr int drain = ofull + 16;
     static constexpr int sarrived = drain + 8;  // [stages] coded groups
     static constexpr int sempty = sarrived + stages * 8;
@@ -190,7 +194,7 @@ __device__ __forceinline__ uint64_t spread_bits(uint32_t bits)
 }
 __device__ __forceinline__ uint32_t gather_bits(uint64_t bytes) { return (uint32_t)((bytes * 0x0102040810204080ull) >> 56); }
 
-template <int kFmt, int kTiles>
+template <int kFmt, int kTiles, int kParts>
 __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
     k_prefix(const PrefixParams P, const __grid_constant__ CUtensorMap tmap)
 {
@@ -216,8 +220,8 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         mbar_init(sbase + S::qfull, 256);
         for (int s = 0; s < 2; ++s) {
             mbar_init(sbase + S::sfull + 8 * s, 1);
-            mbar_init(sbase + S::pready + 16 * s, 128);
-            mbar_init(sbase + S::pready + 16 * s + 8, 128);
+            for (int i = 0; i < 3; ++i) mbar_init(sbase + S::pready + 24 * s + 8 * i, 128);
+            mbar_init(sbase + S::pused + 8 * s, 1);
             mbar_init(sbase + S::ofull + 8 * s, 1);
         }
         mbar_init(sbase + S::drain, 1);
@@ -499,45 +503,44 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         // stream's softmax runs while the other's products do.  (A warp per stream let them fall
         // into step: 368 us against 313 for 128 x 8 heads over 65536 tokens.)
         constexpr uint32_t kQk = mma_desc(128, kPfxBlock, false), kPv = mma_desc(128, kDim, true);
-        auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
-        const uint32_t tm = uniform(tmem);
+        const uint32_t go = elect_one(), tm = uniform(tmem), sb = uniform(sbase);
         bool ok = true;
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
             if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity));
             tc_fence_after();
         };
-        auto unit_addr = [&](int n, int kv) { return uniform(sbase + S::ring + S::slot(n, kv) * kUnitBytes); };
+        auto slot_of = [&](int n, int kv) { return uniform(S::slot(n, kv)); };
         auto wait_unit = [&](int n, int kv) { wait_all(sbase + S::full + 8 * S::slot(n, kv), S::phase(n, kv)); };
         // scores of stream s over K block n; give_back: the last product that reads the block
-        auto qk = [&](int s, int n, bool give_back) {
-            const uint64_t a = smem_desc(sbase + S::q + (kTiles == 2 ? s * kQTileBytes : 0), 16, 1024);
-            const uint64_t b = smem_desc(unit_addr(n, 0), 16, 1024);
-            const uint32_t freebar = uniform(sbase + S::empty + 8 * S::slot(n, 0));
-            if (elect_one()) {
+        auto qk = [&](uint32_t s, int n, bool give_back) {
+            const uint32_t slot = slot_of(n, 0);
+            const uint64_t a = smem_desc(sb + S::q + (kTiles == 2 ? s * kQTileBytes : 0), 16, 1024);
+            const uint64_t b = smem_desc(sb + S::ring + slot * kUnitBytes, 16, S::rows8);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 of the 128 dims: 32 bytes within a half's rows
-                    mma_ss(tm + s * 128, a + (((k >> 2) * kQHalfBytes + (k & 3) * 32) >> 4),
-                           b + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4), kQk, k > 0);
-                mma_commit(sbase + S::sfull + 8 * s);
-                if (give_back) mma_commit(freebar);
-            }
-            __syncwarp();
+            for (int k = 0; k < 8; ++k)  // 16 of the 128 dims: 32 bytes within a half's rows
+                mma_ss(go, tm + s * 128, a + (((k >> 2) * kQHalfBytes + (k & 3) * 32) >> 4),
+                       b + (((k >> 2) * S::cols64 + (k & 3) * 32) >> 4), kQk, k > 0);
+            mma_commit(go, sb + S::sfull + 8 * s);
+            if (give_back) mma_commit(go, sb + S::empty + 8 * slot);
         };
-        // output of stream s: its weights (high and low parts) of 64 tokens times half of V block n
-        auto pv = [&](int s, int n, int half, bool add, bool last, bool give_back) {
-            const uint64_t b = smem_desc(unit_addr(n, 1) + half * 8192, kHalfBytes, 1024);
-            const uint32_t freebar = uniform(sbase + S::empty + 8 * S::slot(n, 1));
-            if (elect_one()) {
+        // output of stream s: its weights of 64 tokens (two parts of 32 tokens after two of the 32 before)
+        // times half of the V block in slot
+        auto pv = [&](uint32_t s, uint32_t slot, uint32_t half, bool add) {
+            const uint64_t b = smem_desc(sb + S::ring + slot * kUnitBytes + half * 8 * S::rows8, S::cols64, S::rows8);
+            const uint32_t w = tm + s * 128 + half * 64, o = tm + kColO + s * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 16 tokens: two atoms of V rows, eight columns of weights
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
+                    mma_ts(go, o, w + (k >> 1) * 32 + part * 16 + (k & 1) * 8, b + ((k * 2 * S::rows8) >> 4), kPv,
+                           part || k ? true : add);
+            if (kParts == 3 && half == 0) mma_commit(go, sb + S::pused + 8 * s);
+        };
+        auto pv_third = [&](uint32_t s, uint32_t slot) {  // third parts, all 128 tokens
+            const uint64_t b = smem_desc(sb + S::ring + slot * kUnitBytes, S::cols64, S::rows8);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 16 tokens: two atoms of V rows, eight columns of weights
-                        mma_ts(tm + kColO + s * 128, tm + s * 128 + half * 64 + part * 32 + k * 8, b + ((k * 2048) >> 4),
-                               kPv, part || k ? true : add);
-                if (last) mma_commit(sbase + S::ofull + 8 * s);
-                if (give_back) mma_commit(freebar);
-            }
-            __syncwarp();
+            for (int k = 0; k < 8; ++k)
+                mma_ts(go, tm + kColO + s * 128, tm + s * 128 + k * 8, b + ((k * 2 * S::rows8) >> 4), kPv, true);
         };
         constexpr int step = kTiles == 2 ? 1 : 2;  // blocks between a stream's blocks
         uint32_t pphase = 0;                       // bit s
@@ -558,32 +561,42 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 for (int s = 0; s < 2; ++s) {  // the streams in turn
                     const int j = kTiles == 2 ? i : 2 * i + s;
                     if (j >= nb || !ok) break;
+                    const uint32_t ph = pphase >> s & 1, pbar = sbase + S::pready + 24 * s, slot = slot_of(n0 + j, 1);
                     if (kTiles == 1 || s == 0) wait_unit(n0 + j, 1);
-                    wait_all(sbase + S::pready + 16 * s, pphase >> s & 1);
+                    wait_all(pbar, ph);
                     if (!ok) break;
-                    pv(s, n0 + j, 0, i % P.fold != 0, false, false);
+                    pv(s, slot, 0, i % P.fold != 0);
                     if (j + step < nb && (kTiles == 1 || s == 0)) wait_unit(n0 + j + step, 0);
-                    wait_all(sbase + S::pready + 16 * s + 8, pphase >> s & 1);
+                    wait_all(pbar + 8, ph);
                     if (!ok) break;
+                    pv(s, slot, 1, true);
+                    if (kParts == 3) {
+                        wait_all(pbar + 16, ph);
+                        if (!ok) break;
+                        pv_third(s, slot);
+                    }
                     pphase ^= 1u << s;
-                    pv(s, n0 + j, 1, true, j + step >= nb, kTiles == 1 || s == 1);
+                    if (j + step >= nb) mma_commit(go, sb + S::ofull + 8 * s);
+                    if (kTiles == 1 || s == 1) mma_commit(go, sb + S::empty + 8 * slot);
                     if (j + step < nb) qk(s, n0 + j + step, kTiles == 1 || s == 1);
                 }
             }
             x += nb;
         }
         if (!ok) {  // no product in flight when tensor memory is given back
-            if (elect_one()) mma_commit(sbase + S::drain);
-            __syncwarp();
+            mma_commit(go, sbase + S::drain);
             mbar_wait(sbase + S::drain, 0, P.status);
         }
         __syncwarp();
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::softmax_regs));
         // ================================ softmax ================================
-        // Thread = query row.  Its 128 scores of a block come from tensor memory at once;
-        // the weights go back over them, 64 tokens at a time, as two BF16 parts, p = high + low (16
-        // bits of p); the product with the first half of V runs while the second half is made.  The
+        // Thread = query row.  Its 128 scores of a block are read twice, for the maximum and, 64 tokens
+        // at a time, for the weights, which go back over them: p = high + low in BF16, 16 bits of p
+        // (off by at most 2^-17 of p, a 2^-9 part of a BF16 output's own rounding), and a third part,
+        // all of p, for fp32 outputs.  The product with the first half of V runs while the second half is
+        // made.  (All scores in registers and unrolled code: 155 K clocks for 27 blocks of 256 rows
+        // against 143 K this way; the loops of all roles share the instruction caches.)  The
         // running maximum moves, and the output is rescaled, only when it grows by more than
         // 2^8: weights up to 2^8 lose nothing in floating point.  Every P.fold blocks the output
         // is added to the partial in memory and begins anew: the tensor cores' fp32 sums drop
@@ -684,11 +697,6 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 const int left = sg.len - (sg.block0 + j) * kPfxBlock;
                 const uint32_t bad = gather_bits(info[n % kInfoRing]);
                 const bool whole = left >= kPfxBlock && bad == 0;
-                uint32_t v[4][32];
-                if (active) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) tmem_ld32(tS + 32 * w, v[w]);
-                }
                 if (!kCoded && !whole) {
                     // rows of V that hold no token: zero, so that weight 0 times them is 0
                     const int slot = S::slot(n, 1);
@@ -704,29 +712,36 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                     fence_async_shared();
                     if (!__all_sync(0xffffffffu, wait.ok)) break;
                 }
+                if (!whole && active) {  // scores without a token: minus infinity
+#pragma unroll 1
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t live = left >= 32 * w + 32 ? ~0u : left <= 32 * w ? 0u : (1u << (left - 32 * w)) - 1;
+                        live &= ~((bad >> (2 * w) & 1 ? 0xFFFFu : 0u) | (bad >> (2 * w + 1) & 1 ? 0xFFFF0000u : 0u));
+                        uint32_t v[32];
+                        tmem_ld32(tS + 32 * w, v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = live >> i & 1 ? v[i] : 0xFF800000u;
+                        tmem_st32(tS + 32 * w, v);
+                    }
+                    tmem_wait_st();
+                }
                 float u = 0.f;
                 if (active) {
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[2][32];
+                        tmem_ld32(tS + 64 * h, v[0]);
+                        tmem_ld32(tS + 64 * h + 32, v[1]);
+                        tmem_wait_ld(v[0]);
+                        tmem_wait_ld(v[1]);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) tmem_wait_ld(v[w]);
-                    if (!whole) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int t = 32 * w + i;
-                                if (t >= left || (bad >> (t >> 4) & 1)) v[w][i] = 0xFF800000u;  // -inf
-                            }
+                        for (int i = 0; i < 32; i += 2) {
+                            top[i & 2] = max3(top[i & 2], __uint_as_float(v[0][i]), __uint_as_float(v[0][i + 1]));
+                            top[(i & 2) + 1] = max3(top[(i & 2) + 1], __uint_as_float(v[1][i]), __uint_as_float(v[1][i + 1]));
+                        }
                     }
-                    float top[4];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        top[w] = __uint_as_float(v[w][0]);
-#pragma unroll
-                        for (int i = 1; i < 31; i += 2)
-                            top[w] = max3(top[w], __uint_as_float(v[w][i]), __uint_as_float(v[w][i + 1]));
-                    }
-                    top[0] = max3(top[0], __uint_as_float(v[0][31]), __uint_as_float(v[1][31]));
-                    top[1] = max3(top[1], __uint_as_float(v[2][31]), __uint_as_float(v[3][31]));
                     const float bm = fmaxf(max3(top[0], top[1], top[2]), top[3]) * P.scale_log2;
                     const bool grow = mine == 0 || bm > m + 8.f;
                     if (mine > 0 && __any_sync(0xffffffffu, grow)) {
@@ -747,11 +762,17 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                 }
                 const uint64_t shift = pack2(-u, -u);
                 uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
+                uint32_t third[kParts == 3 ? 4 : 1][16];
+#pragma unroll(kParts == 3 ? 2 : 1)
                 for (int half = 0; half < 2; ++half) {
                     if (active) {
+                        uint32_t v[2][32];
+                        tmem_ld32(tS + 64 * half, v[0]);
+                        tmem_ld32(tS + 64 * half + 32, v[1]);
+                        tmem_wait_ld(v[0]);
+                        tmem_wait_ld(v[1]);
 #pragma unroll
-                        for (int w = 2 * half; w < 2 * half + 2; ++w) {
+                        for (int w = 0; w < 2; ++w) {
                             uint32_t hi2[16], lo2[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
@@ -763,20 +784,38 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
                                 p1 = ex2(p1);
                                 const uint64_t p = pack2(p0, p1);
                                 sum[i & 1] = add2(sum[i & 1], p);
-                                hi2[i] = pack_bf16x2(p0, p1);
+                                auto rest = [&](uint64_t x, uint32_t part) {  // x without its BF16 part, exact
+                                    return fma2(pack2(__uint_as_float(part << 16), __uint_as_float(part & 0xFFFF0000u)), minus, x);
+                                };
                                 float r0, r1;
-                                unpack2(fma2(pack2(__uint_as_float(hi2[i] << 16), __uint_as_float(hi2[i] & 0xFFFF0000u)),
-                                             minus, p),
-                                        r0, r1);
+                                hi2[i] = pack_bf16x2(p0, p1);
+                                const uint64_t r = rest(p, hi2[i]);
+                                unpack2(r, r0, r1);
                                 lo2[i] = pack_bf16x2(r0, r1);
+                                if (kParts == 3) {
+                                    unpack2(rest(r, lo2[i]), r0, r1);
+                                    third[(kParts == 3 ? 2 * half : 0) + (kParts == 3 ? w : 0)][i] = pack_bf16x2(r0, r1);
+                                }
                             }
-                            tmem_st16(tS + 64 * half + 16 * (w & 1), hi2);
-                            tmem_st16(tS + 64 * half + 32 + 16 * (w & 1), lo2);
+                            tmem_st16(tS + 64 * half + 32 * w, hi2);
+                            tmem_st16(tS + 64 * half + 32 * w + 16, lo2);
                         }
                         tmem_wait_st();
                     }
                     tc_fence_before();
-                    mbar_arrive(sbase + S::pready + 16 * s + 8 * half);
+                    mbar_arrive(sbase + S::pready + 24 * s + 8 * half);
+                }
+                if (kParts == 3) {  // the third parts, over the first half's when they have been used
+                    wait(sbase + S::pused + 8 * s, sphase ^ 1);
+                    if (!__all_sync(0xffffffffu, wait.ok)) break;
+                    tc_fence_after();
+                    if (active) {
+#pragma unroll
+                        for (int w = 0; w < (kParts == 3 ? 4 : 0); ++w) tmem_st16(tS + 16 * w, third[w]);
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(sbase + S::pready + 24 * s + 16);
                 }
                 if (active) {
                     float s0, s1;
@@ -891,7 +930,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
 // ---------------------------------------------------------------------------------
 // launcher
 // ---------------------------------------------------------------------------------
-template <int kFmt, int kTiles>
+template <int kFmt, int kTiles, int kParts>
 static cudaError_t launch_prefix_impl(const PrefixParams &P, const CUtensorMap &map, cudaStream_t stream)
 {
     const int bytes = PfxSmem<kFmt, kTiles>::bytes(P.num_groups);
@@ -900,29 +939,33 @@ static cudaError_t launch_prefix_impl(const PrefixParams &P, const CUtensorMap &
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(dev < 64 && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1ull)) {
-        e = cudaFuncSetAttribute(k_prefix<kFmt, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        e = cudaFuncSetAttribute(k_prefix<kFmt, kTiles, kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e == cudaSuccess && dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_ACQ_REL);
     }
     if (e != cudaSuccess) return e;
-    k_prefix<kFmt, kTiles><<<P.grid, PfxSmem<kFmt, kTiles>::threads, bytes, stream>>>(P, map);
+    k_prefix<kFmt, kTiles, kParts><<<P.grid, PfxSmem<kFmt, kTiles>::threads, bytes, stream>>>(P, map);
     return cudaGetLastError();
 }
 
+template <int kFmt>
+static cudaError_t launch_prefix_of(const PrefixParams &P, const CUtensorMap &map, cudaStream_t stream)
+{
+    if (P.unit_rows == 256)
+        return P.out_bf16 ? launch_prefix_impl<kFmt, 2, 2>(P, map, stream) : launch_prefix_impl<kFmt, 2, 3>(P, map, stream);
+    return P.out_bf16 ? launch_prefix_impl<kFmt, 1, 2>(P, map, stream) : launch_prefix_impl<kFmt, 1, 3>(P, map, stream);
+}
+
 cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_map, const AttnParams &A,
-                          const void *own_map, cudaStream_t stream)
+                          const void *own_map, int sms, cudaStream_t stream)
 {
     const bool after = P.num_groups > 0 && P.grid > 0;
     if (after) {
         CUtensorMap map;
         memcpy(&map, prefix_map, sizeof map);
-        cudaError_t e;
-        if (format == kFmtRaw)
-            e = P.unit_rows == 256 ? launch_prefix_impl<kFmtRaw, 2>(P, map, stream) : launch_prefix_impl<kFmtRaw, 1>(P, map, stream);
-        else
-            e = P.unit_rows == 256 ? launch_prefix_impl<kFmtZf, 2>(P, map, stream) : launch_prefix_impl<kFmtZf, 1>(P, map, stream);
+        const cudaError_t e = format == kFmtRaw ? launch_prefix_of<kFmtRaw>(P, map, stream) : launch_prefix_of<kFmtZf>(P, map, stream);
         if (e != cudaSuccess) return e;
     }
-    if (A.grid == 0) return launch_own(A, P, format, own_map, after, stream);
+    if (A.grid == 0) return launch_own(A, P, format, own_map, after, sms, stream);
     cudaError_t e = launch_attention_partials(A, format, own_map, stream);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];

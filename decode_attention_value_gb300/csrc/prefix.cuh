@@ -19,7 +19,7 @@ __device__ __forceinline__ PfxGroup pfx_group(const PrefixParams &P, int g)
     r.seq0 = P.group_start[g];
     r.seqs = P.group_start[g + 1] - r.seq0;
     r.len = min(max(P.prefix_lens[g], 0), P.max_tokens);
-    r.blocks = (r.len + kPfxBlock - 1) / kPfxBlock;
+    r.blocks = r.len / kPfxBlock + (r.len % kPfxBlock != 0);
     r.tiles = r.blocks > 0 ? (r.seqs * P.G + P.unit_rows - 1) / P.unit_rows : 0;
     return r;
 }
@@ -97,10 +97,15 @@ struct RowSum {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     // up to 32 partials (lane k: maximum and sum of the k-th, -inf for one without tokens) whose
-    // outputs load(k) brings, eight at a time
+    // outputs load(k) brings, eight at a time.  Up to eight are loaded before the maxima are known, of
+    // more only those with tokens: a tile's CTA with one block leaves an empty partial beside it.
     template <class Load>
     __device__ __forceinline__ void add(float pm, float pl, int n, const Load &load)
     {
+        float4 x[8];
+        if (n <= 8)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = k < n ? load(k) : make_float4(0.f, 0.f, 0.f, 0.f);
         float top = pm;
 #pragma unroll
         for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -110,25 +115,36 @@ struct RowSum {
         float sum = none ? 0.f : w * pl;
 #pragma unroll
         for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const uint32_t have = __ballot_sync(0xffffffffu, !none);
+        uint32_t have = __ballot_sync(0xffffffffu, !none);
         l = l * f + sum;
         o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
         m = top;
-        for (int k0 = 0; k0 < n; k0 += 8) {
-            float4 x[8];
+        auto take = [&](const float4 &v, float wk) {
+            o.x += wk * v.x;
+            o.y += wk * v.y;
+            o.z += wk * v.z;
+            o.w += wk * v.w;
+        };
+        if (n <= 8) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (have >> (k0 + k) & 1) x[k] = load(k0 + k);
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                if (have >> k & 1) take(x[k], wk);  // (one without tokens was not written)
             }
+            return;
+        }
+        while (have) {
+            float wk[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
-                o.x += wk * x[k].x;
-                o.y += wk * x[k].y;
-                o.z += wk * x[k].z;
-                o.w += wk * x[k].w;
+                const int at = __ffs(have) - 1;  // -1: none left
+                wk[k] = __shfl_sync(0xffffffffu, w, at & 31);
+                if (at < 0) wk[k] = 0.f;
+                x[k] = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : load(at);
+                have &= have - 1;
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) take(x[k], wk[k]);
         }
     }
     // another warp's

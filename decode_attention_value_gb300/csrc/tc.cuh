@@ -89,42 +89,49 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool b_mn)
     return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (uint32_t)(m / 16) << 24;
 }
 
-// D[tmem] (+)= A[smem] B[smem]: 16 deep, issued by one thread
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// D[tmem] (+)= A[smem] B[smem]: 16 deep, issued by the one thread with go != 0.  The whole warp comes
+// here: the product is predicated, not branched around, so that its operands, equal in all lanes, are
+// worked out in uniform registers (behind a branch the issuing thread moved them there for every
+// product: 93 clocks a product that takes 64).
+__device__ __forceinline__ void mma_ss(uint32_t go, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, g;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 g, %5, 0;\n\t"
+        "@g tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(go)
         : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem]; A: two BF16 a column
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t go, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p, g;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 g, %5, 0;\n\t"
+        "@g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(go)
         : "memory");
 }
 
-// One lane of a converged warp (the same one every time).  Code under it stays warp-uniform for the
-// compiler, so operand descriptors are kept in uniform registers: an issuing thread that has to
-// move them for every product is starved by busy warps of its scheduler (measured with all
-// schedulers busy: 253 clocks a product that takes 64, against 103 this way).
-__device__ __forceinline__ bool elect_one()
+// One lane of a converged warp: 1 there, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
+    return r;
 }
 
-// Arrive on the barrier when every matrix product this thread has issued is complete.
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+// Arrive on the barrier when every matrix product that the thread with go != 0 has issued is complete.
+__device__ __forceinline__ void mma_commit(uint32_t go, uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred g;\n\tsetp.ne.u32 g, %1, 0;\n\t"
+        "@g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(go)
+        : "memory");
 }
+
+// A value that is the same in all lanes, in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
 
 // ---- 8x8 BF16 matrices from fragments to shared memory rows ----
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t (&r)[4])

@@ -2,7 +2,8 @@
 tiles, and paged GQA decode attention over either on one GB300 (sm_103a).
 
 Argument marshalling only: every step runs in the CUDA kernels of ``libkvz.so``
-(built in-tree by ``_build.build()``).  Tensors are torch CUDA tensors; the binding
+(built in-tree by ``_build.build()``), called by ctypes, or through ``_binding`` where a
+decode step's time is the host's (append_tokens, prefix_attention).  Tensors are torch CUDA tensors; the binding
 passes their device pointers and the current CUDA stream through the C ABI declared in
 ``include/kvz.h``.  There is no CPU fallback: importing raises when the library is
 missing, and every call raises on a non-zero return code.
@@ -138,6 +139,10 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError("the native binding is not built; run decode_attention_value_gb300._build.build()") from e
 
 
 def lib() -> ctypes.CDLL:
@@ -163,25 +168,6 @@ def _ptr(t: torch.Tensor | None, dtype=None, name: str = "") -> int | None:
     return t.data_ptr()
 
 
-def _refuse(t: torch.Tensor, dtypes, name: str, dev: int):
-    """What is wrong with a tensor that _ptr_on does not take."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: expected a tensor on CUDA device {dev}, got {t.device}")
-    if dtypes and t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {dtypes[0]}, got {t.dtype}")
-    raise ValueError(f"{name}: expected a contiguous tensor")
-
-
-def _ptr_on(t: torch.Tensor, dtypes, name: str, dev: int) -> int:
-    """_ptr for a tensor that has to be on CUDA device dev (a few hundred nanoseconds: the
-    calls that take many tensors are launched once a layer)."""
-    if (dtypes and t.dtype not in dtypes) or t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, dtypes, name, dev)
-    return t.data_ptr()
-
-
 # torch.cuda.current_stream() and current_device() build objects (3 us a call on the GB300's host);
 # these return the numbers they wrap
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -194,14 +180,6 @@ def _stream(stream) -> int | None:
     return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(_current_device())
 
 
-def _device_of(status: torch.Tensor) -> int:
-    """The device of a call: its status tensor's, which has to be the current one."""
-    dev = status.get_device()
-    if dev < 0 or dev != _current_device():
-        raise ValueError(f"status: expected a tensor on the current CUDA device, got {status.device}")
-    return dev
-
-
 def _check(fn: str, rc: int):
     if rc != 0:
         raise KvzError(fn, rc)
@@ -211,10 +189,6 @@ _U64 = (torch.uint64, torch.int64) if hasattr(torch, "uint64") else (torch.int64
 _U32 = (torch.int32,) + ((torch.uint32,) if hasattr(torch, "uint32") else ())
 _U8 = (torch.uint8,)
 _BF16 = (torch.bfloat16, torch.int16)
-_BF16_ONLY = (torch.bfloat16,)
-_I32 = (torch.int32,)
-_I64 = (torch.int64,)
-_OUT_TYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 
 
 def _pages_of(pool: torch.Tensor) -> int:
@@ -350,37 +324,16 @@ def prefix_attention_workspace_size(hkv: int, batch: int, num_q_heads: int, grou
     return size
 
 
-def _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens, out, status, workspace, stream):
-    """Checks shared by the two prefix attention calls: (device, batch, query heads, groups,
-    prefix columns, own columns, output type, workspace)."""
-    dev = _device_of(status)
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != HEAD_DIM:
-        raise ValueError(f"q: expected [batch][heads][{HEAD_DIM}], got {tuple(shape)}")
-    B, hq, _ = shape
-    if prefix_lens.dim() != 1:
-        raise ValueError(f"prefix_lens: expected [groups], got {tuple(prefix_lens.shape)}")
-    n = prefix_lens.shape[0]
-    if group_start.shape != (n + 1,):
-        raise ValueError(f"group_start: expected [{n + 1}] for {n} groups, got {tuple(group_start.shape)}")
-    pre, own = prefix_ids.shape, page_ids.shape
-    if len(pre) != 2 or pre[0] != n:
-        raise ValueError(f"prefix_ids: expected [{n}][pages], got {tuple(pre)}")
-    if len(own) != 2 or own[0] != B:
-        raise ValueError(f"page_ids: expected [{B}][pages], got {tuple(own)}")
-    if seq_lens.shape != (B,):
-        raise ValueError(f"seq_lens: expected [{B}], got {tuple(seq_lens.shape)}")
-    if out.shape != shape:
-        raise ValueError(f"out: expected {tuple(shape)}, got {tuple(out.shape)}")
-    kind = _OUT_TYPES.get(out.dtype)
-    if kind is None:
-        raise ValueError(f"out: expected torch.float32 or torch.bfloat16, got {out.dtype}")
-    if workspace is None:
-        workspace = torch.empty(prefix_attention_workspace_size(hkv, B, hq, n, pre[1], own[1]), dtype=torch.uint8,
-                                device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
-    return dev, B, hq, n, pre[1], own[1], kind, workspace
+def _prefix_workspace(q, hkv, prefix_ids, page_ids, stream):
+    """A workspace of the call's own; empty for shapes that the call then refuses."""
+    if q.dim() != 3 or prefix_ids.dim() != 2 or page_ids.dim() != 2:
+        raise ValueError("q, prefix_ids, page_ids: expected [batch][heads][128], [groups][pages] and [batch][pages]")
+    size = _lib.kvz_prefix_attention_workspace_size(_dims(hkv), q.shape[0], q.shape[1], prefix_ids.shape[0],
+                                                    prefix_ids.shape[1] + 1, page_ids.shape[1] + 1)
+    workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace
 
 
 def prefix_attention(q, group_start, prefix_ids, prefix_lens, prefix_tail, page_ids, seq_lens, tail_page, meta, arena,
@@ -390,41 +343,27 @@ def prefix_attention(q, group_start, prefix_ids, prefix_lens, prefix_tail, page_
     tokens in the compressed pages prefix_ids[g] plus the raw page prefix_tail[g];
     page_ids, seq_lens and tail_page are each sequence's own tokens behind it.  The prefix
     is read once for all sequences of its group.  out: float32 or BF16 [B][Hq][128]."""
-    hkv = meta.shape[1] if meta.dim() >= 2 else raw_pool.shape[1]
-    dev, B, hq, n, pp, op, ot, workspace = _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens,
-                                                        out, status, workspace, stream)
-    if prefix_tail.shape != (n,) or tail_page.shape != (B,):
-        raise ValueError(f"prefix_tail, tail_page: expected [{n}] and [{B}]")
-    if meta.shape[1:] != (hkv, 2) or raw_pool.shape[1:] != (hkv, 2, PAGE, HEAD_DIM):
-        raise ValueError(f"meta, raw_pool: expected [pages][{hkv}][2] and [pages][{hkv}][2][{PAGE}][{HEAD_DIM}]")
-    _check("kvz_prefix_attention", _lib.kvz_prefix_attention(
-        _dims(hkv), B, hq, _ptr_on(q, _BF16_ONLY, "q", dev), n, _ptr_on(group_start, _I32, "group_start", dev),
-        _ptr_on(prefix_ids, _I32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, _I32, "prefix_lens", dev),
-        _ptr_on(prefix_tail, _I32, "prefix_tail", dev), _ptr_on(page_ids, _I32, "page_ids", dev), op,
-        _ptr_on(seq_lens, _I32, "seq_lens", dev), _ptr_on(tail_page, _I32, "tail_page", dev),
-        _ptr_on(meta, _U64, "meta", dev), meta.shape[0], _ptr_on(arena, _U8, "arena", dev), arena.numel(),
-        _ptr_on(raw_pool, _BF16_ONLY, "raw_pool", dev), raw_pool.shape[0], _ptr_on(out, None, "out", dev), ot,
-        _ptr_on(workspace, _U8, "workspace", dev), workspace.numel(), _ptr_on(status, _U32, "status", dev),
-        _stream(stream)))
+    if meta is None or arena is None:
+        raise ValueError("meta, arena: expected tensors")
+    if workspace is None:
+        workspace = _prefix_workspace(q, raw_pool.shape[1], prefix_ids, page_ids, stream)
+    rc = _binding.prefix_attention(q, group_start, prefix_ids, prefix_lens, prefix_tail, page_ids, seq_lens, tail_page,
+                                   meta, arena, raw_pool, out, status, workspace,
+                                   None if stream is None else stream.cuda_stream)
+    if rc:
+        raise KvzError("kvz_prefix_attention", rc)
 
 
 def prefix_attention_raw(q, group_start, prefix_ids, prefix_lens, page_ids, seq_lens, raw_pool, out, status,
                          workspace=None, stream=None):
     """prefix_attention over plain BF16 pages: prefix_ids and page_ids name raw pages and
     cover the last, partial ones."""
-    pool = raw_pool.shape
-    hkv = pool[1]
-    dev, B, hq, n, pp, op, ot, workspace = _prefix_args(q, hkv, group_start, prefix_ids, prefix_lens, page_ids, seq_lens,
-                                                        out, status, workspace, stream)
-    if pool[1:] != (hkv, 2, PAGE, HEAD_DIM):
-        raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(pool)}")
-    _check("kvz_prefix_attention_raw", _lib.kvz_prefix_attention_raw(
-        _dims(hkv), B, hq, _ptr_on(q, _BF16_ONLY, "q", dev), n, _ptr_on(group_start, _I32, "group_start", dev),
-        _ptr_on(prefix_ids, _I32, "prefix_ids", dev), pp, _ptr_on(prefix_lens, _I32, "prefix_lens", dev),
-        _ptr_on(page_ids, _I32, "page_ids", dev), op, _ptr_on(seq_lens, _I32, "seq_lens", dev),
-        _ptr_on(raw_pool, _BF16_ONLY, "raw_pool", dev), pool[0], _ptr_on(out, None, "out", dev), ot,
-        _ptr_on(workspace, _U8, "workspace", dev), workspace.numel(), _ptr_on(status, _U32, "status", dev),
-        _stream(stream)))
+    if workspace is None:
+        workspace = _prefix_workspace(q, raw_pool.shape[1], prefix_ids, page_ids, stream)
+    rc = _binding.prefix_attention(q, group_start, prefix_ids, prefix_lens, None, page_ids, seq_lens, None, None, None,
+                                   raw_pool, out, status, workspace, None if stream is None else stream.cuda_stream)
+    if rc:
+        raise KvzError("kvz_prefix_attention_raw", rc)
 
 
 # ------------------------------------------------------------------------------------
@@ -445,22 +384,6 @@ def rope_table(inv_freq: torch.Tensor, axis: torch.Tensor | None = None) -> torc
     return torch.stack([turns, axis], 1)
 
 
-def _heads(t: torch.Tensor, name: str, tokens: int, dev: int):
-    """(heads, pointer, token stride, head stride) of a BF16 [tokens][heads][128] tensor
-    whose heads are contiguous."""
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != HEAD_DIM:
-        raise ValueError(f"{name}: expected [{tokens}][heads][{HEAD_DIM}], got {tuple(shape)}")
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
-        _refuse(t, _BF16_ONLY, name, dev)
-    ts, hs, es = t.stride()
-    if es != 1:
-        raise ValueError(f"{name}: expected contiguous heads")
-    heads = shape[1]
-    # a stride nothing steps by may be any number
-    return heads, t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0
-
-
 def append_tokens(k, v, slots, raw_pool, status, q=None, q_out=None, rope=None, positions=None,
                   interleaved: bool = False, rope_scale: float = 1.0, stream=None):
     """Write the keys and values of new tokens, BF16 [T][Hkv][128] (any token and head
@@ -469,59 +392,14 @@ def append_tokens(k, v, slots, raw_pool, status, q=None, q_out=None, rope=None, 
     rope_table) at positions (int32 [T] or [axes][T]).  q [T][Hq][128], when given, is
     rotated into q_out (allocated when None; may be q).  k, v, slots and raw_pool may all
     be None to rotate queries alone.  Returns q_out."""
-    dev = _device_of(status)
-    if k is not None:
-        if v is None or slots is None or raw_pool is None:
-            raise ValueError("append_tokens: k, v, slots and raw_pool go together")
-        T = k.shape[0]
-        hkv, kp, kt, kh = _heads(k, "k", T, dev)
-        hv, vp, vt, vh = _heads(v, "v", T, dev)
-        pool = raw_pool.shape
-        if hv != hkv:
-            raise ValueError(f"v: expected {hkv} heads, got {hv}")
-        if pool[1:] != (hkv, 2, PAGE, HEAD_DIM):
-            raise ValueError(f"raw_pool: expected [pages][{hkv}][2][{PAGE}][{HEAD_DIM}], got {tuple(pool)}")
-        if slots.shape != (T,):
-            raise ValueError(f"slots: expected [{T}], got {tuple(slots.shape)}")
-        pages, pool, sl = pool[0], _ptr_on(raw_pool, _BF16_ONLY, "raw_pool", dev), _ptr_on(slots, _I32, "slots", dev)
-    else:
-        if v is not None or slots is not None or raw_pool is not None:
-            raise ValueError("append_tokens: k, v, slots and raw_pool go together")
-        if q is None:
-            raise ValueError("append_tokens: no tokens (k and q are both None)")
-        T, hkv, pages = q.shape[0], 1, 0
-        kp = vp = pool = sl = None
-        kt = kh = vt = vh = 0
-    if q is not None:
-        hq, qp, qt, qh = _heads(q, "q", T, dev)
-        if q_out is None:
-            q_out = torch.empty((T, hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
-        elif q_out.shape != q.shape:
-            raise ValueError(f"q_out: expected {tuple(q.shape)}, got {tuple(q_out.shape)}")
-        qo = _ptr_on(q_out, _BF16_ONLY, "q_out", dev)
-    else:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        hq = qt = qh = 0
-        qp = qo = None
-    if rope is not None:
-        table = rope.shape
-        if len(table) != 2 or table[1] != 2:
-            raise ValueError(f"rope: expected a rope_table, got {tuple(table)}")
-        if positions is None:
-            raise ValueError("rope without positions")
-        at = positions.shape
-        if len(at) not in (1, 2) or at[-1] != T:
-            raise ValueError(f"positions: expected [{T}] or [axes][{T}], got {tuple(at)}")
-        axes = 1 if len(at) == 1 else at[0]
-        rot, rp, pp = 2 * table[0], _ptr_on(rope, _I64, "rope", dev), _ptr_on(positions, _I32, "positions", dev)
-    else:
-        axes = rot = 0
-        rp = pp = None
-    _check("kvz_append_tokens", _lib.kvz_append_tokens(
-        _dims(hkv), T, hq, qp, qt, qh, kp, kt, kh, vp, vt, vh, sl, pp, axes, rp, rot,
-        ROPE_INTERLEAVED if interleaved else 0, rope_scale, qo, pool, pages, _ptr_on(status, _U32, "status", dev),
-        _stream(stream)))
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if stream is not None:
+            q_out.record_stream(stream)
+    rc = _binding.append_tokens(k, v, slots, raw_pool, status, q, q_out, rope, positions, interleaved, rope_scale,
+                                None if stream is None else stream.cuda_stream)
+    if rc:
+        raise KvzError("kvz_append_tokens", rc)
     return q_out
 
 

@@ -41,9 +41,10 @@ def _append_rows(pools, pages, rows, kv, status, q, rope, positions, interleaved
     if rope is not None:
         positions = torch.as_tensor(positions, dtype=torch.int32, device=dev).reshape(-1, 1, n)
         positions = positions.expand(-1, L, n).reshape(-1, L * n)
-    q_out = append_tokens(kv[:, :, 0], kv[:, :, 1], slots, pools.view(L * per, *pools.shape[2:]), status,
-                          q=None if q is None else q.reshape(L * n, *q.shape[2:]), rope=rope,
-                          positions=positions if rope is not None else None, interleaved=interleaved)
+    with torch.cuda.device(dev):
+        q_out = append_tokens(kv[:, :, 0], kv[:, :, 1], slots, pools.view(L * per, *pools.shape[2:]), status,
+                              q=None if q is None else q.reshape(L * n, *q.shape[2:]), rope=rope,
+                              positions=positions if rope is not None else None, interleaved=interleaved)
     return None if q is None else q_out.view(q.shape)
 
 

@@ -15,8 +15,11 @@
 // Layout: a row is one head of one token, 256 bytes, handled by eight lanes: each holds two
 // 16-byte vectors, eight whole rotary pairs in either pairing.  A block takes a run of
 // consecutive rows (whole tokens as far as possible), computes the sines of the tokens it
-// touches once into shared memory (<= kTokens x 64 pairs) and then streams its rows; the
-// loads of a row do not wait for the sines.
+// touches once into shared memory (<= kAppendTokens x 64 pairs, a lane's eight pairs of a row
+// side by side with the other lanes': no bank is asked twice) and then streams its rows; the
+// loads of a row do not wait for the sines.  Token and head of a row come from its number within
+// the block, a division in 32 bits.
+#include "kvz_device.cuh"
 #include "kvz_internal.h"
 
 namespace kvz {
@@ -25,6 +28,7 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = kAppendThreads / 8;  // rows a block handles at once
 constexpr int kAppendTokens = 8;                 // tokens a block may touch
 
+// cs: the first of the eight pairs' (cos, sin), the next ones eight further each
 __device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float2 *cs, bool neighbours)
 {
     uint32_t *w0 = reinterpret_cast<uint32_t *>(&x), *w1 = reinterpret_cast<uint32_t *>(&y);
@@ -33,7 +37,7 @@ __device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float2 *cs, bo
         for (int i = 0; i < 8; ++i) {
             uint32_t &w = i < 4 ? w0[i] : w1[i - 4];
             const float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xFFFF0000u);
-            const float2 t = cs[i];
+            const float2 t = cs[8 * i];
             w = pack_bf16x2(a * t.x - b * t.y, a * t.y + b * t.x);
         }
         return;
@@ -42,7 +46,7 @@ __device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float2 *cs, bo
     for (int i = 0; i < 4; ++i) {  // pairs are (x element, y element)
         const float a0 = __uint_as_float(w0[i] << 16), a1 = __uint_as_float(w0[i] & 0xFFFF0000u);
         const float b0 = __uint_as_float(w1[i] << 16), b1 = __uint_as_float(w1[i] & 0xFFFF0000u);
-        const float2 t0 = cs[2 * i], t1 = cs[2 * i + 1];
+        const float2 t0 = cs[16 * i], t1 = cs[16 * i + 8];
         w0[i] = pack_bf16x2(a0 * t0.x - b0 * t0.y, a1 * t1.x - b1 * t1.y);
         w1[i] = pack_bf16x2(a0 * t0.y + b0 * t0.x, a1 * t1.y + b1 * t1.x);
     }
@@ -54,7 +58,9 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams P)
     const int H = P.hq + 2 * P.hkv, tid = threadIdx.x;
     const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_block;
     const int64_t row1 = min(row0 + P.rows_per_block, (int64_t)P.tokens * H);
-    const int tok0 = (int)(row0 / H), tok1 = (int)((row1 - 1) / H);
+    const int tok0 = (int)(row0 / H), rows = (int)(row1 - row0);
+    const uint32_t head0 = (uint32_t)(row0 - (int64_t)tok0 * H);
+    const int toks = (int)((head0 + rows - 1) / (uint32_t)H) + 1;
     const int pairs = P.rot / 2;
     const int u = tid & 7;  // the lane's eight pairs (or 16 plain elements) of a row
     const bool turning = u < P.rot / 16;
@@ -68,11 +74,12 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams P)
         bool rotated;
     };
     // a row's source and destination; its two vectors are loaded here
-    auto load = [&](int64_t row, Row &r) {
+    auto load = [&](int row, Row &r) {
         r.dst = nullptr;
-        if (row >= row1) return;
-        r.tok = (int)(row / H);
-        const int h = (int)(row - (int64_t)r.tok * H);
+        if (row >= rows) return;
+        const uint32_t in = (head0 + row) / (uint32_t)H;
+        r.tok = tok0 + (int)in;
+        const int h = (int)(head0 + row - in * (uint32_t)H);
         const uint16_t *src;
         if (h < P.hq) {
             src = P.q + r.tok * P.q_token + h * P.q_head;
@@ -81,9 +88,9 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams P)
         } else {
             const bool is_v = h >= P.hq + P.hkv;
             const int kvh = h - P.hq - (is_v ? P.hkv : 0);
-            const int32_t slot = P.slots[r.tok];
-            if (slot < 0 || slot / kPage >= P.num_raw_pages) {
-                if (slot != -1 && u == 0) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
+            const uint32_t slot = (uint32_t)P.slots[r.tok];
+            if (slot > INT32_MAX || slot / kPage >= P.num_raw_pages) {
+                if (slot != 0xFFFFFFFFu && u == 0) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
                 return;  // -1: a padding token
             }
             src = is_v ? P.v + r.tok * P.v_token + kvh * P.v_head : P.k + r.tok * P.k_token + kvh * P.k_head;
@@ -91,22 +98,23 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams P)
                     ((((int64_t)(slot / kPage) * P.hkv + kvh) * 2 + (is_v ? 1 : 0)) * kPage + slot % kPage) * kDim;
             r.rotated = !is_v;
         }
-        r.x = *reinterpret_cast<const uint4 *>(src + e0);
-        r.y = *reinterpret_cast<const uint4 *>(src + e1);
+        r.x = __ldcs(reinterpret_cast<const uint4 *>(src + e0));
+        r.y = __ldcs(reinterpret_cast<const uint4 *>(src + e1));
     };
     auto store = [&](Row &r) {
         if (!r.dst) return;
-        if (r.rotated && turning) rotate8(r.x, r.y, &cs[r.tok - tok0][8 * u], P.neighbours);
+        if (r.rotated && turning) rotate8(r.x, r.y, &cs[r.tok - tok0][u], P.neighbours);
         *reinterpret_cast<uint4 *>(r.dst + e0) = r.x;
         *reinterpret_cast<uint4 *>(r.dst + e1) = r.y;
     };
 
+    pdl_wait_primary();  // launched while the kernel before it ends
     Row a, b;
-    int64_t row = row0 + (tid >> 3);
+    int row = tid >> 3;
     load(row, a);
     load(row + kAppendRows, b);
     if (pairs > 0) {
-        for (int i = tid; i < (tok1 - tok0 + 1) * pairs; i += kAppendThreads) {
+        for (int i = tid; i < toks * pairs; i += kAppendThreads) {
             const int t = i / pairs, p = i - t * pairs;
             const uint64_t turns = P.rope[2 * p], axis = P.rope[2 * p + 1];
             float s = 0.f, c = 1.f;
@@ -117,11 +125,11 @@ __global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams P)
             } else {
                 atomicOr(P.status, KVZ_STATUS_BAD_INDEX);  // an axis without positions: not turned
             }
-            cs[t][p] = make_float2(c * P.scale, s * P.scale);
+            cs[t][(p & 7) * 8 + (p >> 3)] = make_float2(c * P.scale, s * P.scale);
         }
         __syncthreads();
     }
-    for (; row < row1; row += 2 * kAppendRows) {
+    for (; row < rows; row += 2 * kAppendRows) {
         Row c, d;
         load(row + 2 * kAppendRows, c);
         load(row + 3 * kAppendRows, d);
@@ -144,8 +152,16 @@ cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream)
     P.rows_per_block = (int)per;
     const int64_t blocks = (rows + per - 1) / per;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-    k_append<<<(unsigned)blocks, kAppendThreads, 0, stream>>>(P);
-    return cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kAppendThreads);
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_append, P);
 }
 
 }  // namespace kvz

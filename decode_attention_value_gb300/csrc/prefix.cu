@@ -22,7 +22,6 @@ constexpr uint32_t kUnitBytes = kPfxBlock * kDim * 2;  // K or V of a block, BF1
 constexpr uint32_t kHalfBytes = kUnitBytes / 2;        // its 64-column halves
 constexpr uint32_t kQTileBytes = 128 * kDim * 2;       // 128 query rows, BF16
 constexpr uint32_t kQHalfBytes = kQTileBytes / 2;
-constexpr int kExpWarps = 3;  // 12-bit pages: warps that restore K (warps 10 to 12) and V (13 to 15)
 constexpr uint32_t kGroupBytes = kPage * kDim * 2;  // most bytes of a coded (or raw) K or V group
 constexpr int kInfoRing = 8;
 // tensor memory, 256 columns a stream: 128 of scores, each 32 tokens' overwritten by their weights (16
@@ -35,17 +34,21 @@ constexpr uint32_t kColO = 256;
 // alternate blocks and leave separate partials.
 //
 // Raw pages are copied by TMA into the operands' layout.  12-bit pages are copied as they are, a
-// block's eight K groups and eight V groups into stages of their own, and restored by six warps,
-// three for K and three for V: K of the next blocks is read and restored while V waits for room.
-// The softmax
-// threads take most registers, so that a thread's scores and weights stay in them: 168 a thread at
-// launch (64512) become 256 x 208 + 128 x 80 = 63488 for raw pages; 128 (65536) become
-// 256 x 200 + 256 x 56 = 65536 for 12-bit pages.
-template <int kFmt, int kTiles>
+// block's eight K groups and eight V groups into stages of their own, and restored by warps for K and
+// for V: K of the next blocks is read and restored while V waits for room.  (Restored in place, without
+// stages and with a third block in each ring, a 131072-token prefix x 16 sequences took 186 us against
+// 143.)  The softmax threads take most registers: 168 a thread at launch (64512) become 256 x 208 +
+// 128 x 80 = 63488 for raw pages.  For 12-bit pages and two weight parts, 96 (61440) become 256 x 136 +
+// 384 x 64 = 59392, with a producer warp each for K and V and four restoring warps each (one producer
+// and three restoring warps each: 148 us); three parts need more registers, 128 (65536) become 256 x 200
+// + 256 x 56 = 65536.
+template <int kFmt, int kTiles, int kParts>
 struct PfxSmem {
-    static constexpr bool coded = kFmt != kFmtRaw;
-    static constexpr int threads = coded ? 512 : 384;
-    static constexpr int softmax_regs = coded ? 200 : 208, other_regs = coded ? 56 : 80;
+    static constexpr bool coded = kFmt != kFmtRaw, many = coded && kParts == 2;
+    static constexpr int threads = many ? 640 : coded ? 512 : 384;
+    static constexpr int softmax_regs = many ? 136 : coded ? 200 : 208, other_regs = many ? 64 : coded ? 56 : 80;
+    // 12-bit pages: producer warps (8 and, of two, 10), warps that restore K, as many for V behind them
+    static constexpr int producers = many ? 2 : 1, restorers = many ? 4 : 3, restore0 = many ? 11 : 10;
     // rings of K blocks and of V blocks: K's are given back as soon as the scores are made, V's
     // when the weights have been used
     static constexpr int ku = kTiles == 2 ? (coded ? 1 : 2) : (coded ? 2 : 3), vu = coded ? 2 : 3, units = ku + vu;
@@ -54,7 +57,7 @@ struct PfxSmem {
     static constexpr int stages = coded ? 2 * kPfxPages : 0;  // coded groups of a block
     __host__ __device__ static constexpr int slot(int n, int kv) { return kv ? ku + n % vu : n % ku; }
     __host__ __device__ static constexpr uint32_t phase(int n, int kv) { return (kv ? n / vu : n / ku) & 1; }
-    static constexpr int arrivals = coded ? kExpWarps : 1;  // that fill a block
+    static constexpr int arrivals = coded ? restorers : 1;  // that fill a block
     static constexpr int q = 0;
     static constexpr int ring = q + kTiles * (int)kQTileBytes;
     static constexpr int stage = ring + units * (int)kUnitBytes;
@@ -195,10 +198,10 @@ __device__ __forceinline__ uint64_t spread_bits(uint32_t bits)
 __device__ __forceinline__ uint32_t gather_bits(uint64_t bytes) { return (uint32_t)((bytes * 0x0102040810204080ull) >> 56); }
 
 template <int kFmt, int kTiles, int kParts>
-__global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
+__global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
     k_prefix(const PrefixParams P, const __grid_constant__ CUtensorMap tmap)
 {
-    using S = PfxSmem<kFmt, kTiles>;
+    using S = PfxSmem<kFmt, kTiles, kParts>;
     constexpr bool kCoded = S::coded;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
@@ -206,7 +209,6 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         if (threadIdx.x == 0) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
         return;
     }
-    pdl_launch_dependents();  // the own-pages kernel may be placed as CTAs here finish
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int2 *plan = reinterpret_cast<int2 *>(smem + S::plan);
     uint64_t *info = reinterpret_cast<uint64_t *>(smem + S::info);  // a byte per page
@@ -233,6 +235,10 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
         misc[1] = 0;
         fence_barrier_init();
     }
+    // launched while the kernel before it ends: nothing that it wrote is read before this.  The own-pages
+    // kernel may be placed from here on; it reads what was complete before this kernel
+    pdl_wait_primary();
+    pdl_launch_dependents();
     if (warp == 9) tmem_alloc(sbase + S::misc, 512);
     if (warp == 0) {  // units and blocks before each group
         const bool ok = pfx_groups_ok(P, lane);
@@ -332,16 +338,17 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 1000000) {}
         }
-    } else if (warp == 8) {
+    } else if (warp == 8 || (S::producers == 2 && warp == 10)) {
         // ========================= producer, 12-bit pages =========================
-        // Lane p copies the K group of every block's page p, lane 8 + p its V group, each as soon
-        // as its stage is free.  Places and sizes are worked out by the whole warp, 32 pages (four
+        // Lane p copies the K group of every block's page p, lane 8 + p its V group (of two producers:
+        // lane p of the second), each as soon as its stage is free.  Places and sizes are worked out by the whole warp, 32 pages (four
         // blocks) at a time, two batches on hand, and handed to the copying lanes by shuffles; the
         // metadata of the third batch and the ids of the fourth are fetched ahead.  (A lane working
         // out its own group while the others wait took 600 clocks a group.)
         const uint64_t keep = l2_evict_last();
-        const int nb = hi - lo, page = lane & 7, st = lane & 15;
-        const bool is_v = (lane & 8) != 0, copies = lane < 2 * kPfxPages;
+        const int nb = hi - lo, page = lane & 7;
+        const bool is_v = S::producers == 2 ? warp == 10 : (lane & 8) != 0, copies = lane < 2 * kPfxPages / S::producers;
+        const int st = page + (is_v ? kPfxPages : 0);
         struct Pre {
             int32_t id;
             uint32_t what;  // KV head << 16 | valid tokens << 8 | kind
@@ -456,16 +463,16 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles>::threads, 1)
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 1000000) {}
         }
-    } else if (kCoded && warp >= 10) {
+    } else if (kCoded && warp >= S::restore0 && warp < S::restore0 + 2 * S::restorers) {
         // ================== 12-bit pages to BF16 operands ==================
-        const bool is_v = warp >= 10 + kExpWarps;
-        const int w = (warp - 10) % kExpWarps;
+        const bool is_v = warp >= S::restore0 + S::restorers;
+        const int w = (warp - S::restore0) % S::restorers;
         bool ok = true;
         for (int n = 0; n < hi - lo && ok; ++n) {
             const int slot = S::slot(n, is_v);
             ok = __all_sync(0xffffffffu, wait(sbase + S::empty + 8 * slot, S::phase(n, is_v) ^ 1));
             const uint32_t unit = sbase + S::ring + slot * kUnitBytes;
-            for (int page = w; page < kPfxPages && ok; page += kExpWarps) {  // every third page
+            for (int page = w; page < kPfxPages && ok; page += S::restorers) {
                 const int st = (is_v ? kPfxPages : 0) + page;
                 const uint8_t *stage = smem + S::stage + st * kGroupBytes;
                 ok = __all_sync(0xffffffffu, wait(sbase + S::sarrived + 8 * st, n & 1));
@@ -933,7 +940,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
 template <int kFmt, int kTiles, int kParts>
 static cudaError_t launch_prefix_impl(const PrefixParams &P, const CUtensorMap &map, cudaStream_t stream)
 {
-    const int bytes = PfxSmem<kFmt, kTiles>::bytes(P.num_groups);
+    const int bytes = PfxSmem<kFmt, kTiles, kParts>::bytes(P.num_groups);
     // per process and device: the whole shared memory (an attribute of the function)
     static unsigned long long done = 0;  // bit per device ordinal < 64
     int dev = 0;
@@ -943,8 +950,17 @@ static cudaError_t launch_prefix_impl(const PrefixParams &P, const CUtensorMap &
         if (e == cudaSuccess && dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_ACQ_REL);
     }
     if (e != cudaSuccess) return e;
-    k_prefix<kFmt, kTiles, kParts><<<P.grid, PfxSmem<kFmt, kTiles>::threads, bytes, stream>>>(P, map);
-    return cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(P.grid);
+    cfg.blockDim = dim3(PfxSmem<kFmt, kTiles, kParts>::threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_prefix<kFmt, kTiles, kParts>, P, map);
 }
 
 template <int kFmt>

@@ -300,7 +300,8 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
 }
 
-int check_prefix(int batch, const PrefixArgs &X, const void *out, int32_t out_type)
+int check_prefix(int batch, const PrefixArgs &X, const int32_t *page_ids, const int32_t *seq_lens, const void *out,
+                 int32_t out_type)
 {
     if (X.groups < 0 || X.max_pages < 0) return KVZ_ERR_INVALID_ARG;
     if (out_type != KVZ_OUT_F32 && out_type != KVZ_OUT_BF16) return KVZ_ERR_INVALID_ARG;
@@ -308,7 +309,7 @@ int check_prefix(int batch, const PrefixArgs &X, const void *out, int32_t out_ty
     if (batch == 0) return KVZ_OK;
     if (X.groups > 0 && (!X.group_start || !X.lens || (X.max_pages > 0 && !X.ids))) return KVZ_ERR_INVALID_ARG;
     if (!aligned(X.group_start, 4) || !aligned(X.lens, 4) || !aligned(X.ids, 4) || !aligned(X.tail, 4) ||
-        !aligned(out, 16))
+        !aligned(page_ids, 4) || !aligned(seq_lens, 4) || !aligned(out, 16))
         return KVZ_ERR_ALIGNMENT;
     return KVZ_OK;
 }
@@ -833,7 +834,7 @@ int kvz_prefix_attention(kvz_dims dims, int32_t batch, int32_t num_q_heads, cons
     const PrefixArgs X{num_groups, group_start, prefix_ids, max_prefix_pages, prefix_lens, prefix_tail};
     int rc = check_attention_common(dims, batch, num_q_heads, q, seq_lens, raw_pool, num_raw_pages,
                                     static_cast<const float *>(out), workspace, status, max_pages, page_ids);
-    if (!rc) rc = check_prefix(batch, X, out, out_type);
+    if (!rc) rc = check_prefix(batch, X, page_ids, seq_lens, out, out_type);
     if (rc || batch == 0) return rc;
     if (!tail_page || !meta || !arena || num_meta_pages < 0 || (num_groups > 0 && !prefix_tail))
         return KVZ_ERR_INVALID_ARG;
@@ -854,7 +855,7 @@ int kvz_prefix_attention_raw(kvz_dims dims, int32_t batch, int32_t num_q_heads, 
     const PrefixArgs X{num_groups, group_start, prefix_ids, max_prefix_pages, prefix_lens, nullptr};
     int rc = check_attention_common(dims, batch, num_q_heads, q, seq_lens, raw_pool, num_raw_pages,
                                     static_cast<const float *>(out), workspace, status, max_pages, page_ids);
-    if (!rc) rc = check_prefix(batch, X, out, out_type);
+    if (!rc) rc = check_prefix(batch, X, page_ids, seq_lens, out, out_type);
     if (rc || batch == 0) return rc;
     return run_prefix_attention(FormatArgs{kFmtRaw, nullptr, nullptr, nullptr}, dims, batch, num_q_heads, q, X,
                                 page_ids, max_pages, seq_lens, nullptr, 0, nullptr, 0, raw_pool, num_raw_pages, out,

@@ -222,14 +222,17 @@ int run_attention(const FormatArgs &F, const kvz_dims &d, int batch, int hq, con
     return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
 }
 
-// CTAs of the prefix kernel: one per SM, at most one per block of the longest prefixes.
+// CTAs of the prefix kernel: one per SM, at most one per block of the longest prefixes, or, where its two
+// streams take alternate blocks, per two: they run side by side, and the SMs left over compute the own
+// tokens meanwhile (32 sequences behind 2055 tokens: 72 CTAs instead of 136).
 int prefix_grid(int batch, int hkv, int G, int groups, int prefix_pages, int *grid)
 {
     const int sms = sm_count();
     if (sms < 1) return KVZ_ERR_DEVICE;
-    const int64_t blocks = pfx_max_units(batch, hkv, G, groups) * (((int64_t)prefix_pages + 7) / 8);
-    if (blocks > INT32_MAX) return KVZ_ERR_UNSUPPORTED;
-    *grid = groups > 0 ? (int)(blocks < sms ? blocks : sms) : 0;
+    const int64_t units = pfx_max_units(batch, hkv, G, groups), deep = ((int64_t)prefix_pages + 7) / 8;
+    if (units * deep > INT32_MAX) return KVZ_ERR_UNSUPPORTED;
+    const int64_t want = units * (pfx_unit_rows(batch, G, groups) == 128 ? (deep + 1) / 2 : deep);
+    *grid = groups > 0 ? (int)(want < sms ? want : sms) : 0;
     return KVZ_OK;
 }
 
@@ -279,6 +282,7 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     // last bit, 2^-25 of the sum: 8 blocks keep a float32 output within 2^-18 of that bias, 256
     // keep it under a BF16 output's rounding (2^-9 a value)
     P.fold = out_type == KVZ_OUT_BF16 ? 256 : 8;
+    P.over_G = 0xFFFFFFFFu / (uint32_t)G + 1;
     P.q = static_cast<const uint16_t *>(q);
     P.group_start = X.group_start;
     P.prefix_ids = X.ids;

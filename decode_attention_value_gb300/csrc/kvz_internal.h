@@ -134,6 +134,7 @@ struct PrefixParams {
     int unit_rows;   // query rows of a CTA's tile: 128 or 256
     int grid;        // CTAs
     int fold;        // blocks of a stream summed in tensor memory at a time
+    uint32_t over_G;  // ceil(2^32 / G): the high half of its product with a row is the row's sequence (G > 1)
     const uint16_t *q;
     const int32_t *group_start, *prefix_ids, *prefix_lens, *prefix_tail;
     const uint64_t *meta;
@@ -142,7 +143,7 @@ struct PrefixParams {
     uint64_t arena_bytes;
     const uint16_t *raw_pool;
     int64_t num_raw_pages;
-    float *part_o;   // [slots][2][128][128]: slot = unit + CTA, then stream, row of the tile
+    float *part_o;   // [slots][2][4][16][32][8]: slot = unit + CTA, stream, 32 rows of the tile, 8 columns, row
     float *part_ml;  // [slots][2][128][2]
     void *out;
     bool out_bf16;

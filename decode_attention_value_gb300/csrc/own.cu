@@ -31,6 +31,8 @@ constexpr int kOwnResident = 6;  // blocks an SM holds with one stage a warp
 // The warps' stages, which hold their states afterwards, and a barrier each.
 __host__ __device__ constexpr int own_ring(int stages) { return kOwnWarps * stages * kOwnPageBytes; }
 __host__ __device__ constexpr int own_smem(int stages) { return own_ring(stages) + kOwnWarps * stages * 8; }
+constexpr int kOwnStates = kOwnWarps * 8 * kDim * 4;
+static_assert(own_ring(1) == kOwnStates + kOwnWarps * 8 * kDim * 4, "room for eight partials a warp");
 static_assert(kOwnPages + 1 <= 32 * kOwnWarps, "a lane resolves one page");
 
 template <int kFmt, bool kG8, bool kThird>
@@ -281,6 +283,9 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
     // ---- a head at a time: the states, then the prefix's partials ----
     const int share = G == 1 ? 4 : G == 2 ? 2 : 1;  // warps of a head
     const int part = warp % share;
+    // shared memory behind the states: outputs of prefix partials, 8, 24 or 32 a warp
+    const int most_items = min(32, 16 * stages - 8);
+    const uint32_t items = sbase + kOwnStates + warp * most_items * kDim * 4 + lane * 16;
     PfxItems pre = pfx_items(P, where, b, kvh, min(warp / share, G - 1));
     if (after) pdl_wait_primary();  // the prefix partials are complete
     for (int h0 = 0; h0 < G; h0 += kOwnWarps / share) {  // (uniform: the barrier below)
@@ -291,13 +296,25 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
                 for (int w = 0; w < kOwnWarps; ++w)
                     sum.add(wml[w][h].x, wml[w][h].y, *reinterpret_cast<const float4 *>(states + (w * 8 + h) * kDim + 4 * lane));
             if (h0 > 0) pre = pfx_items(P, where, b, kvh, h);
-            for (int i0 = part; i0 < pre.n; i0 += 32 * share) {
-                const int i = i0 + lane * share;
+            // the prefix's: as many at once as the warp's part of the ring holds, copied while their maxima come
+            const int64_t step = (int64_t)share * pre.step;
+            int64_t row = pre.first + (int64_t)part * pre.step;
+            for (int left = (pre.n - part + share - 1) / share; left > 0; left -= most_items, row += most_items * step) {
+                const int count = min(most_items, left);
+                const float4 *from = pfx_part(P, row, lane);
+#pragma unroll 4
+                for (int k = 0; k < count; ++k, from += step * (kDim / 4)) cp_async_16(items + k * (kDim * 4), from);
                 float2 e = make_float2(-INFINITY, 0.f);
-                if (i < pre.n) e = *reinterpret_cast<const float2 *>(P.part_ml + pre.row(i) * 2);
-                sum.add(e.x, e.y, min(32, (pre.n - i0 + share - 1) / share), [&](int k) {
-                    return reinterpret_cast<const float4 *>(P.part_o + pre.row(i0 + k * share) * kDim)[lane];
-                });
+                if (lane < count) e = *reinterpret_cast<const float2 *>(P.part_ml + (row + lane * step) * 2);
+                const RowSum::Join j = sum.join(e.x, e.y);
+                cp_async_wait_all();
+                const float4 *at = reinterpret_cast<const float4 *>(smem + (items - sbase));
+#pragma unroll 4
+                for (int k = 0; k < count; ++k) {
+                    float4 v = at[k * (kDim / 4)];
+                    if (!(j.have >> k & 1)) v = make_float4(0.f, 0.f, 0.f, 0.f);  // (was not written)
+                    sum.take(v, __shfl_sync(0xffffffffu, j.w, k));
+                }
             }
         }
         if (share > 1) {  // (one turn: G <= 2)

@@ -73,7 +73,7 @@ struct PfxSmem {
     static constexpr int sempty = sarrived + stages * 8;
     static constexpr int sinfo = sempty + stages * 8;
     static constexpr int info = sinfo + stages * 8;   // [kInfoRing][8] bad pages of a block
-    static constexpr int misc = info + kInfoRing * 8;  // tensor memory address, abort flag
+    static constexpr int misc = info + kInfoRing * 8;  // tensor memory address, abort flag, busy CTAs
     static constexpr int plan = misc + 16;  // [groups + 1] {first unit, first block}
     static int bytes(int groups) { return plan + (groups + 1) * 8; }
 };
@@ -245,14 +245,17 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
         if (!ok && lane == 0) atomicOr(P.status, KVZ_STATUS_BAD_ORDER);
         const int per = (P.num_groups + 31) / 32;
         const int g0 = min(P.num_groups, lane * per), g1 = min(P.num_groups, g0 + per);
-        int u = 0, w = 0;
+        int u = 0, w = 0, busy = 0;
         uint32_t bad = 0;
         for (int g = g0; g < g1 && ok; ++g) {
             const PfxGroup r = pfx_group(P, g);
             bad |= P.prefix_lens[g] != r.len;
             u += P.hkv * r.tiles;
             w += P.hkv * r.tiles * r.blocks;
+            busy += P.hkv * r.tiles * pfx_unit_ctas(P, r.blocks);
         }
+        busy = __reduce_add_sync(0xffffffffu, busy);
+        if (lane == 0) misc[2] = (uint32_t)busy;
         if (bad) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
         int su = u, sw = w;
 #pragma unroll
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    const int W = plan[P.num_groups].y, C = min((int)gridDim.x, W), c = blockIdx.x;
+    const int W = plan[P.num_groups].y, C = min((int)gridDim.x, (int)misc[2]), c = blockIdx.x;
     const int lo = c < C ? pfx_first(c, W, C) : 0, hi = c < C ? pfx_first(c + 1, W, C) : 0;
     PfxWait wait{P.status, misc + 1, true};
 
@@ -364,15 +367,14 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
                        (uint32_t)s.kvh << 16 | (uint32_t)min(kPage, s.len - p * kPage) << 8 |
                            (coded ? kGroupCoded : kGroupRaw)};
         };
-        uint64_t mk = 0, mv = 0;
-        auto load_meta = [&](const Pre &r) {
+        auto load_meta = [&](const Pre &r, uint64_t &mk, uint64_t &mv) {
             if ((r.what & 0xFFu) == kGroupCoded && r.id >= 0 && r.id < P.num_meta_pages)
                 ld_keep_u64x2(P.meta + ((int64_t)r.id * P.hkv + (r.what >> 16)) * 2, keep, mk, mv);
         };
         struct Place {
             uint32_t what, offk, offv, tk, tv;  // raw: offk = index of the K and V pair
         };
-        auto resolve = [&](const Pre &r) -> Place {  // from the metadata in mk, mv
+        auto resolve = [&](const Pre &r, uint64_t mk, uint64_t mv) -> Place {
             Place q{r.what & 0xFFFFu, (uint32_t)mk, (uint32_t)mv, (uint32_t)(mk >> 32), (uint32_t)(mv >> 32)};
             uint32_t flag = 0;
             if ((q.what & 0xFFu) == kGroupCoded) {
@@ -392,16 +394,13 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
             }
             return q;
         };
-        Pre third = prep(lane), fourth = prep(32 + lane);
-        load_meta(third);
-        Place a = resolve(third);
-        third = fourth;
-        load_meta(third);
-        fourth = prep(64 + lane);
-        Place b = resolve(third);
-        third = fourth;
-        load_meta(third);
-        fourth = prep(96 + lane);
+        const Pre first = prep(lane), second = prep(32 + lane);
+        Pre third = prep(64 + lane), fourth = prep(96 + lane);
+        uint64_t mk[3] = {0, 0, 0}, mv[3] = {0, 0, 0};
+        load_meta(first, mk[0], mv[0]);
+        load_meta(second, mk[1], mv[1]);
+        load_meta(third, mk[2], mv[2]);
+        Place a = resolve(first, mk[0], mv[0]), b = resolve(second, mk[1], mv[1]);
         const uint32_t emptybar = sbase + S::sempty + 8 * st, bar = sbase + S::sarrived + 8 * st;
         uint64_t since = 0;
         bool ok = true;
@@ -441,9 +440,9 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
                 if (__all_sync(0xffffffffu, n >= min(nb, 4 * (batch + 1)))) {  // every lane is done with `a`
                     ++batch;
                     a = b;
-                    b = resolve(third);
+                    b = resolve(third, mk[2], mv[2]);
                     third = fourth;
-                    load_meta(third);
+                    load_meta(third, mk[2], mv[2]);
                     fourth = prep(32 * (batch + 3) + lane);
                 }
             } else if ((++idle & 1023) == 0) {  // bounded: give up after kWaitLimitNs without a step
@@ -624,9 +623,10 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
             for (int i = 0; i < 8 * kTiles; ++i) {
                 const int row = (tid >> 4) + 16 * i, grow = sg.tile * P.unit_rows + row;
                 qv[i] = make_uint4(0, 0, 0, 0);
+                const int seq = P.G == 1 ? grow : (int)__umulhi(grow, P.over_G);
                 if (row < sg.rows)
                     qv[i] = *reinterpret_cast<const uint4 *>(
-                        P.q + ((int64_t)(sg.seq0 + grow / P.G) * P.hkv * P.G + sg.kvh * P.G + grow % P.G) * kDim + ch * 8);
+                        P.q + ((int64_t)(sg.seq0 + seq) * P.hkv * P.G + sg.kvh * P.G + grow - seq * P.G) * kDim + ch * 8);
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll
@@ -643,48 +643,25 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
             const int rows = min(32, sg.rows - row0 - quad * 32);
             float m = -INFINITY, l = 0.f;
             // The warp's 32 rows of output, complete in tensor memory and relative to maximum ref,
-            // added to their partials, 32 columns at a time.
+            // added to their partials, 32 columns at a time, each lane its row.  The partials of 32 rows are
+            // laid out [8 columns][row], so that a store of the warp writes whole lines.
             float fm = 0.f;  // the partials' maximum
             bool folded = false;
-            auto fold = [&](float ref, uint8_t *stage) {
+            auto fold = [&](float ref) {
                 const float f = !folded || fm == -INFINITY ? 0.f : ex2(fm - ref);
 #pragma unroll 1
                 for (int w = 0; w < 4; ++w) {
                     uint32_t o[32];
                     tmem_ld32(tO + 32 * w, o);
                     tmem_wait_ld(o);
-                    if (!stage) {  // within a segment: each lane its row
-                        if (lane >= rows) continue;
-                        float *at = P.part_o + (slot0 + lane) * kDim + 32 * w;
+                    if (lane >= rows) continue;
+                    float *at = P.part_o + slot0 * kDim + (4 * w * 32 + lane) * 8;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i, at += 32 * 8) {
                         if (folded)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(fmaf(at[i], f, __uint_as_float(o[i])));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) st_global_32b(at + 8 * i, o + 8 * i);
-                        continue;
-                    }
-                    // at its end: through 4 KB of the queries' shared memory, so that memory sees
-                    // whole lines (32-byte stores to 32 rows an instruction took 2.5 us a tile)
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = 4 * i + (lane >> 3), col = lane & 7;
-                        float4 y = *reinterpret_cast<const float4 *>(stage + row * 128 + ((col ^ (row & 7)) << 4));
-                        const float fr = __shfl_sync(0xffffffffu, f, row);
-                        if (row < rows) {
-                            float4 *at = reinterpret_cast<float4 *>(P.part_o + (slot0 + row) * kDim + 32 * w) + col;
-                            if (folded) {
-                                const float4 z = *at;
-                                y = make_float4(fmaf(z.x, fr, y.x), fmaf(z.y, fr, y.y), fmaf(z.z, fr, y.z),
-                                                fmaf(z.w, fr, y.w));
-                            }
-                            *at = y;
-                        }
+                            for (int k = 0; k < 8; ++k) o[8 * i + k] = __float_as_uint(fmaf(at[k], f, __uint_as_float(o[8 * i + k])));
+                        st_global_32b(at, o + 8 * i);
                     }
                 }
                 fm = ref;
@@ -700,7 +677,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
                 // (the products behind these scores were issued after every earlier product of the
                 // stream, so its output is complete)
                 const bool fresh = mine % P.fold == 0;  // the output begins anew
-                if (fresh && mine > 0 && active) fold(m, nullptr);
+                if (fresh && mine > 0 && active) fold(m);
                 const int left = sg.len - (sg.block0 + j) * kPfxBlock;
                 const uint32_t bad = gather_bits(info[n % kInfoRing]);
                 const bool whole = left >= kPfxBlock && bad == 0;
@@ -836,10 +813,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
                 ophase ^= 1;
                 tc_fence_after();
             }
-            // (one tile: the other stream's last scores have read the queries too)
-            if (kTiles == 1) asm volatile("bar.sync 2, 256;" ::: "memory");
-            if (mine > 0 && active && __all_sync(0xffffffffu, wait.ok))
-                fold(m, smem + S::q + (kTiles == 2 ? s * kQTileBytes : 0) + (kTiles == 2 ? quad : warp) * 4096);
+            if (mine > 0 && active && __all_sync(0xffffffffu, wait.ok)) fold(m);
             tc_fence_before();
             if (lane < rows) *reinterpret_cast<float2 *>(P.part_ml + (slot0 + lane) * 2) = make_float2(m, l);
             x += nb;
@@ -893,7 +867,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
     }
     const int share = P.G > 4 ? 1 : P.G > 2 ? 2 : P.G > 1 ? 4 : 8;  // warps of a head
     const int hg = warp / share, part = warp % share;
-    PfxItems pre{0, 1, 0, 0};
+    PfxItems pre{0, 0, 0};
     if (hg < P.G) pre = pfx_items(P, where, b, kvh, hg);
     // own items: CTAs of the split kernel that hold pages of (b, kvh)
     const int64_t T = (int64_t)P.hkv * v[2], AC = A.grid;
@@ -914,14 +888,14 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
             const int64_t cc = a0 + (mine - pre.n);
             // (a CTA of the split kernel without pages wrote nothing)
             if (mine < pre.n)
-                e = *reinterpret_cast<const float2 *>(P.part_ml + pre.row(mine) * 2);
+                e = *reinterpret_cast<const float2 *>(P.part_ml + (pre.first + (int64_t)mine * pre.step) * 2);
             else if (T >= AC || (cc * T + AC - 1) / AC < ((cc + 1) * T + AC - 1) / AC)
                 e = *reinterpret_cast<const float2 *>(A.part_ml + own_row(mine - pre.n) * 2);
         }
-        sum.add(e.x, e.y, min(32, (items - i0 + share - 1) / share), [&](int k) {
+        sum.add(e.x, e.y, [&](int k) {
             const int i = i0 + k * share;
-            const float *o = i < pre.n ? P.part_o + pre.row(i) * kDim : A.part_o + own_row(i - pre.n) * kDim;
-            return reinterpret_cast<const float4 *>(o)[lane];
+            return i < pre.n ? *pfx_part(P, pre.first + (int64_t)i * pre.step, lane)
+                             : reinterpret_cast<const float4 *>(A.part_o + own_row(i - pre.n) * kDim)[lane];
         });
     }
     if (share > 1) {

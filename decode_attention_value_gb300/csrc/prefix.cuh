@@ -33,18 +33,25 @@ __device__ __forceinline__ bool pfx_groups_ok(const PrefixParams &P, int lane)
     return __all_sync(0xffffffffu, ok);
 }
 
+// CTAs that a unit of `blocks` blocks keeps busy: where the two streams take alternate blocks, one per
+// two blocks (they run side by side, and the SMs left over compute the own tokens meanwhile).
+__device__ __forceinline__ int pfx_unit_ctas(const PrefixParams &P, int blocks)
+{
+    return P.unit_rows == 128 ? (blocks + 1) / 2 : blocks;
+}
+
 // First block of CTA c's range of W blocks over C CTAs.
 __device__ __forceinline__ int pfx_first(int c, int W, int C) { return (int)(((int64_t)c * W + C - 1) / C); }
 
-// Where the prefix partials of sequence b's rows are: units and blocks before its group, blocks in
-// all, the group (-1: none).  One warp, from group starts and lengths alone.
+// Where the prefix partials of sequence b's rows are: units and blocks before its group, blocks and
+// CTAs in all, the group (-1: none).  One warp, from group starts and lengths alone.
 struct PfxPlace {
-    int units, blocks, all, group;
+    int units, blocks, all, ctas, group;
 };
 
 __device__ __forceinline__ PfxPlace pfx_place(const PrefixParams &P, int b, int lane)
 {
-    PfxPlace r{0, 0, 0, -1};
+    PfxPlace r{0, 0, 0, 0, -1};
     if (P.num_groups == 0 || !pfx_groups_ok(P, lane)) return r;
     for (int g = lane; g < P.num_groups; g += 32) {
         const PfxGroup s = pfx_group(P, g);
@@ -56,56 +63,66 @@ __device__ __forceinline__ PfxPlace pfx_place(const PrefixParams &P, int b, int 
             r.group = g;
         }
         r.all += n * s.blocks;
+        r.ctas += n * pfx_unit_ctas(P, s.blocks);
     }
     r.units = __reduce_add_sync(0xffffffffu, r.units);
     r.blocks = __reduce_add_sync(0xffffffffu, r.blocks);
     r.all = __reduce_add_sync(0xffffffffu, r.all);
+    r.ctas = min(P.grid, __reduce_add_sync(0xffffffffu, r.ctas));
     r.group = __reduce_max_sync(0xffffffffu, r.group);
     return r;
 }
 
-// The prefix partials of query head hg (within its KV head) of sequence b: item i is a row of
-// part_o and part_ml.
+// The prefix partials of query head hg (within its KV head) of sequence b: item i is row
+// first + i * step of part_o and part_ml.
 struct PfxItems {
-    int n, streams, stream;  // a tile's CTAs leave one or two partials of a row
-    int64_t first;           // row of the first CTA's
-    __device__ __forceinline__ int64_t row(int i) const
-    {
-        const int cta = streams == 2 ? i >> 1 : i, s = streams == 2 ? i & 1 : stream;
-        return first + (int64_t)(2 * cta + s) * 128;
-    }
+    int n, step;  // (step: a multiple of 32)
+    int64_t first;
 };
 
 __device__ __forceinline__ PfxItems pfx_items(const PrefixParams &P, const PfxPlace &w, int b, int kvh, int hg)
 {
-    PfxItems r{0, P.unit_rows == 128 ? 2 : 1, 0, 0};
+    // a tile's CTAs leave two partials of a row, or one of the row's stream
+    const bool both = P.unit_rows == 128;
+    PfxItems r{0, both ? 128 : 256, 0};
     if (w.group < 0) return r;
     const PfxGroup s = pfx_group(P, w.group);
     if (s.blocks == 0) return r;
     const int all = (b - s.seq0) * P.G + hg, tile = all / P.unit_rows, row = all - tile * P.unit_rows;
-    const int ui = kvh * s.tiles + tile, C = min(P.grid, w.all);
+    const int ui = kvh * s.tiles + tile, C = w.ctas;
     const int64_t first = w.blocks + (int64_t)ui * s.blocks, last = first + s.blocks - 1;
     const int c0 = (int)(first * C / w.all), c1 = (int)(last * C / w.all);
-    r.n = (c1 - c0 + 1) * r.streams;
-    r.stream = row >> 7;
-    r.first = (int64_t)(w.units + ui + c0) * 2 * 128 + (row & 127);
+    r.n = (c1 - c0 + 1) * (both ? 2 : 1);
+    r.first = (int64_t)(w.units + ui + c0) * 2 * 128 + row;
     return r;
+}
+
+// 16 bytes from global to shared memory, asynchronously; the thread that asked may read them after
+// cp_async_wait_all.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Columns 4 lane .. 4 lane + 3 of a row of part_o, which holds 32 rows as [8 columns][row].
+__device__ __forceinline__ const float4 *pfx_part(const PrefixParams &P, int64_t row, int lane)
+{
+    return reinterpret_cast<const float4 *>(P.part_o + (row & ~31ll) * kDim + ((lane >> 1) * 32 + (row & 31)) * 8 + (lane & 1) * 4);
 }
 
 // A row's partials merged as they come: running maximum, sum and (four columns a lane) output.
 struct RowSum {
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // up to 32 partials (lane k: maximum and sum of the k-th, -inf for one without tokens) whose
-    // outputs load(k) brings, eight at a time.  Up to eight are loaded before the maxima are known, of
-    // more only those with tokens: a tile's CTA with one block leaves an empty partial beside it.
-    template <class Load>
-    __device__ __forceinline__ void add(float pm, float pl, int n, const Load &load)
+    // Up to 32 partials join (lane k: maximum and sum of the k-th, -inf for one without tokens): the
+    // lane's factor of its partial's output, and which have tokens (the others' were not written).
+    struct Join {
+        float w;
+        uint32_t have;
+    };
+    __device__ __forceinline__ Join join(float pm, float pl)
     {
-        float4 x[8];
-        if (n <= 8)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = k < n ? load(k) : make_float4(0.f, 0.f, 0.f, 0.f);
         float top = pm;
 #pragma unroll
         for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -115,36 +132,36 @@ struct RowSum {
         float sum = none ? 0.f : w * pl;
 #pragma unroll
         for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        uint32_t have = __ballot_sync(0xffffffffu, !none);
         l = l * f + sum;
         o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
         m = top;
-        auto take = [&](const float4 &v, float wk) {
-            o.x += wk * v.x;
-            o.y += wk * v.y;
-            o.z += wk * v.z;
-            o.w += wk * v.w;
-        };
-        if (n <= 8) {
+        return Join{w, __ballot_sync(0xffffffffu, !none)};
+    }
+    __device__ __forceinline__ void take(const float4 &v, float w)
+    {
+        o.x += w * v.x;
+        o.y += w * v.y;
+        o.z += w * v.z;
+        o.w += w * v.w;
+    }
+    // the same with outputs that load(k) brings, eight at a time
+    template <class Load>
+    __device__ __forceinline__ void add(float pm, float pl, const Load &load)
+    {
+        Join j = join(pm, pl);
+        while (j.have) {
+            float4 x[8];
+            float w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                if (have >> k & 1) take(x[k], wk);  // (one without tokens was not written)
-            }
-            return;
-        }
-        while (have) {
-            float wk[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int at = __ffs(have) - 1;  // -1: none left
-                wk[k] = __shfl_sync(0xffffffffu, w, at & 31);
-                if (at < 0) wk[k] = 0.f;
+                const int at = __ffs(j.have) - 1;  // -1: none left
+                w[k] = __shfl_sync(0xffffffffu, j.w, at & 31);
+                if (at < 0) w[k] = 0.f;
                 x[k] = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : load(at);
-                have &= have - 1;
+                j.have &= j.have - 1;
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) take(x[k], wk[k]);
+            for (int k = 0; k < 8; ++k) take(x[k], w[k]);
         }
     }
     // another warp's

@@ -27,6 +27,7 @@ namespace kvz {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = kAppendThreads / 8;  // rows a block handles at once
 constexpr int kAppendTokens = 8;                 // tokens a block may touch
+constexpr int kAppendResident = 3;               // blocks an SM holds
 
 // cs: the first of the eight pairs' (cos, sin), the next ones eight further each
 __device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float2 *cs, bool neighbours)
@@ -52,7 +53,7 @@ __device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float2 *cs, bo
     }
 }
 
-__global__ void __launch_bounds__(kAppendThreads) k_append(const AppendParams P)
+__global__ void __launch_bounds__(kAppendThreads, kAppendResident) k_append(const AppendParams P)
 {
     __shared__ float2 cs[kAppendTokens][64];
     const int H = P.hq + 2 * P.hkv, tid = threadIdx.x;
@@ -144,9 +145,11 @@ cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream)
 {
     const int H = P.hq + 2 * P.hkv;
     const int64_t rows = (int64_t)P.tokens * H;
-    // few rows: one pass of a block each, spread over the SMs; many: eight passes a block, so
-    // that a block's sines serve whole tokens
-    int64_t per = rows <= (int64_t)kAppendRows * 4 * sms ? kAppendRows : 8 * kAppendRows;
+    // passes of a block: as few as let one wave hold all rows, at most eight (whole tokens share their
+    // sines), and even, since a thread keeps two rows in flight (1021 tokens of 48 rows: 7.4 us with eight)
+    int64_t passes = (rows + (int64_t)kAppendRows * kAppendResident * sms - 1) / ((int64_t)kAppendRows * kAppendResident * sms);
+    passes = passes <= 1 ? 1 : passes >= 8 ? 8 : (passes + 1) & ~1ll;
+    int64_t per = passes * kAppendRows;
     const int64_t most = (int64_t)(kAppendTokens - 2) * H + 1;  // touches at most kAppendTokens tokens
     if (per > most) per = most;
     P.rows_per_block = (int)per;

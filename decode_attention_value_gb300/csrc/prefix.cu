@@ -241,18 +241,25 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
     pdl_launch_dependents();
     if (warp == 9) tmem_alloc(sbase + S::misc, 512);
     if (warp == 0) {  // units and blocks before each group
-        const bool ok = pfx_groups_ok(P, lane);
-        if (!ok && lane == 0) atomicOr(P.status, KVZ_STATUS_BAD_ORDER);
+        bool ok = true;  // starts in order and in range
         const int per = (P.num_groups + 31) / 32;
         const int g0 = min(P.num_groups, lane * per), g1 = min(P.num_groups, g0 + per);
         int u = 0, w = 0, busy = 0;
         uint32_t bad = 0;
-        for (int g = g0; g < g1 && ok; ++g) {
-            const PfxGroup r = pfx_group(P, g);
-            bad |= P.prefix_lens[g] != r.len;
+        for (int g = g0; g < g1; ++g) {
+            const int start = P.group_start[g], end = P.group_start[g + 1], len = P.prefix_lens[g];
+            const PfxGroup r = pfx_group(P, start, end, len);
+            ok &= 0 <= start && start <= end && end <= P.batch;
+            bad |= len != r.len;
             u += P.hkv * r.tiles;
             w += P.hkv * r.tiles * r.blocks;
             busy += P.hkv * r.tiles * pfx_unit_ctas(P, r.blocks);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+            if (lane == 0) atomicOr(P.status, KVZ_STATUS_BAD_ORDER);
+            u = w = busy = 0;
+            bad = 0;
         }
         busy = __reduce_add_sync(0xffffffffu, busy);
         if (lane == 0) misc[2] = (uint32_t)busy;
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
         int ru = su - u, rw = sw - w;
         for (int g = g0; g < g1; ++g) {
             plan[g] = make_int2(ru, rw);
-            if (!ok) continue;
+            if (!ok || g + 1 == g1) continue;
             const PfxGroup r = pfx_group(P, g);
             ru += P.hkv * r.tiles;
             rw += P.hkv * r.tiles * r.blocks;

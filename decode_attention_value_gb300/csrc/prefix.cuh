@@ -13,24 +13,19 @@ struct PfxGroup {
     int seq0, seqs, len, blocks, tiles;
 };
 
-__device__ __forceinline__ PfxGroup pfx_group(const PrefixParams &P, int g)
+__device__ __forceinline__ PfxGroup pfx_group(const PrefixParams &P, int start, int end, int len)
 {
     PfxGroup r;
-    r.seq0 = P.group_start[g];
-    r.seqs = P.group_start[g + 1] - r.seq0;
-    r.len = min(max(P.prefix_lens[g], 0), P.max_tokens);
+    r.seq0 = start;
+    r.seqs = end - start;
+    r.len = min(max(len, 0), P.max_tokens);
     r.blocks = r.len / kPfxBlock + (r.len % kPfxBlock != 0);
     r.tiles = r.blocks > 0 ? (r.seqs * P.G + P.unit_rows - 1) / P.unit_rows : 0;
     return r;
 }
-
-// One warp: group starts ordered and in range?
-__device__ __forceinline__ bool pfx_groups_ok(const PrefixParams &P, int lane)
+__device__ __forceinline__ PfxGroup pfx_group(const PrefixParams &P, int g)
 {
-    bool ok = true;
-    for (int g = lane; g < P.num_groups; g += 32) ok &= P.group_start[g] <= P.group_start[g + 1];
-    ok &= P.group_start[0] >= 0 && P.group_start[P.num_groups] <= P.batch;
-    return __all_sync(0xffffffffu, ok);
+    return pfx_group(P, P.group_start[g], P.group_start[g + 1], P.prefix_lens[g]);
 }
 
 // CTAs that a unit of `blocks` blocks keeps busy: where the two streams take alternate blocks, one per
@@ -52,10 +47,13 @@ struct PfxPlace {
 __device__ __forceinline__ PfxPlace pfx_place(const PrefixParams &P, int b, int lane)
 {
     PfxPlace r{0, 0, 0, 0, -1};
-    if (P.num_groups == 0 || !pfx_groups_ok(P, lane)) return r;
+    if (P.num_groups == 0) return r;
+    bool ok = true;  // starts in order and in range
     for (int g = lane; g < P.num_groups; g += 32) {
-        const PfxGroup s = pfx_group(P, g);
+        const int start = P.group_start[g], end = P.group_start[g + 1];
+        const PfxGroup s = pfx_group(P, start, end, P.prefix_lens[g]);
         const int n = P.hkv * s.tiles;
+        ok &= 0 <= start && start <= end && end <= P.batch;
         if (s.seq0 + s.seqs <= b) {
             r.units += n;
             r.blocks += n * s.blocks;
@@ -65,6 +63,7 @@ __device__ __forceinline__ PfxPlace pfx_place(const PrefixParams &P, int b, int 
         r.all += n * s.blocks;
         r.ctas += n * pfx_unit_ctas(P, s.blocks);
     }
+    if (!__all_sync(0xffffffffu, ok)) return PfxPlace{0, 0, 0, 0, -1};
     r.units = __reduce_add_sync(0xffffffffu, r.units);
     r.blocks = __reduce_add_sync(0xffffffffu, r.blocks);
     r.all = __reduce_add_sync(0xffffffffu, r.all);

@@ -10,7 +10,8 @@
 // multiplication), so far positions lose nothing; the top 32 bits, 2^-32 turn = 1.5e-9 rad,
 // go through sincospif.
 //
-// Bound: memory.  (Hq + 2 Hkv) 256 bytes a token are read once and written once.
+// Bound: memory.  (Hq + 2 Hkv) 256 bytes a token are read once and written once: 16381 tokens of 48
+// heads in 69 us, 5.7 TB/s, 0.85 of the measured copy bandwidth; one decode token is a launch.
 //
 // Layout: a row is one head of one token, 256 bytes, handled by eight lanes: each holds two
 // 16-byte vectors, eight whole rotary pairs in either pairing.  A block takes a run of

@@ -5,9 +5,19 @@
 // of one matrix Q.  Over the group's prefix, S = Q K^T and O = exp2(S c - m) V are matrix
 // products with many rows, so they run on the tcgen05 tensor cores instead of once per
 // sequence: the bytes of the prefix are read n times less often, and the arithmetic per byte
-// grows with n G.  Each sequence's own pages go through the split kernel of attention.cu.
-// Both leave partial results (running maximum m, sum l, unnormalised O) and one merge adds
-// them: sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, in a fixed order.
+// grows with n G.  The kernel leaves partial results (running maximum m, sum l, unnormalised
+// O), which are added in a fixed order: sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, for up
+// to 1024 own tokens a sequence by the kernel that computes those (own.cu), else, with the
+// partials of attention.cu's split kernel over the own pages, by the merge below.
+//
+// Bound: with many rows the tensor cores (256 rows a CTA: 85 clocks a product that takes 64, 56% of
+// the pipe's time over the launch; 128 x 8 heads behind 16384 tokens: 71 us of 91); with few rows the
+// bytes of the prefix for raw pages (131072 tokens x 32 sequences: 5.3 TB/s), the restoring of groups
+// for 12-bit ones (131072 x 16: 3.0 TB/s); for short prefixes a chain of about 8 us: group table, page
+// ids, pages, scores, weights, output.
+//
+// Split: a unit is (group, KV head, tile of 128 or 256 rows); the units' blocks of 128 tokens are one
+// line, cut into equal ranges, a CTA each, so that any mix of groups keeps all SMs busy.
 #include <cuda.h>
 
 #include <cstring>

@@ -254,11 +254,15 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     int grid = 0, pgrid = 0, rc = 0;
     if (max_pages > kOwnPages) rc = attention_grid(batch, hkv, raw ? max_pages : max_pages + 1, &grid);
     if (rc) return rc;
+    const int pages = max_pages + (raw ? 0 : 2);  // (12-bit: two tails)
+    const bool direct = X.groups > 0 && max_pages <= kOwnPages && X.max_pages <= kDirectPages - pages &&
+                        prefix_direct(batch * hkv, X.max_pages + pages, sm_count());
     rc = prefix_grid(batch, hkv, G, X.groups, raw ? X.max_pages : X.max_pages + 1, &pgrid);
     if (rc) return rc;
     const size_t rows = pfx_part_rows(pfx_max_units(batch, hkv, G, X.groups), pgrid);
     const size_t prefix_bytes = rows * (kDim + 2) * 4;
     if (prefix_bytes + (grid > 0 ? attn_ws_bytes(batch, hkv, grid, G) : 0) > ws_bytes) return KVZ_ERR_WORKSPACE;
+    if (direct) pgrid = 0;  // (the workspace is asked for all the same)
     CUtensorMap map, pmap;
     rc = raw_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &map);
     if (!rc) rc = prefix_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &pmap);
@@ -278,6 +282,7 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     P.max_tokens = X.max_pages * kPage + (raw ? 0 : kPage - 1);
     P.unit_rows = pfx_unit_rows(batch, G, X.groups);
     P.grid = pgrid;
+    P.direct = direct;
     // blocks of 128 tokens (16 steps of a sum) between folds.  Each step drops about half of the
     // last bit, 2^-25 of the sum: 8 blocks keep a float32 output within 2^-18 of that bias, 256
     // keep it under a BF16 output's rounding (2^-9 a value)

@@ -134,6 +134,7 @@ struct PrefixParams {
     int unit_rows;   // query rows of a CTA's tile: 128 or 256
     int grid;        // CTAs
     int fold;        // blocks of a stream summed in tensor memory at a time
+    bool direct;      // no prefix kernel: the own tokens' kernel reads the prefix too
     uint32_t over_G;  // ceil(2^32 / G): the high half of its product with a row is the row's sequence (G > 1)
     const uint16_t *q;
     const int32_t *group_start, *prefix_ids, *prefix_lens, *prefix_tail;
@@ -163,6 +164,10 @@ inline size_t pfx_part_rows(int64_t units, int grid) { return grid > 0 ? (size_t
 // Own tokens up to this many pages a sequence go through one block per (sequence, KV head), which
 // merges the prefix partials too (own.cu); longer ones are split over CTAs (A.grid > 0).
 constexpr int kOwnPages = 64;
+// Prefix and own pages of a sequence that this kernel can take together, and whether it should (pages
+// that the tables can name, blocks = sequences x KV heads).
+constexpr int kDirectPages = 128;
+bool prefix_direct(int blocks, int pages, int sms);
 cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, const void *map, bool after_prefix,
                        int sms, cudaStream_t stream);
 // prefix_map: tensor map of the raw pool with one page's 16 K or V rows x 64 columns a box

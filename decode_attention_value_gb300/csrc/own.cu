@@ -7,15 +7,17 @@
 // with 0..200 own tokens took 56 us behind the prefix kernel, 52 MB of pages at 8 us.  Here the
 // partials never leave the block.
 //
-// A warp takes every fourth page, one to four in flight in its own shared-memory stages, and runs the
+// Short prefixes of few sequences come here too (P.direct): every block reads its group's prefix pages
+// before its own, from L2 after the first, and there is no other kernel to wait for.
+//
+// A warp takes every fourth (sixteenth) page, one or two in flight in its own shared-memory stages, and runs the
 // m16n8k16 products of attention.cu on it: S^T = K Q^T with the query heads in the columns, a
 // running softmax, O^T += V^T P^T with P as two BF16 parts (three for fp32 outputs).  The block's
 // warps leave their states in shared memory; then each head's warp adds the states and the prefix
 // partials, in order.
 //
 // Bound: the latency of a block's dependent reads (lengths and page ids, pages, partials), so those
-// of a kind are issued together, and as many blocks as fit run at once: with few blocks a warp has
-// up to four pages in flight, with many one (1024 blocks behind 128 x 8 heads and 16384 tokens, 52 MB of
+// of a kind are issued together, and as many warps and blocks as fit run at once (1024 blocks behind 128 x 8 heads and 16384 tokens, 52 MB of
 // pages and 25 MB of partials: the whole call 95 us, with two pages in flight and three blocks an SM 100).
 #include <cuda.h>
 
@@ -26,23 +28,24 @@
 
 namespace kvz {
 
-constexpr int kOwnWarps = 4, kOwnThreads = kOwnWarps * 32;
+// Warps of a block: 16 where every block has an SM to itself, else 4 (six blocks an SM with one stage a
+// warp).  A warp needs about 0.8 us a page, so a sequence's pages are spread over as many as there is room for.
 constexpr int kOwnPageBytes = 2 * kPage * kDim * 2;
-constexpr int kOwnResident = 6;  // blocks an SM holds with one stage a warp
-// The warps' stages, which hold their states afterwards, and a barrier each.
-__host__ __device__ constexpr int own_ring(int stages) { return kOwnWarps * stages * kOwnPageBytes; }
-__host__ __device__ constexpr int own_smem(int stages) { return own_ring(stages) + kOwnWarps * stages * 8; }
-constexpr int kOwnStates = kOwnWarps * 8 * kDim * 4;
-static_assert(own_ring(1) == kOwnStates + kOwnWarps * 8 * kDim * 4, "room for eight partials a warp");
-static_assert(kOwnPages + 1 <= 32 * kOwnWarps, "a lane resolves one page");
+// The warps' stages, which hold their states afterwards and prefix partials behind those, and a barrier each.
+__host__ __device__ constexpr int own_ring(int warps, int stages) { return warps * stages * kOwnPageBytes; }
+__host__ __device__ constexpr int own_smem(int warps, int stages) { return own_ring(warps, stages) + warps * stages * 8; }
+__host__ __device__ constexpr int own_states(int warps) { return warps * 8 * kDim * 4; }
+static_assert(own_ring(1, 1) == own_states(1) + 8 * kDim * 4, "room for eight partials a warp");
+static_assert(kOwnPages + 1 <= 32 * 4 && kDirectPages <= 32 * 4, "a lane resolves one page");
 
-template <int kFmt, bool kG8, bool kThird>
-__global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnParams A, const PrefixParams P, const int after,
-                                                                   const int log_stages, const __grid_constant__ CUtensorMap tmap)
+template <int kFmt, bool kG8, bool kThird, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : 1)
+    k_own(const AttnParams A, const PrefixParams P, const int after, const int log_stages,
+          const __grid_constant__ CUtensorMap tmap)
 {
     constexpr bool kCoded = kFmt != kFmtRaw;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ float2 wml[kOwnWarps][8];  // a warp's (maximum, sum) of each head
+    __shared__ float2 wml[kWarps][8];  // a warp's (maximum, sum) of each head
     const uint32_t sbase = smem_addr(smem);
     if (sbase & 1023u) {  // the swizzled TMA destinations need 1024-byte alignment
         if (threadIdx.x == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
@@ -50,13 +53,41 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int b = blockIdx.x / A.hkv, kvh = blockIdx.x % A.hkv, G = A.G;
-    // lane i holds the place of the warp's i-th page, page warp + 4 i
-    const int page = warp + kOwnWarps * lane;
+    if (after == 2) pdl_wait_primary();  // launched while the kernel before it ends
+    // ---- the prefix's pages, if they are read here ----
+    int group = -1, plen = 0;
+    if (P.direct) {
+        bool in_order = true, in_range = true;
+        for (int i = lane; i < P.num_groups; i += 32) {
+            const int start = P.group_start[i], end = P.group_start[i + 1], len = P.prefix_lens[i];
+            in_order &= 0 <= start && start <= end && end <= P.batch;
+            in_range &= 0 <= len && len <= P.max_tokens;
+            if (start <= b && b < end) {
+                group = i;
+                plen = min(max(len, 0), P.max_tokens);
+            }
+        }
+        in_order = __all_sync(0xffffffffu, in_order);
+        if (blockIdx.x == 0 && warp == 0) {
+            if (!in_order && lane == 0) atomicOr(A.status, KVZ_STATUS_BAD_ORDER);
+            if (in_order && !in_range) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
+        }
+        group = in_order ? __reduce_max_sync(0xffffffffu, group) : -1;
+        plen = __reduce_max_sync(0xffffffffu, plen);
+        if (group < 0) plen = 0;
+    }
+    const int np = (plen + kPage - 1) / kPage;
+    // lane i holds the place of the warp's i-th page, page warp + 4 i of the prefix's and then the own ones
+    const int page = warp + kWarps * lane, mypage = page - np;
     int L = A.seq_lens[b];
-    int32_t id = page < A.max_pages ? A.page_ids[(int64_t)b * A.max_pages + page] : -1;
+    int32_t id = -1;
+    if (page < np)
+        id = kCoded && page == plen / kPage ? P.prefix_tail[group] : P.prefix_ids[(int64_t)group * P.max_pages + page];
+    else if (mypage < A.max_pages)
+        id = A.page_ids[(int64_t)b * A.max_pages + mypage];
     const int32_t tail = kCoded ? A.tail_page[b] : 0;
     const int stages = 1 << log_stages;
-    const uint32_t ring = sbase + warp * stages * kOwnPageBytes, bar0 = sbase + own_ring(stages) + warp * stages * 8;
+    const uint32_t ring = sbase + warp * stages * kOwnPageBytes, bar0 = sbase + own_ring(kWarps, stages) + warp * stages * 8;
     if (lane == 0) {  // a warp's barriers are its own
         for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8 * s, 1);
         fence_barrier_init();
@@ -66,8 +97,8 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
     const int most = A.max_pages * kPage + (kCoded ? kPage - 1 : 0);
     if ((L < 0 || L > most) && tid == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
     L = L < 0 ? 0 : L <= most ? L : A.max_pages * kPage + (kCoded ? L % kPage : 0);
-    const int n = (L + kPage - 1) / kPage;
-    const int mine = (n - warp + kOwnWarps - 1) / kOwnWarps;  // pages warp, warp + 4, ...
+    const int n = np + (L + kPage - 1) / kPage;
+    const int mine = (n - warp + kWarps - 1) / kWarps;  // pages warp, warp + 4, ...
 
     float o[8][4];
 #pragma unroll
@@ -78,9 +109,10 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
     uint32_t kind = kSkip, tk = 0, tv = 0;
     const uint8_t *srck = nullptr, *srcv = nullptr;
     int row = 0;
+    const int tokens = page < np ? plen - page * kPage : L - mypage * kPage;  // from the page's first on
     if (page < n) {
         uint32_t flag = 0;
-        if (kCoded && page < L / kPage) {
+        if (kCoded && tokens >= kPage) {
             if (id < 0 || id >= A.num_meta_pages) {
                 flag = KVZ_STATUS_BAD_INDEX;
             } else {
@@ -99,7 +131,7 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
                 srcv = A.arena + (uint64_t)ofv * kGranule;
             }
         } else {
-            if (kCoded) id = tail;
+            if (kCoded && page >= np) id = tail;
             if (id < 0 || id >= A.num_raw_pages) {
                 flag = kCoded && id == -1 ? KVZ_STATUS_BAD_TAIL : KVZ_STATUS_BAD_INDEX;
             } else {
@@ -139,7 +171,7 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
         qf[kt][0] = qhas ? __ldg(qg + 8 * kt + t) : 0u;
         qf[kt][1] = qhas ? __ldg(qg + 8 * kt + t + 4) : 0u;
     }
-    const PfxPlace where = pfx_place(P, b, lane);
+    const PfxPlace where = after == 1 ? pfx_place(P, b, lane) : PfxPlace{0, 0, 0, 0, -1};
 
     bool ok = true;
     for (int i = 0; i < mine && ok; ++i) {
@@ -150,7 +182,7 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
             const uint32_t sta = ring + s * kOwnPageBytes;
             const uint8_t *st = smem + (sta - sbase);
             const uint32_t tagk = __shfl_sync(0xffffffffu, tk, i), tagv = __shfl_sync(0xffffffffu, tv, i);
-            const int valid = min(kPage, L - (warp + kOwnWarps * i) * kPage);
+            const int valid = min(kPage, __shfl_sync(0xffffffffu, tokens, i));
             // ---- S^T = K Q^T over the page's 16 tokens ----
             float sc[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t off = 0;
@@ -282,19 +314,19 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
     __syncthreads();
 
     // ---- a head at a time: the states, then the prefix's partials ----
-    const int share = G == 1 ? 4 : G == 2 ? 2 : 1;  // warps of a head
+    const int heads = G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8;
+    const int share = kWarps > heads ? kWarps / heads : 1;  // warps of a head
     const int part = warp % share;
     // shared memory behind the states: outputs of prefix partials, 8, 24 or 32 a warp
     const int most_items = min(32, 16 * stages - 8);
-    const uint32_t items = sbase + kOwnStates + warp * most_items * kDim * 4 + lane * 16;
+    const uint32_t items = sbase + own_states(kWarps) + warp * most_items * kDim * 4 + lane * 16;
     PfxItems pre = pfx_items(P, where, b, kvh, min(warp / share, G - 1));
-    if (after) pdl_wait_primary();  // the prefix partials are complete
-    for (int h0 = 0; h0 < G; h0 += kOwnWarps / share) {  // (uniform: the barrier below)
+    if (after == 1) pdl_wait_primary();  // the prefix partials are complete
+    for (int h0 = 0; h0 < G; h0 += kWarps / share) {  // (uniform: the barrier below)
         const int h = h0 + warp / share;
         RowSum sum;
         if (h < G) {
-            if (part == 0)
-                for (int w = 0; w < kOwnWarps; ++w)
+            for (int w = part; w < kWarps; w += share)
                     sum.add(wml[w][h].x, wml[w][h].y, *reinterpret_cast<const float4 *>(states + (w * 8 + h) * kDim + 4 * lane));
             if (h0 > 0) pre = pfx_items(P, where, b, kvh, h);
             // the prefix's: as many at once as the warp's part of the ring holds, copied while their maxima come
@@ -333,7 +365,18 @@ __global__ void __launch_bounds__(kOwnThreads, kOwnResident) k_own(const AttnPar
     }
 }
 
-template <int kFmt, bool kG8, bool kThird>
+// Measured, us, here against the prefix kernel and this one behind it (4 query heads a KV head, 40 own
+// tokens): up to a block an SM, 16 warps, raw pages of 256 / 1024 / 1900 tokens 6.7 / 9.7 / 12.5 against
+// 10.5 / 10.8 / 11.4, 12-bit pages 8.8 / 14.3 / 20 against 15.9 / 15.7 / 16.7; 256 blocks of four warps,
+// raw, 256 / 512 tokens 8.6 / 12.2 against 11.5 / 12.0, 12-bit 13 / 20 against 16 / 17; 512 blocks, 128 /
+// 256 tokens 8.2 / 10.6 against 12.2 / 12.7, 12-bit 12 / 18 against 17 / 17.5; 1024 blocks, 128 / 256
+// tokens 13.8 / 18.5 against 17.5 / 17.9, 12-bit 22 / 31 against 24 / 25.
+bool prefix_direct(int blocks, int pages, int sms)
+{
+    return pages <= (blocks <= sms ? 80 : blocks <= 2 * sms ? 28 : blocks <= 4 * sms ? 20 : 12);
+}
+
+template <int kFmt, bool kG8, bool kThird, int kWarps>
 static cudaError_t launch_own_impl(const AttnParams &A, const PrefixParams &P, const CUtensorMap &map, bool after, int sms,
                                    cudaStream_t stream)
 {
@@ -342,34 +385,36 @@ static cudaError_t launch_own_impl(const AttnParams &A, const PrefixParams &P, c
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(dev < 64 && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1ull)) {
-        e = cudaFuncSetAttribute(k_own<kFmt, kG8, kThird>, cudaFuncAttributeMaxDynamicSharedMemorySize, own_smem(4));
+        e = cudaFuncSetAttribute(k_own<kFmt, kG8, kThird, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, own_smem(kWarps, kWarps == 4 ? 2 : 1));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_own<kFmt, kG8, kThird>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            e = cudaFuncSetAttribute(k_own<kFmt, kG8, kThird, kWarps>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
         if (e == cudaSuccess && dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_ACQ_REL);
     }
     if (e != cudaSuccess) return e;
-    // pages in flight: four a warp (128 KB a block) when an SM has one block, two for up to three
-    // blocks, else one
-    const int blocks = A.batch * A.hkv, log_stages = blocks <= sms ? 2 : blocks <= 3 * sms ? 1 : 0;
+    // pages in flight: two a warp for up to three blocks of four warps an SM, else one
+    const int blocks = A.batch * A.hkv, log_stages = kWarps == 4 && blocks <= 3 * sms ? 1 : 0;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kOwnThreads);
-    cfg.dynamicSmemBytes = own_smem(1 << log_stages);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = own_smem(kWarps, 1 << log_stages);
     cfg.stream = stream;
     cfg.attrs = at;
-    cfg.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_own<kFmt, kG8, kThird>, A, P, after ? 1 : 0, log_stages, map);
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_own<kFmt, kG8, kThird, kWarps>, A, P, after ? 1 : 2, log_stages, map);
 }
 
 template <int kFmt, bool kG8>
 static cudaError_t launch_own_of(const AttnParams &A, const PrefixParams &P, const CUtensorMap &map, bool after, int sms,
                                  cudaStream_t stream)
 {
-    return P.out_bf16 ? launch_own_impl<kFmt, kG8, false>(A, P, map, after, sms, stream)
-                      : launch_own_impl<kFmt, kG8, true>(A, P, map, after, sms, stream);
+    if (A.batch * A.hkv <= sms)
+        return P.out_bf16 ? launch_own_impl<kFmt, kG8, false, 16>(A, P, map, after, sms, stream)
+                          : launch_own_impl<kFmt, kG8, true, 16>(A, P, map, after, sms, stream);
+    return P.out_bf16 ? launch_own_impl<kFmt, kG8, false, 4>(A, P, map, after, sms, stream)
+                      : launch_own_impl<kFmt, kG8, true, 4>(A, P, map, after, sms, stream);
 }
 
 cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, const void *map, bool after_prefix, int sms,

@@ -10,6 +10,8 @@ PAGE, D = 16, 128
 
 
 class PrefixCase:
+    wide = False  # prefix tables too wide for the kernel that reads short prefixes with the own tokens
+
     def __init__(self, groups, own, hq, hkv, seed=0, lead=0, k_scale=1.0, v_scale=1.0, k=None, v=None):
         """groups: [(sequences, prefix tokens)]; own: own tokens of each sequence (lead
         sequences of no group first, then the groups', then the rest without one).  k, v:
@@ -29,14 +31,19 @@ class PrefixCase:
         pages = lambda n: (n + PAGE - 1) // PAGE  # noqa: E731
         self.pw = max([pages(p) for _, p in groups], default=0)
         self.ow = max([pages(n) for n in self.own], default=0)
-        total = len(groups) * self.pw + B * self.ow + 3
+        n_prefix = len(groups) * self.pw
+        total = n_prefix + B * self.ow + 3
         ids = torch.randperm(total, generator=g, device="cuda").to(torch.int32)
         self.prefix_ids = ids[: len(groups) * self.pw].view(len(groups), self.pw).contiguous()
-        self.page_ids = ids[len(groups) * self.pw:][: B * self.ow].view(B, self.ow).contiguous()
+        if self.wide and self.pw < 130:
+            pad = torch.full((len(groups), 130 - self.pw), -1, dtype=torch.int32, device="cuda")
+            self.prefix_ids = torch.cat([self.prefix_ids, pad], 1)
+        self.page_ids = ids[n_prefix:][: B * self.ow].view(B, self.ow).contiguous()
         draw = lambda f, scale: (torch.randn((total, hkv, PAGE, D), generator=g, device="cuda") * scale if f is None  # noqa: E731
                                  else f((total, hkv, PAGE, D), g))
         self.pool = torch.stack([draw(k, k_scale), draw(v, v_scale)], 2).to(torch.bfloat16)
         self.q = torch.randn((B, hq, D), generator=g, device="cuda").to(torch.bfloat16)
+        self.pw = self.prefix_ids.shape[1]
         # whatever stands behind a last token is no part of the batch
         for ids_, lens in ((self.prefix_ids, [p for _, p in groups]), (self.page_ids, self.own)):
             for r, n in enumerate(lens):
@@ -65,7 +72,7 @@ class PrefixCase:
         self.prefix_tail = rest([p for _, p in self.groups], self.prefix_ids)
         self.tail_page = rest(self.own, self.page_ids)
         whole = max([p // PAGE for _, p in self.groups], default=0)
-        self.prefix_whole = self.prefix_ids[:, :whole].contiguous()
+        self.prefix_whole = self.prefix_ids[:, : max(whole, 130 if self.wide else 0)].contiguous()
         self.own_whole = self.page_ids[:, : max(self.own, default=0) // PAGE].contiguous()
         self.coded = True
 

@@ -10,6 +10,13 @@ pytestmark = pytest.mark.gpu
 BOTH = ["raw", "coded"]
 
 
+@pytest.fixture(autouse=True, params=[False, True], ids=["narrow", "wide"])
+def both_ways(request, monkeypatch):
+    """Short prefixes are read with the own tokens; tables wide enough for long ones send them through the
+    prefix kernel.  Every test runs both ways."""
+    monkeypatch.setattr(PrefixCase, "wide", request.param)
+
+
 def run(case, kind, **kw):
     out = case.run_raw(**kw) if kind == "raw" else case.run_coded(**kw)
     torch.cuda.synchronize()

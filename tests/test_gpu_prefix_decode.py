@@ -10,6 +10,13 @@ from test_gpu_append import _angles, _close, _rotated, _table
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True, params=[False, True], ids=["narrow", "wide"])
+def both_ways(request, monkeypatch):
+    """Short prefixes are read with the own tokens; tables wide enough for long ones send them through the
+    prefix kernel.  Every test runs both ways."""
+    monkeypatch.setattr(PrefixCase, "wide", request.param)
+
+
 @pytest.mark.parametrize("kind,steps", [("raw", 21), ("coded", 15)])
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

@@ -12,6 +12,13 @@ pytestmark = pytest.mark.gpu
 DELAY_NS = 50_000  # far longer than the kernels' start
 
 
+@pytest.fixture(autouse=True, params=[False, True], ids=["narrow", "wide"])
+def both_ways(request, monkeypatch):
+    """Short prefixes are read with the own tokens; tables wide enough for long ones send them through the
+    prefix kernel.  Every test runs both ways."""
+    monkeypatch.setattr(PrefixCase, "wide", request.param)
+
+
 @pytest.fixture(scope="module")
 def kvz():
     import decode_attention_value_gb300 as m

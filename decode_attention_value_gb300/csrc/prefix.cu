@@ -12,8 +12,8 @@
 //
 // Bound: with many rows the tensor cores (256 rows a CTA: 85 clocks a product that takes 64, 56% of
 // the pipe's time over the launch; 128 x 8 heads behind 16384 tokens: 71 us of 91); with few rows the
-// bytes of the prefix for raw pages (131072 tokens x 32 sequences: 5.3 TB/s), the restoring of groups
-// for 12-bit ones (131072 x 16: 3.0 TB/s); for short prefixes a chain of about 8 us: group table, page
+// bytes of the prefix for raw pages (131072 tokens x 32 sequences: 5.4 TB/s), the restoring of groups
+// for 12-bit ones (131072 x 16: 3.1 TB/s); for short prefixes a chain of about 8 us: group table, page
 // ids, pages, scores, weights, output.
 //
 // Split: a unit is (group, KV head, tile of 128 or 256 rows); the units' blocks of 128 tokens are one
@@ -972,6 +972,7 @@ cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_
         const cudaError_t e = format == kFmtRaw ? launch_prefix_of<kFmtRaw>(P, map, stream) : launch_prefix_of<kFmtZf>(P, map, stream);
         if (e != cudaSuccess) return e;
     }
+    // (P.direct: no prefix kernel ran, the own tokens' kernel reads the prefix)
     if (A.grid == 0) return launch_own(A, P, format, own_map, after, sms, stream);
     cudaError_t e = launch_attention_partials(A, format, own_map, stream);
     if (e != cudaSuccess) return e;

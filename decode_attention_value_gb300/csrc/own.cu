@@ -10,7 +10,7 @@
 // Short prefixes of few sequences come here too (P.direct): every block reads its group's prefix pages
 // before its own, from L2 after the first, and there is no other kernel to wait for.
 //
-// A warp takes every fourth (sixteenth) page, one or two in flight in its own shared-memory stages, and runs the
+// A warp takes every fourth (eighth, sixteenth) page, one or two in flight in its own shared-memory stages, and runs the
 // m16n8k16 products of attention.cu on it: S^T = K Q^T with the query heads in the columns, a
 // running softmax, O^T += V^T P^T with P as two BF16 parts (three for fp32 outputs).  The block's
 // warps leave their states in shared memory; then each head's warp adds the states and the prefix
@@ -28,18 +28,24 @@
 
 namespace kvz {
 
-// Warps of a block: 16 where every block has an SM to itself, else 4 (six blocks an SM with one stage a
-// warp).  A warp needs about 0.8 us a page, so a sequence's pages are spread over as many as there is room for.
+// Warps of a block: 16 where every block has an SM to itself, 8 for up to two blocks an SM, else 4 (six
+// blocks an SM with one stage a warp).  A warp needs about 0.8 us a page, so a sequence's pages are spread
+// over as many as there is room for.
 constexpr int kOwnPageBytes = 2 * kPage * kDim * 2;
-// The warps' stages, which hold their states afterwards and prefix partials behind those, and a barrier each.
-__host__ __device__ constexpr int own_ring(int warps, int stages) { return warps * stages * kOwnPageBytes; }
-__host__ __device__ constexpr int own_smem(int warps, int stages) { return own_ring(warps, stages) + warps * stages * 8; }
+// Shared memory: the warps' stages, which afterwards hold their states and, behind those, outputs of prefix
+// partials; room for more of these where it costs no block; a barrier a stage.
 __host__ __device__ constexpr int own_states(int warps) { return warps * 8 * kDim * 4; }
-static_assert(own_ring(1, 1) == own_states(1) + 8 * kDim * 4, "room for eight partials a warp");
+__host__ __device__ constexpr int own_items(int warps, int stages) { return min(32, 16 * stages - 8 + (warps > 4 ? 8 : 0)); }
+__host__ __device__ constexpr int own_ring(int warps, int stages) { return warps * stages * kOwnPageBytes; }
+__host__ __device__ constexpr int own_bars(int warps, int stages)
+{
+    return max(own_ring(warps, stages), own_states(warps) + warps * own_items(warps, stages) * kDim * 4);
+}
+__host__ __device__ constexpr int own_smem(int warps, int stages) { return own_bars(warps, stages) + warps * stages * 8; }
 static_assert(kOwnPages + 1 <= 32 * 4 && kDirectPages <= 32 * 4, "a lane resolves one page");
 
 template <int kFmt, bool kG8, bool kThird, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : 1)
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : kWarps == 8 ? 2 : 1)
     k_own(const AttnParams A, const PrefixParams P, const int after, const int log_stages,
           const __grid_constant__ CUtensorMap tmap)
 {
@@ -77,7 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : 1)
         if (group < 0) plen = 0;
     }
     const int np = (plen + kPage - 1) / kPage;
-    // lane i holds the place of the warp's i-th page, page warp + 4 i of the prefix's and then the own ones
+    // lane i holds the place of the warp's i-th page, page warp + kWarps i of the prefix's and then the own ones
     const int page = warp + kWarps * lane, mypage = page - np;
     int L = A.seq_lens[b];
     int32_t id = -1;
@@ -87,7 +93,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : 1)
         id = A.page_ids[(int64_t)b * A.max_pages + mypage];
     const int32_t tail = kCoded ? A.tail_page[b] : 0;
     const int stages = 1 << log_stages;
-    const uint32_t ring = sbase + warp * stages * kOwnPageBytes, bar0 = sbase + own_ring(kWarps, stages) + warp * stages * 8;
+    const uint32_t ring = sbase + warp * stages * kOwnPageBytes, bar0 = sbase + own_bars(kWarps, stages) + warp * stages * 8;
     if (lane == 0) {  // a warp's barriers are its own
         for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8 * s, 1);
         fence_barrier_init();
@@ -98,7 +104,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : 1)
     if ((L < 0 || L > most) && tid == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
     L = L < 0 ? 0 : L <= most ? L : A.max_pages * kPage + (kCoded ? L % kPage : 0);
     const int n = np + (L + kPage - 1) / kPage;
-    const int mine = (n - warp + kWarps - 1) / kWarps;  // pages warp, warp + 4, ...
+    const int mine = (n - warp + kWarps - 1) / kWarps;  // pages warp, warp + kWarps, ...
 
     float o[8][4];
 #pragma unroll
@@ -317,8 +323,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : 1)
     const int heads = G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8;
     const int share = kWarps > heads ? kWarps / heads : 1;  // warps of a head
     const int part = warp % share;
-    // shared memory behind the states: outputs of prefix partials, 8, 24 or 32 a warp
-    const int most_items = min(32, 16 * stages - 8);
+    const int most_items = own_items(kWarps, stages);  // 8 to 24
     const uint32_t items = sbase + own_states(kWarps) + warp * most_items * kDim * 4 + lane * 16;
     PfxItems pre = pfx_items(P, where, b, kvh, min(warp / share, G - 1));
     if (after == 1) pdl_wait_primary();  // the prefix partials are complete
@@ -367,13 +372,13 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : 1)
 
 // Measured, us, here against the prefix kernel and this one behind it (4 query heads a KV head, 40 own
 // tokens): up to a block an SM, 16 warps, raw pages of 256 / 1024 / 1900 tokens 6.7 / 9.7 / 12.5 against
-// 10.5 / 10.8 / 11.4, 12-bit pages 8.8 / 14.3 / 20 against 15.9 / 15.7 / 16.7; 256 blocks of four warps,
-// raw, 256 / 512 tokens 8.6 / 12.2 against 11.5 / 12.0, 12-bit 13 / 20 against 16 / 17; 512 blocks, 128 /
+// 10.5 / 10.8 / 11.4, 12-bit pages 8.8 / 14.3 / 20 against 15.9 / 15.7 / 16.7; 256 blocks of eight warps,
+// raw, 512 / 1024 tokens 10.2 / 14.2 against 12.0 / 12.7, 12-bit 14.6 / 22 against 17 / 17.7; 512 blocks, 128 /
 // 256 tokens 8.2 / 10.6 against 12.2 / 12.7, 12-bit 12 / 18 against 17 / 17.5; 1024 blocks, 128 / 256
 // tokens 13.8 / 18.5 against 17.5 / 17.9, 12-bit 22 / 31 against 24 / 25.
 bool prefix_direct(int blocks, int pages, int sms)
 {
-    return pages <= (blocks <= sms ? 80 : blocks <= 2 * sms ? 28 : blocks <= 4 * sms ? 20 : 12);
+    return pages <= (blocks <= sms ? 80 : blocks <= 2 * sms ? 46 : blocks <= 4 * sms ? 20 : 12);
 }
 
 template <int kFmt, bool kG8, bool kThird, int kWarps>
@@ -410,9 +415,13 @@ template <int kFmt, bool kG8>
 static cudaError_t launch_own_of(const AttnParams &A, const PrefixParams &P, const CUtensorMap &map, bool after, int sms,
                                  cudaStream_t stream)
 {
-    if (A.batch * A.hkv <= sms)
+    const int blocks = A.batch * A.hkv;
+    if (blocks <= sms)
         return P.out_bf16 ? launch_own_impl<kFmt, kG8, false, 16>(A, P, map, after, sms, stream)
                           : launch_own_impl<kFmt, kG8, true, 16>(A, P, map, after, sms, stream);
+    if (blocks <= 2 * sms)
+        return P.out_bf16 ? launch_own_impl<kFmt, kG8, false, 8>(A, P, map, after, sms, stream)
+                          : launch_own_impl<kFmt, kG8, true, 8>(A, P, map, after, sms, stream);
     return P.out_bf16 ? launch_own_impl<kFmt, kG8, false, 4>(A, P, map, after, sms, stream)
                       : launch_own_impl<kFmt, kG8, true, 4>(A, P, map, after, sms, stream);
 }

@@ -35,6 +35,13 @@ def _append_rows(pools, pages, rows, kv, status, q, rope, positions, interleaved
     q [layers][n][hq][128], rotated in the result, or None; positions [n] or [axes][n]."""
     L, per, n = pools.shape[0], pools.shape[1], kv.shape[1]
     dev = pools.device
+    if not pools.is_cuda:  # a cache kept on the host: rows as they are
+        if rope is not None:
+            raise ValueError("append: rotation needs a cache on a CUDA device")
+        at = [torch.as_tensor(np.asarray(x), dtype=torch.int64) for x in (pages, rows)]
+        # separated index tensors put the indexed dimension first: [n][layers][hkv][2][128]
+        pools[:, at[0], :, :, at[1], :] = kv.to(pools).transpose(0, 1)
+        return None if q is None else q.clone()
     kv = kv.to(device=dev, dtype=torch.bfloat16).contiguous().view(L * n, *kv.shape[2:])
     slots = (np.arange(L)[:, None] * per + np.asarray(pages)[None]) * PAGE + np.asarray(rows)[None]
     slots = torch.from_numpy(slots.reshape(-1).astype(np.int32)).to(dev)

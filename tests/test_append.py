@@ -90,3 +90,21 @@ def test_rope_table_is_the_frequency_in_turns(kvz):
         kvz.rope_table(inv[None])
     with pytest.raises(ValueError):
         kvz.rope_table(inv, axis[:-1])
+
+
+def test_caches_on_the_host_append(kvz):
+    """A cache kept on the host takes tokens as they are and refuses to rotate them."""
+    from decode_attention_value_gb300.cache import RawKVCache
+
+    c = RawKVCache(2, 2, 3, 4, num_slots=9, device="cpu")
+    c.admit(1, torch.zeros((2, 1, 2, 2, 16, 128), dtype=torch.bfloat16), 15)
+    for step in range(3):  # past the page's end
+        kv = torch.randn((2, 2, 2, 2, 128)).to(torch.bfloat16)
+        q = torch.randn((2, 2, 4, 128)).to(torch.bfloat16)
+        assert torch.equal(c.append([2, 1], kv, q=q), q)
+        for i, slot in enumerate((2, 1)):
+            n = int(c.lens[slot]) - 1
+            assert torch.equal(c.pool[:, c.pages[slot][n // 16], :, :, n % 16], kv[:, i])
+    assert c.lens[[1, 2]].tolist() == [18, 3]
+    with pytest.raises(ValueError):
+        c.append([0], kv[:, :1], rope=kvz.rope_table(torch.ones(64)))

@@ -11,7 +11,7 @@
 // go through sincospif.
 //
 // Bound: memory.  (Hq + 2 Hkv) 256 bytes a token are read once and written once: 16381 tokens of 48
-// heads in 69 us, 5.7 TB/s, 0.85 of the measured copy bandwidth; one decode token is a launch.
+// heads in 64 to 67 us, 6.0 to 6.2 TB/s, 0.88 to 0.91 of the measured copy bandwidth; one decode token is a launch.
 //
 // Layout: a row is one head of one token, 256 bytes, handled by eight lanes: each holds two
 // 16-byte vectors, eight whole rotary pairs in either pairing.  A block takes a run of
@@ -106,8 +106,14 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendResident) k_append(cons
     auto store = [&](Row &r) {
         if (!r.dst) return;
         if (r.rotated && turning) rotate8(r.x, r.y, &cs[r.tok - tok0][u], P.neighbours);
-        *reinterpret_cast<uint4 *>(r.dst + e0) = r.x;
-        *reinterpret_cast<uint4 *>(r.dst + e1) = r.y;
+        uint4 *d0 = reinterpret_cast<uint4 *>(r.dst + e0), *d1 = reinterpret_cast<uint4 *>(r.dst + e1);
+        if (P.streaming) {
+            __stcs(d0, r.x);
+            __stcs(d1, r.y);
+        } else {
+            *d0 = r.x;
+            *d1 = r.y;
+        }
     };
 
     pdl_wait_primary();  // launched while the kernel before it ends
@@ -154,6 +160,9 @@ cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream)
     const int64_t most = (int64_t)(kAppendTokens - 2) * H + 1;  // touches at most kAppendTokens tokens
     if (per > most) per = most;
     P.rows_per_block = (int)per;
+    // Rows that would fill half of the 129 MB L2 are written past it (201 MB: 69.9 -> 66.9 us, 151 MB:
+    // 55.8 -> 52.7); fewer stay there for the attention call that reads them (29 MB: 10.6 us, streamed 11.5).
+    P.streaming = rows * kDim * 2 > (64ll << 20);
     const int64_t blocks = (rows + per - 1) / per;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute at[1];

@@ -123,6 +123,7 @@ struct AppendParams {
     int64_t num_raw_pages;
     uint32_t *status;
     int rows_per_block;  // set by the launcher
+    bool streaming;      // the same: results written past L2
 };
 cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream);
 

@@ -300,3 +300,14 @@ def test_cache_append_rotates(compressed):
     assert cache.lens[slots].tolist() == [18] * 3 and int(cache.status.item()) == 0
     with pytest.raises(ValueError):
         cache.append([1, 1], kv[:, :2])
+
+
+def test_large_calls_are_written_past_the_cache():
+    """More than 64 MB of results: 6001 tokens of 56 heads, ragged, with padding and a partial rotation."""
+    import decode_attention_value_gb300 as kvz
+
+    T, hq, hkv = 6001, 40, 8
+    q, k, v, pool, slots = _inputs(T, hq, hkv, T // PAGE + 4, seed=61)
+    slots[5::97] = -1
+    pos = torch.randint(0, 131072, (T,), device="cuda", dtype=torch.int32)
+    _check(kvz, q, k, v, pool, slots, _table(kvz, 96), pos, 96, False)

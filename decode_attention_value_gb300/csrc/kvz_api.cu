@@ -261,7 +261,10 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     if (rc) return rc;
     const size_t rows = pfx_part_rows(pfx_max_units(batch, hkv, G, X.groups), pgrid);
     const size_t prefix_bytes = rows * (kDim + 2) * 4;
-    if (prefix_bytes + (grid > 0 ? attn_ws_bytes(batch, hkv, grid, G) : 0) > ws_bytes) return KVZ_ERR_WORKSPACE;
+    // the prefix kernel stores 32 bytes at a time: its partials begin at a multiple of 32
+    const size_t pad = (size_t)(-reinterpret_cast<uintptr_t>(ws) & 31);
+    if (pad + prefix_bytes + (grid > 0 ? attn_ws_bytes(batch, hkv, grid, G) : 0) > ws_bytes) return KVZ_ERR_WORKSPACE;
+    uint8_t *const partials = static_cast<uint8_t *>(ws) + pad;
     if (direct) pgrid = 0;  // (the workspace is asked for all the same)
     CUtensorMap map, pmap;
     rc = raw_tensor_map(raw_pool ? raw_pool : ws, num_raw_pages > 0 ? num_raw_pages : 1, hkv, &map);
@@ -270,7 +273,7 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     AttnParams A;
     // the own pages' kernel runs beside the prefix kernel as its programmatic dependent
     attention_params(&A, F, d, batch, hq, grid, q, page_ids, max_pages, seq_lens, tail_page, num_meta_pages, arena,
-                     arena_bytes, num_raw_pages, nullptr, static_cast<uint8_t *>(ws) + prefix_bytes, status, 0u);
+                     arena_bytes, num_raw_pages, nullptr, partials + prefix_bytes, status, 0u);
     A.overlap = pgrid > 0 ? 2 : 0;
     PrefixParams P;
     memset(&P, 0, sizeof P);
@@ -299,7 +302,7 @@ int run_prefix_attention(const FormatArgs &F, const kvz_dims &d, int batch, int 
     P.arena_bytes = arena_bytes;
     P.raw_pool = static_cast<const uint16_t *>(raw_pool);
     P.num_raw_pages = num_raw_pages;
-    P.part_o = static_cast<float *>(ws);
+    P.part_o = reinterpret_cast<float *>(partials);
     P.part_ml = P.part_o + rows * kDim;
     P.out = out;
     P.out_bf16 = out_type == KVZ_OUT_BF16;
@@ -825,11 +828,12 @@ size_t kvz_prefix_attention_workspace_size(kvz_dims dims, int32_t batch, int32_t
     if (dims_ok(dims) && num_q_heads >= 1 && num_q_heads % dims.num_kv_heads != 0) return 0;
     size_t own = kvz_attention_workspace_size(dims, batch, num_q_heads, table_pages);
     if (own == 0 || batch == 0) return own;
-    if (table_pages <= kOwnPages) own = 16;  // (merged where they are computed)
+    if (table_pages <= kOwnPages) own = 0;  // (merged where they are computed)
     const int G = num_q_heads / dims.num_kv_heads;
     int grid = 0;
     if (prefix_grid(batch, dims.num_kv_heads, G, num_groups, prefix_pages, &grid) != KVZ_OK) return 0;
-    return own + pfx_part_rows(pfx_max_units(batch, dims.num_kv_heads, G, num_groups), grid) * (kDim + 2) * 4;
+    // 16: from the workspace's alignment to the partials'
+    return 16 + own + pfx_part_rows(pfx_max_units(batch, dims.num_kv_heads, G, num_groups), grid) * (kDim + 2) * 4;
 }
 
 int kvz_prefix_attention(kvz_dims dims, int32_t batch, int32_t num_q_heads, const void *q, int32_t num_groups,

@@ -275,8 +275,9 @@ int kvz_decode_attention_noalloc(kvz_dims dims, int32_t batch, int32_t num_q_hea
  *               end), [batch][num_q_heads][128], 16-byte aligned:
  *               softmax(q.K^T / sqrt(128)) V over the prefix and the own tokens
  *  workspace    >= kvz_prefix_attention_workspace_size(dims, batch, num_q_heads,
- *               num_groups, prefix_pages, table_pages) bytes, where the compressed call
- *               counts the tail slots: prefix_pages = max_prefix_pages + 1, table_pages =
+ *               num_groups, prefix_pages, table_pages) bytes (16-B aligned; the size holds
+ *               what its partials' own alignment takes), where the compressed call counts
+ *               the tail slots: prefix_pages = max_prefix_pages + 1, table_pages =
  *               max_pages + 1 (raw call: without the + 1; more is never too small)
  * Prefix pages may be pages of other sequences.  A page with unusable metadata or an index
  * out of range is left out of the softmax and flagged; a row without any token is zero.

@@ -180,6 +180,16 @@ def _stream(stream) -> int | None:
     return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(_current_device())
 
 
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """Memory on like's device for a call on `stream` (None: the current one), from that
+    stream's own blocks: a block that was freed on the current stream is free only behind
+    work queued there, which `stream` does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _check(fn: str, rc: int):
     if rc != 0:
         raise KvzError(fn, rc)
@@ -229,7 +239,7 @@ def encode_pages(raw_pool, src_page, dst_page, dst_seq, meta, arena, cursors, st
     hkv = raw_pool.shape[1]
     n = src_page.numel()
     if workspace is None:
-        workspace = torch.empty(encode_workspace_size(hkv, n), dtype=torch.uint8, device=raw_pool.device)
+        workspace = _empty(encode_workspace_size(hkv, n), torch.uint8, raw_pool, stream)
     rc = _lib.kvz_encode_pages(
         _dims(hkv), _ptr(raw_pool, _BF16, "raw_pool"), _pages_of(raw_pool),
         _ptr(src_page, torch.int32, "src_page"), _ptr(dst_page, torch.int32, "dst_page"),
@@ -245,7 +255,7 @@ def encode_sizes(raw_pool, src_page, granules, status, workspace=None, stream=No
     hkv = raw_pool.shape[1]
     n = src_page.numel()
     if workspace is None:
-        workspace = torch.empty(encode_workspace_size(hkv, n), dtype=torch.uint8, device=raw_pool.device)
+        workspace = _empty(encode_workspace_size(hkv, n), torch.uint8, raw_pool, stream)
     rc = _lib.kvz_encode_sizes(
         _dims(hkv), _ptr(raw_pool, _BF16, "raw_pool"), _pages_of(raw_pool), _ptr(src_page, torch.int32, "src_page"),
         n, _ptr(granules, _U32, "granules"), _ptr(workspace, _U8, "workspace"), workspace.numel(),
@@ -274,8 +284,7 @@ def decode_attention(q, page_ids, seq_lens, tail_page, meta, arena, raw_pool, ou
     hkv = meta.shape[1] if meta.dim() >= 2 else raw_pool.shape[1]
     max_pages = page_ids.shape[1] if page_ids.dim() == 2 else 0
     if workspace is None:
-        workspace = torch.empty(attention_workspace_size(hkv, B, hq, max_pages + 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(attention_workspace_size(hkv, B, hq, max_pages + 1), torch.uint8, q, stream)
     args = (
         _dims(hkv), B, hq, _ptr(q, _BF16, "q"), _ptr(page_ids, torch.int32, "page_ids"), max_pages,
         _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(tail_page, torch.int32, "tail_page"),
@@ -296,8 +305,7 @@ def decode_attention_raw(q, page_ids, seq_lens, raw_pool, out, status, workspace
     hkv = raw_pool.shape[1]
     max_pages = page_ids.shape[1]
     if workspace is None:
-        workspace = torch.empty(attention_workspace_size(hkv, B, hq, max_pages), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(attention_workspace_size(hkv, B, hq, max_pages), torch.uint8, q, stream)
     args = (
         _dims(hkv), B, hq, _ptr(q, _BF16, "q"), _ptr(page_ids, torch.int32, "page_ids"), max_pages,
         _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(raw_pool, _BF16, "raw_pool"), _pages_of(raw_pool),
@@ -330,10 +338,7 @@ def _prefix_workspace(q, hkv, prefix_ids, page_ids, stream):
         raise ValueError("q, prefix_ids, page_ids: expected [batch][heads][128], [groups][pages] and [batch][pages]")
     size = _lib.kvz_prefix_attention_workspace_size(_dims(hkv), q.shape[0], q.shape[1], prefix_ids.shape[0],
                                                     prefix_ids.shape[1] + 1, page_ids.shape[1] + 1)
-    workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace
+    return _empty(size, torch.uint8, q, stream)
 
 
 def prefix_attention(q, group_start, prefix_ids, prefix_lens, prefix_tail, page_ids, seq_lens, tail_page, meta, arena,
@@ -390,12 +395,12 @@ def append_tokens(k, v, slots, raw_pool, status, q=None, q_out=None, rope=None, 
     stride of 8 elements), to rows slots (int32 [T], page * 16 + row, -1 = padding) of the
     raw pages raw_pool (BF16 [P][Hkv][2][16][128]), rotating the keys by rope (see
     rope_table) at positions (int32 [T] or [axes][T]).  q [T][Hq][128], when given, is
-    rotated into q_out (allocated when None; may be q).  k, v, slots and raw_pool may all
-    be None to rotate queries alone.  Returns q_out."""
+    rotated into q_out (allocated on the call's stream when None; may be q).  k, v, slots
+    and raw_pool may all be None to rotate queries alone.  Returns q_out."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        if stream is not None:
-            q_out.record_stream(stream)
+        q_out = _empty(q.shape, torch.bfloat16, q, stream)
+        if stream is not None and q_out.is_cuda:  # the caller may read it on the current stream
+            q_out.record_stream(torch.cuda.current_stream(q_out.device))
     rc = _binding.append_tokens(k, v, slots, raw_pool, status, q, q_out, rope, positions, interleaved, rope_scale,
                                 None if stream is None else stream.cuda_stream)
     if rc:
@@ -433,7 +438,7 @@ def ga_encode_pages(raw_pool, bases, src_page, dst_page, dst_seq, meta, arena, c
     hkv = raw_pool.shape[1]
     n = src_page.numel()
     if workspace is None:
-        workspace = torch.empty(encode_workspace_size(hkv, n), dtype=torch.uint8, device=raw_pool.device)
+        workspace = _empty(encode_workspace_size(hkv, n), torch.uint8, raw_pool, stream)
     rc = _lib.kvz_ga_encode_pages(
         _dims(hkv), _ptr(raw_pool, _BF16, "raw_pool"), _pages_of(raw_pool), _ptr(bases, _U8, "bases"),
         _ptr(src_page, torch.int32, "src_page"), _ptr(dst_page, torch.int32, "dst_page"),
@@ -462,8 +467,7 @@ def ga_decode_attention(q, page_ids, seq_lens, tail_page, meta, arena, bases, ra
     hkv = meta.shape[1] if meta.dim() >= 2 else raw_pool.shape[1]
     max_pages = page_ids.shape[1] if page_ids.dim() == 2 else 0
     if workspace is None:
-        workspace = torch.empty(attention_workspace_size(hkv, B, hq, max_pages + 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(attention_workspace_size(hkv, B, hq, max_pages + 1), torch.uint8, q, stream)
     rc = _lib.kvz_ga_decode_attention(
         _dims(hkv), B, hq, _ptr(q, _BF16, "q"), _ptr(page_ids, torch.int32, "page_ids"), max_pages,
         _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(tail_page, torch.int32, "tail_page"),
@@ -492,7 +496,7 @@ def f8_encode_pages(fmt: int, raw_pool, bases, src_page, dst_page, dst_seq, meta
     hkv = raw_pool.shape[1]
     n = src_page.numel()
     if workspace is None:
-        workspace = torch.empty(encode_workspace_size(hkv, n), dtype=torch.uint8, device=raw_pool.device)
+        workspace = _empty(encode_workspace_size(hkv, n), torch.uint8, raw_pool, stream)
     rc = _lib.kvz_f8_encode_pages(
         _dims(hkv), fmt, _ptr(raw_pool, _BF16, "raw_pool"), _pages_of(raw_pool), _ptr(bases, _U8, "bases"),
         _ptr(src_page, torch.int32, "src_page"), _ptr(dst_page, torch.int32, "dst_page"),
@@ -520,8 +524,7 @@ def f8_decode_attention(fmt: int, q, page_ids, seq_lens, tail_page, meta, arena,
     hkv = meta.shape[1] if meta.dim() >= 2 else raw_pool.shape[1]
     max_pages = page_ids.shape[1] if page_ids.dim() == 2 else 0
     if workspace is None:
-        workspace = torch.empty(attention_workspace_size(hkv, B, hq, max_pages + 1), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _empty(attention_workspace_size(hkv, B, hq, max_pages + 1), torch.uint8, q, stream)
     rc = _lib.kvz_f8_decode_attention(
         _dims(hkv), fmt, B, hq, _ptr(q, _BF16, "q"), _ptr(page_ids, torch.int32, "page_ids"), max_pages,
         _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(tail_page, torch.int32, "tail_page"),

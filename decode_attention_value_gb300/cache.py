@@ -290,7 +290,7 @@ class RawKVCache:
             self.pool[:, torch.as_tensor(ids, device=self.device)] = prompt[:, :n]
 
     def append(self, slots, kv: torch.Tensor, q=None, rope=None, positions=None, interleaved: bool = False):
-        """CompressedKVCache.append."""
+        """CompressedKVCache.append; a refused call changes nothing."""
         slots = list(slots)
         if len(set(slots)) != len(slots):
             raise ValueError("append: a slot is named twice")
@@ -299,11 +299,12 @@ class RawKVCache:
         starting = [s for s in slots if self.lens[s] % PAGE == 0]  # a new page starts
         if len(starting) > len(self.free):
             raise OutOfSpace("no free page slot")
-        for s in starting:
-            self.pages[s].append(self.free.pop())
-        page = [self.pages[s][int(self.lens[s]) // PAGE] for s in slots]
+        fresh = dict(zip(starting, reversed(self.free)))  # taken once the call has been accepted
+        page = [fresh[s] if s in fresh else self.pages[s][int(self.lens[s]) // PAGE] for s in slots]
         q = _append_rows(self.pool, page, self.lens[slots] % PAGE, kv, self.status, q, rope,
                          self.lens[slots] if positions is None else positions, interleaved)
+        for s in starting:
+            self.pages[s].append(self.free.pop())
         self.lens[slots] += 1
         return q
 

@@ -1,0 +1,77 @@
+"""What a refused append leaves of a cache: everything as it was."""
+import pytest
+import torch
+
+L, HKV, HQ = 2, 2, 4
+
+
+@pytest.fixture(scope="module")
+def kvz():
+    from decode_attention_value_gb300 import _build
+
+    _build.build()
+    import decode_attention_value_gb300 as m
+
+    return m
+
+
+def _state(c):
+    rows = c.pool if hasattr(c, "pool") else c.tails
+    return (list(getattr(c, "free", [])), [list(p) for p in getattr(c, "pages", [])], c.lens.tolist(), rows.clone())
+
+
+def _refused(c, slots, bad, then):
+    """Each of `bad`, several times over, is refused and changes nothing; `then` works afterwards."""
+    for kw in bad:
+        for _ in range(3):
+            before = _state(c)
+            with pytest.raises((ValueError, RuntimeError)):
+                c.append(slots, **kw)
+            after = _state(c)
+            assert before[:3] == after[:3], list(kw)
+            assert torch.equal(before[3].view(torch.int16), after[3].view(torch.int16)), list(kw)
+    lens = c.lens.copy()
+    c.append(slots, **then)
+    assert (c.lens[slots] == lens[slots] + 1).all()
+    args = c.batch_args(slots)
+    assert args[1].tolist() == c.lens[slots].tolist()
+
+
+def _kv(n, dev):
+    return torch.randn((L, n, HKV, 2, 128), device=dev).to(torch.bfloat16)
+
+
+def test_refused_appends_take_no_pages(kvz):
+    from decode_attention_value_gb300.cache import OutOfSpace, RawKVCache
+
+    c = RawKVCache(L, HKV, 3, 4, num_slots=9, device="cpu")
+    c.admit(1, torch.zeros((L, 1, HKV, 2, 16, 128), dtype=torch.bfloat16), 16)  # slots 0, 1 and 2 start a page
+    good = dict(kv=_kv(3, "cpu"))
+    bad = [dict(kv=_kv(3, "cpu"), rope=kvz.rope_table(torch.ones(64))), dict(kv=_kv(2, "cpu"))]
+    _refused(c, [2, 0, 1], bad, good)
+    assert c.free_pages() == 5 and [len(p) for p in c.pages] == [1, 2, 1]
+    for i, slot in enumerate([2, 0, 1]):
+        n = int(c.lens[slot]) - 1
+        assert torch.equal(c.pool[:, c.pages[slot][n // 16], :, :, n % 16], good["kv"][:, i])
+    assert len({p for own in c.pages for p in own} | set(c.free)) == 9  # no page lost, none held twice
+    c.free = c.free[:1]
+    c.lens[:] = [16, 32, 16]  # every slot starts a page
+    before = _state(c)
+    with pytest.raises(OutOfSpace):
+        c.append([0, 1], _kv(2, "cpu"))
+    assert _state(c)[:3] == before[:3]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["raw", "compressed"])
+def test_refused_appends_on_the_gpu(kvz, name):
+    from decode_attention_value_gb300.cache import CompressedKVCache, RawKVCache
+
+    c = RawKVCache(L, HKV, 3, 4, num_slots=9) if name == "raw" else CompressedKVCache(L, HKV, 3, 4, arena_bytes=1 << 24)
+    rope = kvz.rope_table(torch.ones(64, dtype=torch.float64)).cuda()
+    q = torch.randn((L, 3, HQ, 128), device="cuda").to(torch.bfloat16)
+    kv = _kv(3, "cuda")
+    bad = [dict(kv=kv, q=q, rope=rope, positions=[1, 2]), dict(kv=kv, q=q.float(), rope=rope),
+           dict(kv=kv, q=q[..., :64], rope=rope), dict(kv=kv, rope=rope.int()), dict(kv=_kv(2, "cuda"))]
+    _refused(c, [2, 0, 1], bad, dict(kv=kv, q=q, rope=rope))
+    assert int(c.status.item()) == 0

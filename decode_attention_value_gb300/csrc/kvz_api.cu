@@ -232,7 +232,8 @@ int prefix_grid(int batch, int hkv, int G, int groups, int prefix_pages, int *gr
     const int64_t units = pfx_max_units(batch, hkv, G, groups), deep = ((int64_t)prefix_pages + 7) / 8;
     if (units * deep > INT32_MAX) return KVZ_ERR_UNSUPPORTED;
     const int64_t want = units * (pfx_unit_rows(batch, G, groups) == 128 ? (deep + 1) / 2 : deep);
-    *grid = groups > 0 ? (int)(want < sms ? want : sms) : 0;
+    // (tables without a page, too: the kernel is where starts and lengths are checked)
+    *grid = groups > 0 ? (int)(want < 1 ? 1 : want < sms ? want : sms) : 0;
     return KVZ_OK;
 }
 

@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : kWarps == 8 ? 2
     for (int i = 0; i < stages && i < mine; ++i) issue(i);
 
     // ---- while the pages come: the queries, and where the prefix's partials are ----
-    // B operand of QK^T, column = head (n % 4 when G <= 4)
+    // B operand of QK^T, column = head (n % 4 when G <= 4).  Plain loads: the kernel before this one may
+    // have written q, and read-only loads may be moved over the wait for it
     uint32_t qf[8][2];
     const int qhead = kG8 ? g : (g & 3);
     const bool qhas = qhead < G;
@@ -174,8 +175,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : kWarps == 8 ? 2
         A.q + ((int64_t)b * A.hkv * G + (int64_t)kvh * G + (qhas ? qhead : 0)) * kDim);
 #pragma unroll
     for (int kt = 0; kt < 8; ++kt) {
-        qf[kt][0] = qhas ? __ldg(qg + 8 * kt + t) : 0u;
-        qf[kt][1] = qhas ? __ldg(qg + 8 * kt + t + 4) : 0u;
+        qf[kt][0] = qhas ? qg[8 * kt + t] : 0u;
+        qf[kt][1] = qhas ? qg[8 * kt + t + 4] : 0u;
     }
     const PfxPlace where = after == 1 ? pfx_place(P, b, lane) : PfxPlace{0, 0, 0, 0, -1};
 

@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
                     qv[i] = *reinterpret_cast<const uint4 *>(
                         P.q + ((int64_t)(sg.seq0 + seq) * P.hkv * P.G + sg.kvh * P.G + grow - seq * P.G) * kDim + ch * 8);
             }
+            __syncwarp();
             asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll
             for (int i = 0; i < 8 * kTiles; ++i) {
@@ -671,15 +672,18 @@ __global__ void __launch_bounds__(PfxSmem<kFmt, kTiles, kParts>::threads, 1)
                     uint32_t o[32];
                     tmem_ld32(tO + 32 * w, o);
                     tmem_wait_ld(o);
-                    if (lane >= rows) continue;
-                    float *at = P.part_o + slot0 * kDim + (4 * w * 32 + lane) * 8;
+                    if (lane < rows) {
+                        float *at = P.part_o + slot0 * kDim + (4 * w * 32 + lane) * 8;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i, at += 32 * 8) {
-                        if (folded)
+                        for (int i = 0; i < 4; ++i, at += 32 * 8) {
+                            if (folded)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) o[8 * i + k] = __float_as_uint(fmaf(at[k], f, __uint_as_float(o[8 * i + k])));
-                        st_global_32b(at, o + 8 * i);
+                                for (int k = 0; k < 8; ++k)
+                                    o[8 * i + k] = __float_as_uint(fmaf(at[k], f, __uint_as_float(o[8 * i + k])));
+                            st_global_32b(at, o + 8 * i);
+                        }
                     }
+                    __syncwarp();  // the tensor memory loads want the whole warp, lanes without a row too
                 }
                 fm = ref;
                 folded = true;

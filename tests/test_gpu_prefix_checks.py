@@ -42,3 +42,19 @@ def test_starts_and_lengths_of_a_table_without_pages(kind, n, own):
         flagged(c.kvz.STATUS_BAD_INDEX)
         c.prefix_lens.copy_(lens)
     flagged(0)
+
+
+@pytest.mark.parametrize("kind", ["raw", "coded"])
+@pytest.mark.parametrize("n", [1, 33, 161])
+def test_rows_that_fill_no_warp_over_many_blocks(monkeypatch, kind, n):
+    """The last warp's lanes without a row keep step while the others add to their partials (every eight
+    blocks for fp32 outputs; 626 blocks a KV head are at least 16 a CTA)."""
+    monkeypatch.setattr(PrefixCase, "wide", True)
+    c = PrefixCase([(n, 80003)], [3] * n, 4, 4, seed=82)
+    run = c.run_raw if kind == "raw" else c.run_coded
+    ref = c.reference()
+    first = run()
+    c.check(first, ref)
+    c.check(run(dtype=torch.bfloat16), ref)
+    assert torch.equal(run(), first)
+    assert int(c.status.item()) == 0

@@ -2,7 +2,8 @@
 Python module _binding beside it (csrc/python, against torch's headers and libkvz.so).
 
 Each translation unit is compiled in parallel, then linked into one shared library
-next to this file.  Rebuilds only when a source is newer than the libraries.
+next to this file.  Rebuilds only when a source is newer than the libraries, or when the
+binding was compiled against another torch or Python than the ones in use.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import importlib.util
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvz.so")
 BINDING_SRC = os.path.join(CSRC, "python", "binding.cpp")
 BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+STAMP = os.path.join(PKG, "_binding.against")  # the torch and Python that it was built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{os.path.join(ROOT, 'include')}"]
@@ -42,8 +45,21 @@ def _deps() -> list[str]:
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
+def _against() -> str:
+    """What the binding depends on beside its sources: the torch and the Python in use."""
+    spec = importlib.util.find_spec("torch")
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
+        return f"{sys.version}\n{spec.origin}\n{f.read()}"
+
+
 def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BINDING):
+        return False
+    try:
+        with open(STAMP) as f:
+            if f.read() != _against():
+                return False
+    except OSError:
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
@@ -72,6 +88,8 @@ def _link_binding(obj: str):
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(STAMP, "w") as f:
+        f.write(_against())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:

@@ -147,7 +147,9 @@ __device__ __forceinline__ void fma_pv_tile(float (&o)[4][2], const uint32_t (&a
 // ---------------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------------
-template <int kFmt, bool kG8>
+// kThird: weights in three BF16 parts (all 24 bits of them) instead of two; the own pages of a
+// shared-prefix call with fp32 outputs, whose other kernels hold them so.
+template <int kFmt, bool kG8, bool kThird>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams P, const __grid_constant__ CUtensorMap tmap)
 {
     constexpr bool kCompressed = kFmt != kFmtRaw;
@@ -646,9 +648,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
                     pl0 = movmatrix_trans(pack(r0, r1));
                     pl1 = movmatrix_trans(pack(r2, r3));
                 }
+                uint32_t pt0 = 0, pt1 = 0;  // third parts: columns 0..3 of G <= 4, else all
+                if (kThird) {
+                    const bool low = !G8 && t >= 2;
+                    pt0 = movmatrix_trans(low ? 0u : pack_bf16x2(r0 - bf16_round(r0), r1 - bf16_round(r1)));
+                    pt1 = movmatrix_trans(low ? 0u : pack_bf16x2(r2 - bf16_round(r2), r3 - bf16_round(r3)));
+                }
                 auto pv = [&](float (&acc)[4], const uint32_t (&a)[4]) {
                     mma_bf16_16816(acc, a, pb0, pb1);
                     if (G8) mma_bf16_16816(acc, a, pl0, pl1);
+                    if (kThird) mma_bf16_16816(acc, a, pt0, pt1);
                 };
                 auto pv16 = [&](float (&acc)[4], const uint32_t (&a)[4]) {
                     mma_f16_16816(acc, a, pb0, pb1);
@@ -1009,15 +1018,15 @@ __global__ void __launch_bounds__(128 * kGroups, 1) k_attn_merge(const AttnParam
 // ---------------------------------------------------------------------------------
 // launcher
 // ---------------------------------------------------------------------------------
-template <int kFmt, bool kG8>
+template <int kFmt, bool kG8, bool kThird>
 static cudaError_t configure(int dev)
 {
     // per process and device: allow the full shared-memory carve-out (attributes are per function)
     static unsigned long long done = 0;  // bit per device ordinal < 64
     if (dev < 64 && (__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1ull) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(k_attn<kFmt, kG8>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    cudaError_t e = cudaFuncSetAttribute(k_attn<kFmt, kG8, kThird>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_attn<kFmt, kG8>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+        e = cudaFuncSetAttribute(k_attn<kFmt, kG8, kThird>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     // the merge runs between attention launches: same carve-out, no reconfiguration
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attn_merge<1>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e == cudaSuccess)
@@ -1029,8 +1038,8 @@ static cudaError_t configure(int dev)
 template <int kFmt, bool kG8>
 static cudaError_t occupancy(int dev, int batch, int *n)
 {
-    cudaError_t e = configure<kFmt, kG8>(dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, k_attn<kFmt, kG8>, kThreads,
+    cudaError_t e = configure<kFmt, kG8, false>(dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, k_attn<kFmt, kG8, false>, kThreads,
                                                                      Smem::bytes(batch, kFmt >= kFmtGa));
     return e;
 }
@@ -1057,12 +1066,12 @@ cudaError_t attn_ctas_per_sm(int batch, int *out)
     return e;
 }
 
-template <int kFmt, bool kG8>
+template <int kFmt, bool kG8, bool kThird>
 static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream_t stream, bool merge)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = configure<kFmt, kG8>(dev);
+    if (e == cudaSuccess) e = configure<kFmt, kG8, kThird>(dev);
     if (e != cudaSuccess) return e;
     CUtensorMap map;
     memcpy(&map, tmap, sizeof(map));
@@ -1070,7 +1079,7 @@ static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream
     const int64_t units = (int64_t)P.batch * P.hkv;
     const bool groups = (int64_t)P.grid > (int64_t)kMergeChunk * units;
     if (!P.overlap) {
-        k_attn<kFmt, kG8><<<P.grid, kThreads, Smem::bytes(P.batch, kFmt >= kFmtGa), stream>>>(P, map);
+        k_attn<kFmt, kG8, kThird><<<P.grid, kThreads, Smem::bytes(P.batch, kFmt >= kFmtGa), stream>>>(P, map);
         e = cudaGetLastError();
         if (e != cudaSuccess || !merge) return e;
         if (groups)
@@ -1090,7 +1099,7 @@ static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_attn<kFmt, kG8>, P, map);
+    e = cudaLaunchKernelEx(&cfg, k_attn<kFmt, kG8, kThird>, P, map);
     if (e != cudaSuccess || !merge) return e;
     cfg.gridDim = dim3(P.batch * P.hkv);
     cfg.blockDim = dim3(groups ? 128 * kMergeGroups : 128);
@@ -1101,28 +1110,37 @@ static cudaError_t launch_impl(const AttnParams &P, const void *tmap, cudaStream
 }
 
 template <bool kG8>
-static cudaError_t launch_format(const AttnParams &P, int format, const void *tmap, cudaStream_t stream, bool merge)
+static cudaError_t launch_format(const AttnParams &P, int format, const void *tmap, cudaStream_t stream)
 {
     switch (format) {
-    case kFmtRaw: return launch_impl<kFmtRaw, kG8>(P, tmap, stream, merge);
-    case kFmtZf: return launch_impl<kFmtZf, kG8>(P, tmap, stream, merge);
-    case kFmtGa: return launch_impl<kFmtGa, kG8>(P, tmap, stream, merge);
-    case kFmtF8E4: return launch_impl<kFmtF8E4, kG8>(P, tmap, stream, merge);
-    case kFmtF8E5: return launch_impl<kFmtF8E5, kG8>(P, tmap, stream, merge);
+    case kFmtRaw: return launch_impl<kFmtRaw, kG8, false>(P, tmap, stream, true);
+    case kFmtZf: return launch_impl<kFmtZf, kG8, false>(P, tmap, stream, true);
+    case kFmtGa: return launch_impl<kFmtGa, kG8, false>(P, tmap, stream, true);
+    case kFmtF8E4: return launch_impl<kFmtF8E4, kG8, false>(P, tmap, stream, true);
+    case kFmtF8E5: return launch_impl<kFmtF8E5, kG8, false>(P, tmap, stream, true);
     default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_attention(const AttnParams &P, int format, const void *tmap, cudaStream_t stream)
 {
-    return P.G > 4 ? launch_format<true>(P, format, tmap, stream, true)
-                   : launch_format<false>(P, format, tmap, stream, true);
+    return P.G > 4 ? launch_format<true>(P, format, tmap, stream) : launch_format<false>(P, format, tmap, stream);
 }
 
-cudaError_t launch_attention_partials(const AttnParams &P, int format, const void *tmap, cudaStream_t stream)
+template <int kFmt>
+static cudaError_t launch_partials(const AttnParams &P, const void *tmap, bool third, cudaStream_t stream)
 {
-    return P.G > 4 ? launch_format<true>(P, format, tmap, stream, false)
-                   : launch_format<false>(P, format, tmap, stream, false);
+    if (P.G > 4)
+        return third ? launch_impl<kFmt, true, true>(P, tmap, stream, false)
+                     : launch_impl<kFmt, true, false>(P, tmap, stream, false);
+    return third ? launch_impl<kFmt, false, true>(P, tmap, stream, false)
+                 : launch_impl<kFmt, false, false>(P, tmap, stream, false);
+}
+
+cudaError_t launch_attention_partials(const AttnParams &P, int format, const void *tmap, bool third, cudaStream_t stream)
+{
+    return format == kFmtRaw ? launch_partials<kFmtRaw>(P, tmap, third, stream)
+                             : launch_partials<kFmtZf>(P, tmap, third, stream);
 }
 
 }  // namespace kvz

@@ -978,7 +978,9 @@ cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_
     }
     // (P.direct: no prefix kernel ran, the own tokens' kernel reads the prefix)
     if (A.grid == 0) return launch_own(A, P, format, own_map, after, sms, stream);
-    cudaError_t e = launch_attention_partials(A, format, own_map, stream);
+    // (fp32 outputs: three weight parts here as well.  32 sequences x 32/8 heads behind 2055 tokens with 0 to
+    // 4000 own ones: raw pages 60.5 -> 61.0 us, 12-bit 60.2 -> 62.1; off by 9.4e-7 with two parts, 8.7e-7)
+    cudaError_t e = launch_attention_partials(A, format, own_map, !P.out_bf16, stream);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -188,9 +188,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
         uint32_t bad_len = 0;
         const uint64_t keep = l2_evict_last();
         for (int b = b0; b < b1; ++b) {
-            const int L = ld_keep_s32(P.seq_lens + b, keep);
-            bad_len |= L < 0;
-            s += L > 0 ? (L + kPage - 1) / kPage : 0;
+            const int len = ld_keep_s32(P.seq_lens + b, keep), L = named_tokens(len, P.max_pages, kCompressed);
+            bad_len |= L != len;
+            s += (L + kPage - 1) / kPage;
         }
         if (bad_len) atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
         int incl = s;
@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
         int run = incl - s;
         for (int b = b0; b < b1; ++b) {
             pref[b] = run;
-            const int L = ld_keep_s32(P.seq_lens + b, keep);
-            run += L > 0 ? (L + kPage - 1) / kPage : 0;
-            tail_len[b] = (uint8_t)(L > 0 ? L % kPage : 0);
+            const int L = named_tokens(ld_keep_s32(P.seq_lens + b, keep), P.max_pages, kCompressed);
+            run += (L + kPage - 1) / kPage;
+            tail_len[b] = (uint8_t)(L % kPage);
         }
         if (lane == 31) pref[B] = incl;
     }
@@ -931,8 +931,7 @@ __global__ void __launch_bounds__(128 * kGroups, 1) k_attn_merge(const AttnParam
     // kernel's count), before the wait: the lengths were complete before the call started
     int pb = 0, nb = 0, pB = 0;
     for (int i = threadIdx.x; i < P.batch; i += blockDim.x) {
-        const int L = P.seq_lens[i];
-        const int pages = L > 0 ? (L + kPage - 1) / kPage : 0;
+        const int pages = (named_tokens(P.seq_lens[i], P.max_pages, P.tail_page != nullptr) + kPage - 1) / kPage;
         pB += pages;
         pb += i < b ? pages : 0;
         nb += i == b ? pages : 0;

@@ -147,6 +147,8 @@ int check_attention_common(const kvz_dims &d, int batch, int hq, const void *q, 
     const int G = hq / d.num_kv_heads;
     if (G < 1 || G > 8) return KVZ_ERR_UNSUPPORTED;
     if (batch > kMaxBatch) return KVZ_ERR_UNSUPPORTED;
+    // the kernels count a table's pages, tails included, in 32 bits
+    if (batch * (max_pages + 1LL) > INT32_MAX || max_pages > (INT32_MAX - kPage) / kPage) return KVZ_ERR_UNSUPPORTED;
     if (batch == 0) return KVZ_OK;
     if (!q || !seq_lens || !out || !ws || !status || (max_pages > 0 && !page_ids)) return KVZ_ERR_INVALID_ARG;
     if (num_raw_pages > 0 && !raw_pool) return KVZ_ERR_INVALID_ARG;

@@ -220,6 +220,14 @@ __device__ __forceinline__ void prefetch_tensormap(const void *tmap)
 // ---------------------------------------------------------------------------------
 // programmatic dependent launch
 // ---------------------------------------------------------------------------------
+// Tokens that a sequence of length L has in a table of max_pages pages (and, where `tail`, L % 16 in a
+// page of their own behind it): L, unless it is negative or longer than the table can name.
+__device__ __forceinline__ int named_tokens(int L, int max_pages, bool tail)
+{
+    if (L <= 0) return 0;
+    return L / kPage < max_pages ? L : max_pages * kPage + (tail ? L % kPage : 0);
+}
+
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

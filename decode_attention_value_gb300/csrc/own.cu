@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : kWarps == 8 ? 2
     const int np = (plen + kPage - 1) / kPage;
     // lane i holds the place of the warp's i-th page, page warp + kWarps i of the prefix's and then the own ones
     const int page = warp + kWarps * lane, mypage = page - np;
-    int L = A.seq_lens[b];
+    const int len = A.seq_lens[b], L = named_tokens(len, A.max_pages, kCoded);
     int32_t id = -1;
     if (page < np)
         id = kCoded && page == plen / kPage ? P.prefix_tail[group] : P.prefix_ids[(int64_t)group * P.max_pages + page];
@@ -99,10 +99,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : kWarps == 8 ? 2
         fence_barrier_init();
     }
     __syncwarp();
-    // tokens that the table cannot name are left out (12-bit: whole pages; the tail has its own id)
-    const int most = A.max_pages * kPage + (kCoded ? kPage - 1 : 0);
-    if ((L < 0 || L > most) && tid == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
-    L = L < 0 ? 0 : L <= most ? L : A.max_pages * kPage + (kCoded ? L % kPage : 0);
+    if (L != len && tid == 0) atomicOr(A.status, KVZ_STATUS_BAD_INDEX);
     const int n = np + (L + kPage - 1) / kPage;
     const int mine = (n - warp + kWarps - 1) / kWarps;  // pages warp, warp + kWarps, ...
 

@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const PrefixPara
     // ---- before the wait: what the lengths say (they were complete before the call) ----
     int v[3] = {0, 0, 0};  // own pages of the sequences before b, of b, of all
     for (int i = tid; i < P.batch; i += kMergeThreads) {
-        const int L = A.seq_lens[i], pages = L > 0 ? (L + kPage - 1) / kPage : 0;
+        const int pages = (named_tokens(A.seq_lens[i], A.max_pages, A.tail_page != nullptr) + kPage - 1) / kPage;
         v[0] += i < b ? pages : 0;
         v[1] += i == b ? pages : 0;
         v[2] += pages;

@@ -152,7 +152,9 @@ int kvz_decode_blocks(kvz_dims dims, const uint64_t *meta, int64_t num_meta_page
  *               G = num_q_heads / num_kv_heads (an integer, 1 <= G <= 8)
  *  page_ids     int32 [batch][max_pages] meta page ids of each sequence's completed pages
  *  seq_lens     int32 [batch] tokens in context; the first seq_lens/16 pages come from
- *               page_ids, the last seq_lens%16 tokens from raw page tail_page[b]
+ *               page_ids, the last seq_lens%16 tokens from raw page tail_page[b].  A
+ *               negative length counts as 0, one beyond the table as the table's pages
+ *               (and the seq_lens%16 tokens of the tail), both flagged KVZ_STATUS_BAD_INDEX
  *  tail_page    int32 [batch] raw page id of the tail (-1 when seq_lens%16 == 0)
  *  out          float32 [batch][num_q_heads][128]:
  *               softmax(q.K^T / sqrt(128)) V over the sequence's tokens

@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
         // column n = head n % 4 (zero if >= G); G = 5..8: column n = head n (zero if >= G).
         // FP8 pages multiply in f16 (every FP8 value is an f16 value, so the K and V
         // operands need no further widening): Q is converted once per segment and reloaded
-        // in BF16 for a raw BF16 tail page.
+        // in BF16 for a raw BF16 tail page.  Plain loads: read-only ones may be moved over the
+        // wait for the kernel that writes Q.
         uint32_t qf[8][2];
         const int qhead = G8 ? g : (g & 3);
         const bool qhas = qhead < G;
@@ -430,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
         uint32_t qbad = 0;  // FP8: a finite query that overflows f16
 #pragma unroll
         for (int kt = 0; kt < 8; ++kt) {
-            qf[kt][0] = qhas ? __ldg(qg + 8 * kt + t) : 0u;
-            qf[kt][1] = qhas ? __ldg(qg + 8 * kt + t + 4) : 0u;
+            qf[kt][0] = qhas ? qg[8 * kt + t] : 0u;
+            qf[kt][1] = qhas ? qg[8 * kt + t + 4] : 0u;
             if constexpr (kF8) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
@@ -551,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn(const AttnParams 
                         raw_k_frag(sta, j, 1, lane, a1);
                         if constexpr (kF8) {  // BF16 page: BF16 queries again
                             const int k0 = 2 * j, k1 = 2 * j + 1;
-                            const uint32_t q00 = qhas ? __ldg(qg + 8 * k0 + t) : 0u;
-                            const uint32_t q01 = qhas ? __ldg(qg + 8 * k0 + t + 4) : 0u;
-                            const uint32_t q10 = qhas ? __ldg(qg + 8 * k1 + t) : 0u;
-                            const uint32_t q11 = qhas ? __ldg(qg + 8 * k1 + t + 4) : 0u;
+                            const uint32_t q00 = qhas ? qg[8 * k0 + t] : 0u;
+                            const uint32_t q01 = qhas ? qg[8 * k0 + t + 4] : 0u;
+                            const uint32_t q10 = qhas ? qg[8 * k1 + t] : 0u;
+                            const uint32_t q11 = qhas ? qg[8 * k1 + t + 4] : 0u;
                             mma_bf16_16816(sc, a0, q00, q01);
                             mma_bf16_16816(sc, a1, q10, q11);
                         } else {

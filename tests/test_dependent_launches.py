@@ -8,7 +8,7 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "decode_attention_value_gb300", "csrc")
 
 
-@pytest.mark.parametrize("name", ["append.cu", "own.cu", "prefix.cu", "prefix.cuh"])
+@pytest.mark.parametrize("name", ["append.cu", "attention.cu", "own.cu", "prefix.cu", "prefix.cuh"])
 def test_no_read_only_loads(name):
     with open(os.path.join(CSRC, name)) as f:
         code = re.sub(r"//[^\n]*", "", f.read())

@@ -170,7 +170,7 @@ class CompressedKVCache:
         (append_tokens' table) the keys are rotated to positions (int [n] or [axes][n];
         each sequence's length so far when None), and so are the step's queries q
         [layers][n][hq][128]: the rotated copy is returned."""
-        slots = list(slots)
+        slots = [range(self.max_seqs)[s] for s in slots]  # (-1: the last one, as in the other calls)
         if len(set(slots)) != len(slots):
             raise ValueError("append: a slot is named twice")
         if not slots:
@@ -291,7 +291,7 @@ class RawKVCache:
 
     def append(self, slots, kv: torch.Tensor, q=None, rope=None, positions=None, interleaved: bool = False):
         """CompressedKVCache.append; a refused call changes nothing."""
-        slots = list(slots)
+        slots = [range(self.max_seqs)[s] for s in slots]  # (-1: the last one, as in the other calls)
         if len(set(slots)) != len(slots):
             raise ValueError("append: a slot is named twice")
         if not slots:

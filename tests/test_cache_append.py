@@ -75,3 +75,34 @@ def test_refused_appends_on_the_gpu(kvz, name):
            dict(kv=kv, q=q[..., :64], rope=rope), dict(kv=kv, rope=rope.int()), dict(kv=_kv(2, "cuda"))]
     _refused(c, [2, 0, 1], bad, dict(kv=kv, q=q, rope=rope))
     assert int(c.status.item()) == 0
+
+
+def test_slots_counted_from_the_end(kvz):
+    from decode_attention_value_gb300.cache import RawKVCache
+
+    c = RawKVCache(L, HKV, 3, 4, num_slots=9, device="cpu")
+    kv = _kv(2, "cpu")
+    before = _state(c)
+    with pytest.raises(ValueError):  # the same slot by both names
+        c.append([2, -1], kv)
+    with pytest.raises(IndexError):
+        c.append([0, 3], kv)
+    assert _state(c)[:3] == before[:3]
+    c.append([0, -1], kv)
+    assert c.lens.tolist() == [1, 0, 1] and torch.equal(c.pool[:, c.pages[2][0], :, :, 0], kv[:, 1])
+
+
+@pytest.mark.gpu
+def test_slots_counted_from_the_end_on_the_gpu(kvz):
+    """Also where a page fills: each layer's rows go to the layer's own last tail page."""
+    from decode_attention_value_gb300.cache import CompressedKVCache
+
+    a, b = (CompressedKVCache(L, HKV, 3, 4, arena_bytes=1 << 24) for _ in range(2))
+    for step in range(17):
+        kv = _kv(2, "cuda")
+        a.append([1, 2], kv)
+        b.append([1, -1], kv)
+        assert a.lens.tolist() == b.lens.tolist() == [0, step + 1, step + 1]
+        assert torch.equal(a.tails, b.tails), step
+    assert torch.equal(a.meta, b.meta) and torch.equal(a.arena, b.arena)
+    assert int(a.status.item()) == 0 and int(b.status.item()) == 0

@@ -168,8 +168,9 @@ class CompressedKVCache:
         kv: BF16 [layers][len(slots)][hkv][2][128].  Pages that fill are encoded here.
         Raises OutOfSpace, with nothing changed, when a filled page has no room.  With rope
         (append_tokens' table) the keys are rotated to positions (int [n] or [axes][n];
-        each sequence's length so far when None), and so are the step's queries q
-        [layers][n][hq][128]: the rotated copy is returned."""
+        each sequence's length so far when None: pass them for tokens behind a prefix that
+        the cache does not hold), and so are the step's queries q [layers][n][hq][128]: the
+        rotated copy is returned."""
         slots = [range(self.max_seqs)[s] for s in slots]  # (-1: the last one, as in the other calls)
         if len(set(slots)) != len(slots):
             raise ValueError("append: a slot is named twice")

@@ -7,8 +7,8 @@
 // in fp32, rounded once to BF16.  theta = position * frequency, where the position comes
 // from the pair's axis.  A frequency is kept in turns as a 64-bit fixed-point fraction F:
 // position * F modulo 2^64 is then the angle modulo one turn exactly (the wrap of integer
-// multiplication), so far positions lose nothing; the top 32 bits, 2^-32 turn = 1.5e-9 rad,
-// go through sincospif.
+// multiplication), so far positions lose nothing; the top 32 bits go through sincospif, whose
+// fp32 argument rounds them to 24: off by at most 2^-25 of half a turn, 9.4e-8 rad.
 //
 // Bound: memory.  (Hq + 2 Hkv) 256 bytes a token are read once and written once: 16381 tokens of 48
 // heads in 64 to 67 us, 6.0 to 6.2 TB/s, 0.88 to 0.91 of the measured copy bandwidth; one decode token is a launch.
@@ -161,7 +161,8 @@ cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream)
     if (per > most) per = most;
     P.rows_per_block = (int)per;
     // Rows that would fill half of the 129 MB L2 are written past it (201 MB: 69.9 -> 66.9 us, 151 MB:
-    // 55.8 -> 52.7); fewer stay there for the attention call that reads them (29 MB: 10.6 us, streamed 11.5).
+    // 55.8 -> 52.7); fewer stay there for the attention call that reads them (29 MB, in a run of appends that
+    // nothing reads: 11.8 us, streamed 11.5).
     P.streaming = rows * kDim * 2 > (64ll << 20);
     const int64_t blocks = (rows + per - 1) / per;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;

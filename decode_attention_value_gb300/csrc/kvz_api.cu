@@ -1,6 +1,7 @@
 // kvz_api.cu -- the C ABI (include/kvz.h): host-side argument checks, launch
-// configuration and the TMA tensor map for raw pages.  All compute runs in the
-// kernels of codec.cu, ga_codec.cu and attention.cu; nothing here touches device data.
+// configuration and the TMA tensor maps for raw pages.  All compute runs in the kernels of
+// the other .cu files (codecs, attention, prefix, own, append); nothing here touches device
+// data.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

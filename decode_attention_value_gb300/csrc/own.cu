@@ -18,7 +18,8 @@
 //
 // Bound: the latency of a block's dependent reads (lengths and page ids, pages, partials), so those
 // of a kind are issued together, and as many warps and blocks as fit run at once (1024 blocks behind 128 x 8 heads and 16384 tokens, 52 MB of
-// pages and 25 MB of partials: the whole call 95 us, with two pages in flight and three blocks an SM 100).
+// pages and 25 MB of partials: the whole call 90 to 92 us; with two pages in flight and three blocks an SM
+// 100 where this took 95).
 #include <cuda.h>
 
 #include <cstring>
@@ -29,7 +30,8 @@
 namespace kvz {
 
 // Warps of a block: 16 where every block has an SM to itself, 8 for up to two blocks an SM, else 4 (six
-// blocks an SM with one stage a warp).  A warp needs about 0.8 us a page, so a sequence's pages are spread
+// blocks an SM with one stage a warp: 80 registers a thread, for which the 12-bit variants spill 40 to 48
+// bytes; the raw ones fit).  A warp needs about 0.8 us a page, so a sequence's pages are spread
 // over as many as there is room for.
 constexpr int kOwnPageBytes = 2 * kPage * kDim * 2;
 // Shared memory: the warps' stages, which afterwards hold their states and, behind those, outputs of prefix
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 4 ? 6 : kWarps == 8 ? 2
                 }
             }
         }
-        if (share > 1) {  // (one turn: G <= 2)
+        if (share > 1) {  // (one turn of the loop, since kWarps / share = heads >= G: all warps meet here)
             __syncthreads();
             if (part > 0 && h < G) {
                 *reinterpret_cast<float4 *>(states + warp * 8 * kDim + 4 * lane) = sum.o;

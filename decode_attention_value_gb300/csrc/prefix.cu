@@ -12,8 +12,9 @@
 //
 // Bound: with many rows the tensor cores (256 rows a CTA: 85 clocks a product that takes 64, 56% of
 // the pipe's time over the launch; 128 x 8 heads behind 16384 tokens: 71 us of 91); with few rows the
-// bytes of the prefix for raw pages (131072 tokens x 32 sequences: 5.4 TB/s), the restoring of groups
-// for 12-bit ones (131072 x 16: 3.1 TB/s); for short prefixes a chain of about 8 us: group table, page
+// bytes of the prefix for raw pages (131072 tokens x 32 sequences: 5.4 TB/s); for 12-bit ones (131072 x 16:
+// 3.2 TB/s) no unit is busy: a stage's round (copy, restore, refill) over 16 stages an SM, about 49 KB, of
+// which the products wait for K 45% of the time; for short prefixes a chain of about 8 us: group table, page
 // ids, pages, scores, weights, output.
 //
 // Split: a unit is (group, KV head, tile of 128 or 256 rows); the units' blocks of 128 tokens are one

@@ -171,17 +171,20 @@ class CompressedKVCache:
         each sequence's length so far when None: pass them for tokens behind a prefix that
         the cache does not hold), and so are the step's queries q [layers][n][hq][128]: the
         rotated copy is returned."""
-        slots = [range(self.max_seqs)[s] for s in slots]  # (-1: the last one, as in the other calls)
+        known = range(self.max_seqs)
+        slots = [known[s] for s in slots]  # (-1: the last one, as in the other calls)
         if len(set(slots)) != len(slots):
             raise ValueError("append: a slot is named twice")
         if not slots:
             return None if q is None else q.clone()
-        done = sorted(s for s in slots if (self.lens[s] + 1) % PAGE == 0)
-        pos = self.lens[slots] % PAGE
-        idx = torch.as_tensor(slots, dtype=torch.int64, device=self.device)
-        saved = self.tails[:, idx].clone() if done else None
-        q = _append_rows(self.tails, slots, pos, kv, self.status, q, rope,
-                         self.lens[slots] if positions is None else positions, interleaved)
+        lens = self.lens[slots]
+        pos = lens % PAGE
+        done = sorted(s for s, r in zip(slots, pos.tolist()) if r == PAGE - 1)
+        if done:
+            idx = torch.as_tensor(slots, dtype=torch.int64, device=self.device)
+            saved = self.tails[:, idx]  # (a copy)
+        q = _append_rows(self.tails, slots, pos, kv, self.status, q, rope, lens if positions is None else positions,
+                         interleaved)
         if done:
             try:
                 self._finalize(done)
@@ -292,18 +295,20 @@ class RawKVCache:
 
     def append(self, slots, kv: torch.Tensor, q=None, rope=None, positions=None, interleaved: bool = False):
         """CompressedKVCache.append; a refused call changes nothing."""
-        slots = [range(self.max_seqs)[s] for s in slots]  # (-1: the last one, as in the other calls)
+        known = range(self.max_seqs)
+        slots = [known[s] for s in slots]  # (-1: the last one, as in the other calls)
         if len(set(slots)) != len(slots):
             raise ValueError("append: a slot is named twice")
         if not slots:
             return None if q is None else q.clone()
-        starting = [s for s in slots if self.lens[s] % PAGE == 0]  # a new page starts
+        lens = self.lens[slots]
+        starting = [s for s, n in zip(slots, lens.tolist()) if n % PAGE == 0]  # a new page starts
         if len(starting) > len(self.free):
             raise OutOfSpace("no free page slot")
         fresh = dict(zip(starting, reversed(self.free)))  # taken once the call has been accepted
-        page = [fresh[s] if s in fresh else self.pages[s][int(self.lens[s]) // PAGE] for s in slots]
-        q = _append_rows(self.pool, page, self.lens[slots] % PAGE, kv, self.status, q, rope,
-                         self.lens[slots] if positions is None else positions, interleaved)
+        page = [fresh[s] if s in fresh else self.pages[s][n // PAGE] for s, n in zip(slots, lens.tolist())]
+        q = _append_rows(self.pool, page, lens % PAGE, kv, self.status, q, rope,
+                         lens if positions is None else positions, interleaved)
         for s in starting:
             self.pages[s].append(self.free.pop())
         self.lens[slots] += 1

@@ -106,3 +106,20 @@ def test_slots_counted_from_the_end_on_the_gpu(kvz):
         assert torch.equal(a.tails, b.tails), step
     assert torch.equal(a.meta, b.meta) and torch.equal(a.arena, b.arena)
     assert int(a.status.item()) == 0 and int(b.status.item()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["raw", "compressed"])
+def test_an_append_copies_to_the_device_once(kvz, monkeypatch, name):
+    """A step's host time is its transfers: the rows' places are one, where no page fills."""
+    from decode_attention_value_gb300.cache import CompressedKVCache, RawKVCache
+
+    c = RawKVCache(L, HKV, 3, 4, num_slots=9) if name == "raw" else CompressedKVCache(L, HKV, 3, 4, arena_bytes=1 << 24)
+    kv = _kv(2, "cuda")
+    c.append([0, 2], kv)
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA, torch.profiler.ProfilerActivity.CPU]) as p:
+        c.append([0, 2], kv)
+        torch.cuda.synchronize()
+    copies = [e for e in p.events() if "Memcpy HtoD" in e.name]
+    assert len(copies) <= 1, [e.name for e in p.events()]
+    assert c.lens.tolist() == [2, 0, 2]

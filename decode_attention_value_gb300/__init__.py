@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -62,6 +63,7 @@ EXPORTS = (
     "kvz_selftest_bounded_wait", "kvz_encode_sizes", "kvz_alloc_reserve_granules", "kvz_alloc_room",
     "kvz_f8_calibrate", "kvz_f8_encode_pages", "kvz_f8_decode_blocks", "kvz_f8_decode_attention",
     "kvz_decode_attention_ex", "kvz_decode_attention_raw_ex", "kvz_selftest_late_writer",
+    "kvz_append_tokens_normed", "kvz_plan_step", "kvz_release_pages",
     "kvz_append_tokens", "kvz_prefix_attention_workspace_size", "kvz_prefix_attention", "kvz_prefix_attention_raw",
 )
 
@@ -104,6 +106,11 @@ def _load() -> ctypes.CDLL:
                                                     sz, P, P]),
         "kvz_append_tokens": (ctypes.c_int, [Dims, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P, i32, P, i32,
                                              ctypes.c_uint32, ctypes.c_float, P, P, i64, P, P]),
+        "kvz_append_tokens_normed": (ctypes.c_int, [Dims, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P, i32, P,
+                                                    i32, ctypes.c_uint32, ctypes.c_float, P, P, i32, i32,
+                                                    ctypes.c_float, P, P, i64, P, P]),
+        "kvz_plan_step": (ctypes.c_int, [i32, i32, P, P, P, i32, P, i32, P, i32, P, P, P, P, P, P, P, P, P, P]),
+        "kvz_release_pages": (ctypes.c_int, [i32, P, P, i32, P, i32, P, i32, P, P, P]),
         "kvz_selftest_late_writer": (ctypes.c_int, [P, P, u64, u64, P]),
         "kvz_alloc_create": (ctypes.c_int, [u64, ctypes.c_uint32, i32, i32, ctypes.POINTER(P)]),
         "kvz_alloc_destroy": (None, [P]),
@@ -390,22 +397,73 @@ def rope_table(inv_freq: torch.Tensor, axis: torch.Tensor | None = None) -> torc
 
 
 def append_tokens(k, v, slots, raw_pool, status, q=None, q_out=None, rope=None, positions=None,
-                  interleaved: bool = False, rope_scale: float = 1.0, stream=None):
+                  interleaved: bool = False, rope_scale: float = 1.0, stream=None, q_norm=None, k_norm=None,
+                  norm_eps: float = 1e-6):
     """Write the keys and values of new tokens, BF16 [T][Hkv][128] (any token and head
     stride of 8 elements), to rows slots (int32 [T], page * 16 + row, -1 = padding) of the
     raw pages raw_pool (BF16 [P][Hkv][2][16][128]), rotating the keys by rope (see
     rope_table) at positions (int32 [T] or [axes][T]).  q [T][Hq][128], when given, is
     rotated into q_out (allocated on the call's stream when None; may be q).  k, v, slots
-    and raw_pool may all be None to rotate queries alone.  Returns q_out."""
+    and raw_pool may all be None to rotate queries alone.  With q_norm or k_norm (BF16 or float32, [128] or
+    [heads][128]) that operand's heads become x / sqrt(mean(x^2) + norm_eps) * weight before they turn.
+    Returns q_out."""
     if q is not None and q_out is None:
         q_out = _empty(q.shape, torch.bfloat16, q, stream)
         if stream is not None and q_out.is_cuda:  # the caller may read it on the current stream
             q_out.record_stream(torch.cuda.current_stream(q_out.device))
     rc = _binding.append_tokens(k, v, slots, raw_pool, status, q, q_out, rope, positions, interleaved, rope_scale,
-                                None if stream is None else stream.cuda_stream)
+                                None if stream is None else stream.cuda_stream, q_norm, k_norm, norm_eps)
     if rc:
         raise KvzError("kvz_append_tokens", rc)
     return q_out
+
+
+# ------------------------------------------------------------------------------------
+# the tables of a step
+# ------------------------------------------------------------------------------------
+class StepPlan(NamedTuple):
+    """What plan_step fills, int32 on the device: q_start [requests + 1], seq_lens [requests], page_ids
+    [requests][pages], positions and slots [tokens]."""
+
+    q_start: torch.Tensor
+    seq_lens: torch.Tensor
+    page_ids: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+
+
+def new_step_plan(requests: int, tokens: int, pages: int, device="cuda") -> StepPlan:
+    """Buffers of a step with up to `tokens` new tokens, of an empty one until plan_step fills them."""
+    new = lambda fill, *shape: torch.full(shape, fill, dtype=torch.int32, device=device)  # noqa: E731
+    return StepPlan(new(0, requests + 1), new(0, requests), new(-1, requests, pages), new(0, tokens), new(-1, tokens))
+
+
+def plan_step(rows, new_tokens, lens, tables, free_pages, free_count, plan: StepPlan, status, lens_out=None,
+              free_out=None, stream=None) -> StepPlan:
+    """The tables of a step in which request rows[b] (int32 [B], -1: none) gets new_tokens[b] (int32 [B]) tokens.
+    lens (int32 [rows]) are the tokens that each row of tables (int32 [rows][pages]) holds, and the first
+    free_count[0] of free_pages are free: tables is extended by pages from their end, and lens and free_count
+    are brought forward, in place or into lens_out and free_out.  Fills and returns plan (new_step_plan), whose
+    positions and slots go to append_tokens and whose q_start, page_ids and seq_lens to chunk_attention_raw.  A step
+    that cannot be taken (too few free pages: STATUS_ARENA_FULL) is empty and changes nothing."""
+    rc = _binding.plan_step(rows, new_tokens, lens, tables, free_pages, free_count, *plan,
+                            lens if lens_out is None else lens_out, free_count if free_out is None else free_out,
+                            status, None if stream is None else stream.cuda_stream)
+    if rc:
+        raise KvzError("kvz_plan_step", rc)
+    return plan
+
+
+def release_pages(rows, lens, tables, free_pages, free_count, status, stream=None):
+    """Give the pages of rows (int32 [B], -1: none) back to the free list of plan_step: their lens become 0."""
+    if tables.dim() != 2 or lens.numel() != tables.shape[0] or free_count.numel() != 1:
+        raise ValueError("lens, tables, free_count: expected [rows], [rows][pages] and one value")
+    i32 = torch.int32
+    rc = _lib.kvz_release_pages(
+        rows.numel(), _ptr(rows, i32, "rows"), _ptr(lens, i32, "lens"), lens.numel(), _ptr(tables, i32, "tables"),
+        tables.shape[1], _ptr(free_pages, i32, "free_pages"), free_pages.numel(), _ptr(free_count, i32, "free_count"),
+        _ptr(status, _U32, "status"), _stream(stream))
+    _check("kvz_release_pages", rc)
 
 
 def apply_cursor_updates(idx, pos, end, cursors, stream=None):

@@ -879,26 +879,31 @@ int kvz_prefix_attention_raw(kvz_dims dims, int32_t batch, int32_t num_q_heads, 
                                 out_type, workspace, workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int64_t q_token_stride,
-                      int64_t q_head_stride, const void *k, int64_t k_token_stride, int64_t k_head_stride,
-                      const void *v, int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots,
-                      const int32_t *positions, int32_t num_axes, const uint64_t *rope, int32_t rot_dim,
-                      uint32_t flags, float rope_scale, void *q_out, void *raw_pool, int64_t num_raw_pages,
-                      uint32_t *status, kvz_stream_t stream)
+int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q,
+                             int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                             const int32_t *slots, const int32_t *positions, int32_t num_axes, const uint64_t *rope,
+                             int32_t rot_dim, uint32_t flags, float rope_scale, const void *q_norm,
+                             const void *k_norm, int32_t norm_type, int32_t norm_flags, float norm_eps, void *q_out,
+                             void *raw_pool, int64_t num_raw_pages, uint32_t *status, kvz_stream_t stream)
 {
     if (!dims_ok(dims)) return dims.num_kv_heads >= 1 ? KVZ_ERR_UNSUPPORTED : KVZ_ERR_INVALID_ARG;
     if (num_tokens < 0 || num_q_heads < 0 || num_raw_pages < 0 || (flags & ~KVZ_ROPE_FLAGS_ALL))
         return KVZ_ERR_INVALID_ARG;
     if (rot_dim < 0 || rot_dim > kDim || num_axes < 0) return KVZ_ERR_INVALID_ARG;
     if (rot_dim % 16 != 0 || num_axes > KVZ_ROPE_MAX_AXES) return KVZ_ERR_UNSUPPORTED;
+    if (norm_type != KVZ_OUT_F32 && norm_type != KVZ_OUT_BF16) return KVZ_ERR_INVALID_ARG;
+    if (norm_flags & ~KVZ_NORM_FLAGS_ALL || !(norm_eps >= 0.f)) return KVZ_ERR_INVALID_ARG;  // (a NaN too)
     if (num_tokens == 0) return KVZ_OK;
     const bool kv = k || v || slots || raw_pool;  // all of them, or none (queries alone)
     if ((!kv && !q) || !status) return KVZ_ERR_INVALID_ARG;
     if (kv && (!k || !v || !slots || !raw_pool)) return KVZ_ERR_INVALID_ARG;
     if ((num_q_heads > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return KVZ_ERR_INVALID_ARG;
+    if ((q_norm && !q) || (k_norm && !kv)) return KVZ_ERR_INVALID_ARG;
     if (rot_dim > 0 && (!rope || !positions || num_axes < 1)) return KVZ_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(raw_pool, 16) ||
-        !aligned(rope, 16) || !aligned(slots, 4) || !aligned(positions, 4) || !aligned(status, 4))
+        !aligned(rope, 16) || !aligned(slots, 4) || !aligned(positions, 4) || !aligned(status, 4) ||
+        !aligned(q_norm, 16) || !aligned(k_norm, 16))
         return KVZ_ERR_ALIGNMENT;
     const int64_t strides[6] = {q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride,
                                 v_head_stride};
@@ -932,7 +937,107 @@ int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, co
     P.raw_pool = static_cast<uint16_t *>(raw_pool);
     P.num_raw_pages = num_raw_pages;
     P.status = status;
+    P.q_norm = q_norm;
+    P.k_norm = k_norm;
+    P.q_norm_head = norm_flags & KVZ_NORM_Q_PER_HEAD ? kDim : 0;
+    P.k_norm_head = norm_flags & KVZ_NORM_K_PER_HEAD ? kDim : 0;
+    P.norm_f32 = norm_type == KVZ_OUT_F32;
+    P.eps = norm_eps;
     cudaError_t e = launch_append(P, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
+}
+
+int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int64_t q_token_stride,
+                      int64_t q_head_stride, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                      const void *v, int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots,
+                      const int32_t *positions, int32_t num_axes, const uint64_t *rope, int32_t rot_dim,
+                      uint32_t flags, float rope_scale, void *q_out, void *raw_pool, int64_t num_raw_pages,
+                      uint32_t *status, kvz_stream_t stream)
+{
+    return kvz_append_tokens_normed(dims, num_tokens, num_q_heads, q, q_token_stride, q_head_stride, k, k_token_stride,
+                                    k_head_stride, v, v_token_stride, v_head_stride, slots, positions, num_axes, rope,
+                                    rot_dim, flags, rope_scale, nullptr, nullptr, KVZ_OUT_BF16, 0, 0.f, q_out, raw_pool,
+                                    num_raw_pages, status, stream);
+}
+
+// What plan_step and release_pages have in common.
+static int check_plan(int32_t batch, const int32_t *rows, const int32_t *lens, int32_t num_rows, const int32_t *tables,
+                      int32_t width, const int32_t *free_pages, int32_t free_capacity, const int32_t *free_count,
+                      const uint32_t *status)
+{
+    if (batch < 0 || num_rows < 0 || width < 0 || free_capacity < 0) return KVZ_ERR_INVALID_ARG;
+    if (batch > kMaxBatch || width > (INT32_MAX - kPage) / kPage) return KVZ_ERR_UNSUPPORTED;
+    if (!status || !free_count || (batch > 0 && !rows) || (num_rows > 0 && !lens)) return KVZ_ERR_INVALID_ARG;
+    if ((num_rows > 0 && width > 0 && !tables) || (free_capacity > 0 && !free_pages)) return KVZ_ERR_INVALID_ARG;
+    if (!aligned(rows, 4) || !aligned(lens, 4) || !aligned(tables, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_count, 4) || !aligned(status, 4))
+        return KVZ_ERR_ALIGNMENT;
+    return KVZ_OK;
+}
+
+int kvz_plan_step(int32_t batch, int32_t num_tokens, const int32_t *rows, const int32_t *new_tokens,
+                  const int32_t *lens, int32_t num_rows, int32_t *tables, int32_t width, const int32_t *free_pages,
+                  int32_t free_capacity, const int32_t *free_count, int32_t *q_start, int32_t *seq_lens,
+                  int32_t *page_ids, int32_t *positions, int32_t *slots, int32_t *lens_out, int32_t *free_out,
+                  uint32_t *status, kvz_stream_t stream)
+{
+    int rc = check_plan(batch, rows, lens, num_rows, tables, width, free_pages, free_capacity, free_count, status);
+    if (rc) return rc;
+    if (num_tokens < 0) return KVZ_ERR_INVALID_ARG;
+    if (!q_start || !free_out || (num_rows > 0 && !lens_out)) return KVZ_ERR_INVALID_ARG;
+    if (batch > 0 && (!new_tokens || !seq_lens || (width > 0 && !page_ids))) return KVZ_ERR_INVALID_ARG;
+    if (num_tokens > 0 && (!positions || !slots)) return KVZ_ERR_INVALID_ARG;
+    if (!aligned(new_tokens, 4) || !aligned(q_start, 4) || !aligned(seq_lens, 4) || !aligned(page_ids, 4) ||
+        !aligned(positions, 4) || !aligned(slots, 4) || !aligned(lens_out, 4) || !aligned(free_out, 4))
+        return KVZ_ERR_ALIGNMENT;
+    PlanParams P;
+    memset(&P, 0, sizeof P);
+    P.batch = batch;
+    P.tokens = num_tokens;
+    P.num_rows = num_rows;
+    P.width = width;
+    P.free_capacity = free_capacity;
+    P.rows = rows;
+    P.new_tokens = new_tokens;
+    P.lens = lens;
+    P.tables = tables;
+    P.free_pages = free_pages;
+    P.free_count = free_count;
+    P.q_start = q_start;
+    P.seq_lens = seq_lens;
+    P.page_ids = page_ids;
+    P.positions = positions;
+    P.slots = slots;
+    P.lens_out = lens_out;
+    P.free_out = free_out;
+    P.vector = width % 4 == 0 && aligned(page_ids, 16);
+    P.status = status;
+    cudaError_t e = launch_plan(P, false, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
+}
+
+int kvz_release_pages(int32_t batch, const int32_t *rows, int32_t *lens, int32_t num_rows, int32_t *tables,
+                      int32_t width, int32_t *free_pages, int32_t free_capacity, int32_t *free_count,
+                      uint32_t *status, kvz_stream_t stream)
+{
+    int rc = check_plan(batch, rows, lens, num_rows, tables, width, free_pages, free_capacity, free_count, status);
+    if (rc || batch == 0) return rc;
+    PlanParams P;
+    memset(&P, 0, sizeof P);
+    P.batch = batch;
+    P.num_rows = num_rows;
+    P.width = width;
+    P.free_capacity = free_capacity;
+    P.rows = rows;
+    P.lens = lens;
+    P.tables = tables;
+    P.free_pages = free_pages;
+    P.free_count = free_count;
+    P.lens_out = lens;
+    P.free_out = free_count;
+    P.free_out_pages = free_pages;
+    P.status = status;
+    cudaError_t e = launch_plan(P, true, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
 }
 

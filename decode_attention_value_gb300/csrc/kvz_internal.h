@@ -124,8 +124,28 @@ struct AppendParams {
     uint32_t *status;
     int rows_per_block;  // set by the launcher
     bool streaming;      // the same: results written past L2
+    // norm weights (null: that operand is not normed), BF16 or (norm_f32) fp32; a head's begin norm_head values
+    // behind the one before's
+    const void *q_norm, *k_norm;
+    int q_norm_head, k_norm_head;
+    bool norm_f32;
+    float eps;
 };
 cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream);
+
+// Step tables from lengths, and pages given back (plan.cu).
+struct PlanParams {
+    int batch, tokens, num_rows, width, free_capacity;
+    const int32_t *rows, *new_tokens, *lens;
+    int32_t *tables;  // [num_rows][width]
+    const int32_t *free_pages, *free_count;
+    int32_t *q_start, *seq_lens, *page_ids, *positions, *slots;
+    int32_t *lens_out, *free_out;  // may be lens and free_count
+    int32_t *free_out_pages;       // release: free_pages
+    bool vector;                   // rows of page_ids begin at multiples of 16 bytes
+    uint32_t *status;
+};
+cudaError_t launch_plan(const PlanParams &P, bool release, cudaStream_t stream);
 
 // Shared-prefix attention (prefix.cu): the prefix half; the own pages go through AttnParams.
 constexpr int kPfxMaxGroups = 256;

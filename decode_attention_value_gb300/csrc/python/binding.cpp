@@ -143,11 +143,33 @@ void count(Py_ssize_t n, Py_ssize_t want)
     if (n != want) throw Refused{"wrong number of arguments"};
 }
 
-// k, v, slots, raw_pool, status, q, q_out, rope, positions, interleaved, rope_scale, stream
+// Norm weights [128] or [heads][128], BF16 or float32, or None.
+struct Norm {
+    const void *data = nullptr;
+    int32_t type = KVZ_OUT_BF16;
+    bool per_head = false;
+};
+
+Norm norm_of(PyObject *o, const char *name, int64_t heads, int dev)
+{
+    Norm n;
+    if (o == Py_None) return n;
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != kBf16)
+        throw Refused{std::string(name) + ": expected torch.float32 or torch.bfloat16, got " + c10::toString(t.scalar_type())};
+    n.per_head = t.dim() == 2;
+    if (n.per_head) dims_of(t, name, {heads, 128}, "[128] or [heads][128]");
+    else dims_of(t, name, {128}, "[128] or [heads][128]");
+    n.type = t.scalar_type() == at::kFloat ? KVZ_OUT_F32 : KVZ_OUT_BF16;
+    n.data = data(t, name, dev, t.scalar_type(), t.scalar_type());
+    return n;
+}
+
+// k, v, slots, raw_pool, status, q, q_out, rope, positions, interleaved, rope_scale, stream, q_norm, k_norm, norm_eps
 PyObject *append_tokens(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return guarded([&] {
-        count(n, 12);
+        count(n, 15);
         const int dev = device_of(a[4]);
         const bool kv = a[0] != Py_None;
         int64_t T = 0, pages = 0;
@@ -200,17 +222,23 @@ PyObject *append_tokens(PyObject *, PyObject *const *a, Py_ssize_t n)
             positions = static_cast<const int32_t *>(data(pt, "positions", dev, kI32, kI32));
         }
         const int interleaved = PyObject_IsTrue(a[9]);
-        const double scale = PyFloat_AsDouble(a[10]);
-        if (interleaved < 0 || PyErr_Occurred()) throw Refused{"interleaved, rope_scale: expected a truth value and a number"};
+        const double scale = PyFloat_AsDouble(a[10]), eps = PyFloat_AsDouble(a[14]);
+        if (interleaved < 0 || PyErr_Occurred())
+            throw Refused{"interleaved, rope_scale, norm_eps: expected a truth value and numbers"};
+        if ((a[12] != Py_None && a[5] == Py_None) || (a[13] != Py_None && !kv)) throw Refused{"q_norm without q, or k_norm without k"};
+        const Norm qn = norm_of(a[12], "q_norm", q.heads, dev), kn = norm_of(a[13], "k_norm", hkv, dev);
+        if (qn.data && kn.data && qn.type != kn.type) throw Refused{"q_norm, k_norm: expected weights of one type"};
+        const int32_t nflags = (qn.per_head ? KVZ_NORM_Q_PER_HEAD : 0) | (kn.per_head ? KVZ_NORM_K_PER_HEAD : 0);
         uint32_t *status = data<uint32_t>(a[4], "status", dev, kI32, at::kUInt32);
         const kvz_stream_t stream = stream_of(a[11], dev);
         const kvz_dims dims{hkv, 128, 16};
         const int32_t tokens = i32(T, "tokens");
         int rc = 0;
         Py_BEGIN_ALLOW_THREADS;
-        rc = kvz_append_tokens(dims, tokens, q.heads, q.data, q.token, q.head, k.data, k.token, k.head, v.data, v.token,
-                               v.head, slots, positions, axes, rope, rot, interleaved ? KVZ_ROPE_INTERLEAVED : 0u,
-                               (float)scale, q_out, pool, pages, status, stream);
+        rc = kvz_append_tokens_normed(dims, tokens, q.heads, q.data, q.token, q.head, k.data, k.token, k.head, v.data,
+                                      v.token, v.head, slots, positions, axes, rope, rot,
+                                      interleaved ? KVZ_ROPE_INTERLEAVED : 0u, (float)scale, qn.data, kn.data,
+                                      qn.data ? qn.type : kn.type, nflags, (float)eps, q_out, pool, pages, status, stream);
         Py_END_ALLOW_THREADS;
         return rc;
     });
@@ -284,7 +312,55 @@ PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// rows, new_tokens, lens, tables, free_pages, free_count, q_start, seq_lens, page_ids, positions, slots, lens_out,
+// free_out, status, stream
+PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&] {
+        count(n, 15);
+        const int dev = device_of(a[13]);
+        const char *names[] = {"rows", "new_tokens", "lens", "tables", "free_pages", "free_count", "q_start", "seq_lens",
+                               "page_ids", "positions", "slots", "lens_out", "free_out"};
+        int32_t *p[13];
+        int64_t size[13];
+        for (int i = 0; i < 13; ++i) {
+            const at::Tensor &t = tensor(a[i], names[i]);
+            p[i] = static_cast<int32_t *>(data(t, names[i], dev, kI32, kI32));
+            size[i] = t.numel();
+        }
+        const at::Tensor &tables = tensor(a[3], "tables"), &rows = tensor(a[0], "rows"), &positions = tensor(a[9], "positions");
+        dims_of(rows, "rows", {-1}, "[requests]");
+        const int64_t B = rows.size(0);
+        dims_of(tensor(a[2], "lens"), "lens", {-1}, "[rows]");
+        dims_of(tables, "tables", {size[2], -1}, "[rows of lens][pages]");
+        dims_of(tensor(a[4], "free_pages"), "free_pages", {-1}, "[pages]");
+        dims_of(positions, "positions", {-1}, "[tokens]");
+        const int64_t want[13] = {B, B, size[2], size[3], size[4], 1, B + 1, B, B * tables.size(1), size[9], size[9], size[2], 1};
+        for (int i = 0; i < 13; ++i)
+            if (size[i] != want[i])
+                throw Refused{std::string(names[i]) + ": expected " + std::to_string(want[i]) + " values, got " + std::to_string(size[i])};
+        // what is written may overlap nothing else, but lens_out and free_out may be lens and free_count
+        for (int i : {3, 6, 7, 8, 9, 10, 11, 12})
+            for (int j = 0; j < 13; ++j) {
+                if (i == j || (i == 11 && j == 2 && p[i] == p[j]) || (i == 12 && j == 5 && p[i] == p[j])) continue;
+                if (size[i] && size[j] && p[i] < p[j] + size[j] && p[j] < p[i] + size[i])
+                    throw Refused{std::string(names[i]) + " overlaps " + names[j]};
+            }
+        uint32_t *status = data<uint32_t>(a[13], "status", dev, kI32, at::kUInt32);
+        const kvz_stream_t stream = stream_of(a[14], dev);
+        const int32_t batch = i32(B, "rows"), tokens = i32(size[9], "positions"), num_rows = i32(size[2], "lens");
+        const int32_t width = i32(tables.size(1), "tables"), capacity = i32(size[4], "free_pages");
+        int rc = 0;
+        Py_BEGIN_ALLOW_THREADS;
+        rc = kvz_plan_step(batch, tokens, p[0], p[1], p[2], num_rows, p[3], width, p[4], capacity, p[5], p[6], p[7], p[8], p[9],
+                           p[10], p[11], p[12], status, stream);
+        Py_END_ALLOW_THREADS;
+        return rc;
+    });
+}
+
 PyMethodDef methods[] = {
+    {"plan_step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan_step)), METH_FASTCALL, nullptr},
     {"append_tokens", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_tokens)), METH_FASTCALL, nullptr},
     {"prefix_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_attention)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

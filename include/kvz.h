@@ -343,6 +343,58 @@ int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, co
                       uint32_t flags, float rope_scale, void *q_out, void *raw_pool, int64_t num_raw_pages,
                       uint32_t *status, kvz_stream_t stream);
 
+/* kvz_append_tokens_normed -- kvz_append_tokens with a norm of each query and key head before the rotation:
+ * x / sqrt(mean(x^2) + norm_eps) * weight over the head's 128 values, in fp32, with the rotation's rounding to
+ * BF16 as the only one.
+ *  q_norm, k_norm  weights [128], or [heads][128] with KVZ_NORM_Q_PER_HEAD / KVZ_NORM_K_PER_HEAD in norm_flags;
+ *                  norm_type KVZ_OUT_F32: float32, KVZ_OUT_BF16: BF16; 16-byte aligned.  NULL: that operand
+ *                  is not normed (both NULL: kvz_append_tokens)
+ *  norm_eps        >= 0; with 0 a head of zeros becomes NaN, as the formula says */
+#define KVZ_NORM_Q_PER_HEAD 1
+#define KVZ_NORM_K_PER_HEAD 2
+#define KVZ_NORM_FLAGS_ALL 3
+int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q,
+                             int64_t q_token_stride, int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                             int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                             const int32_t *slots, const int32_t *positions, int32_t num_axes, const uint64_t *rope,
+                             int32_t rot_dim, uint32_t flags, float rope_scale, const void *q_norm,
+                             const void *k_norm, int32_t norm_type, int32_t norm_flags, float norm_eps, void *q_out,
+                             void *raw_pool, int64_t num_raw_pages, uint32_t *status, kvz_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * kvz_plan_step / kvz_release_pages -- the tables of a serving step (several new tokens a request) built on the
+ * GPU, with pages out of a free list and back.  The pages name no such calls; they fill the tables that
+ * kvz_append_tokens and the attention calls over raw pages read, and can be captured into a graph with them.
+ *
+ *  rows         int32 [batch] (batch <= 1024) the requests' rows of lens and tables, no row twice; -1: no request
+ *               in this place
+ *  new_tokens   int32 [batch] >= 0, new tokens of each request
+ *  lens         int32 [num_rows] tokens that each row holds;  lens_out: the same after the step (may be lens)
+ *  tables       int32 [num_rows][width] each row's pages (ceil(lens / 16) of them), extended in place
+ *  free_pages   int32 [free_capacity], the first free_count[0] of them free; taken from the end on, requests
+ *               in order.  free_out: the count after the step (may be free_count)
+ *  q_start      int32 [batch + 1] where each request's new tokens begin among the step's
+ *  seq_lens     int32 [batch] tokens of each request, the new ones with them
+ *  page_ids     int32 [batch][width] its pages, -1 behind them
+ *  positions, slots  int32 [num_tokens] of each new token; behind the last one 0 and -1 (padding)
+ * No output may overlap an input or another output but for lens_out = lens and free_out = free_count.
+ * A step that cannot be taken is empty and changes nothing (q_start and seq_lens 0, slots and page_ids -1): a row out
+ * of range, a negative length, one beyond width pages, more tokens than num_tokens (KVZ_STATUS_BAD_INDEX), a row
+ * named twice (KVZ_STATUS_BAD_ORDER), too few free pages (KVZ_STATUS_ARENA_FULL).  A page id that no slot can name
+ * gives slot -1 and KVZ_STATUS_BAD_INDEX.
+ *
+ * kvz_release_pages: the rows' pages go back to the end of the free list, their lens become 0, their tables -1.
+ * The same conditions, and more pages than free_capacity has room for (KVZ_STATUS_BAD_INDEX), change nothing.
+ * --------------------------------------------------------------------------------- */
+int kvz_plan_step(int32_t batch, int32_t num_tokens, const int32_t *rows, const int32_t *new_tokens,
+                  const int32_t *lens, int32_t num_rows, int32_t *tables, int32_t width, const int32_t *free_pages,
+                  int32_t free_capacity, const int32_t *free_count, int32_t *q_start, int32_t *seq_lens,
+                  int32_t *page_ids, int32_t *positions, int32_t *slots, int32_t *lens_out, int32_t *free_out,
+                  uint32_t *status, kvz_stream_t stream);
+int kvz_release_pages(int32_t batch, const int32_t *rows, int32_t *lens, int32_t num_rows, int32_t *tables,
+                      int32_t width, int32_t *free_pages, int32_t free_capacity, int32_t *free_count,
+                      uint32_t *status, kvz_stream_t stream);
+
 /* ---------------------------------------------------------------------------------
  * Group-adaptive additive tiles: a second compressed format, from the page "GAAC:
  * Lossless KV Compression for Bandwidth-Efficient LLM Inference on Personal Devices"

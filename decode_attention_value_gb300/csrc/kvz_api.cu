@@ -960,6 +960,153 @@ int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, co
                                     num_raw_pages, status, stream);
 }
 
+// Where the parts of a chunk attention workspace are, from its start rounded up to 256 bytes.
+struct ChunkLayout {
+    size_t part_o = 0, part_ml, merge, table, pages, bytes;
+};
+static ChunkLayout chunk_layout(int grid, int64_t restored, int hkv)
+{
+    ChunkLayout l;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    l.part_ml = (size_t)grid * 2 * 256 * kDim * 4;
+    l.merge = l.part_ml + (size_t)grid * 2 * 256 * 8;
+    l.table = up(l.merge + (size_t)grid * 16);
+    l.pages = up(l.table + (size_t)restored * hkv * 4);
+    l.bytes = l.pages + (size_t)restored * hkv * 2 * kPage * kDim * 2;
+    return l;
+}
+// Raw pages that a call with 12-bit pages restores into its workspace (0 for a raw call), -1: too many.
+static int64_t chunk_restored(const kvz_dims &d, int batch, int max_pages, bool coded)
+{
+    const int64_t n = coded ? (int64_t)batch * (max_pages + 1LL) : 0;
+    return n * d.num_kv_heads * 32 >= (int64_t)1 << 31 ? -1 : n;
+}
+constexpr int kChunkMaxPages = 1 << 26;  // of a table: its keys are counted in 30 bits
+
+size_t kvz_chunk_attention_workspace_size(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
+                                          int32_t max_pages, int32_t coded)
+{
+    if (!dims_ok(dims) || num_tokens < 0 || batch < 0 || batch > kMaxBatch || max_pages < 0 || max_pages > kChunkMaxPages)
+        return 0;
+    if (num_q_heads < 1 || num_q_heads % dims.num_kv_heads != 0 || num_q_heads / dims.num_kv_heads > 8) return 0;
+    const int sms = sm_count();
+    const int64_t restored = chunk_restored(dims, batch, max_pages, coded != 0);
+    if (sms < 1 || restored < 0) return 0;
+    return chunk_layout(sms, restored, dims.num_kv_heads).bytes + 240;  // (from 16-byte alignment to 256)
+}
+
+static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const void *q, int32_t batch,
+                     const int32_t *q_start, const int32_t *page_ids, int32_t max_pages, const int32_t *seq_lens,
+                     const ChunkCoded *X, const void *raw_pool, int64_t num_raw_pages, int32_t window, int32_t sinks,
+                     void *out, int32_t out_type, void *ws, size_t ws_bytes, uint32_t *status, cudaStream_t stream)
+{
+    if (!dims_ok(d)) return d.num_kv_heads >= 1 ? KVZ_ERR_UNSUPPORTED : KVZ_ERR_INVALID_ARG;
+    if (num_tokens < 0 || batch < 0 || hq < 1 || max_pages < 0 || num_raw_pages < 0 || window < 0 || sinks < 0)
+        return KVZ_ERR_INVALID_ARG;
+    if (hq % d.num_kv_heads != 0 || (out_type != KVZ_OUT_F32 && out_type != KVZ_OUT_BF16)) return KVZ_ERR_INVALID_ARG;
+    const int G = hq / d.num_kv_heads;
+    if (G > 8 || batch > kMaxBatch || max_pages > kChunkMaxPages || num_tokens > 1 << 24) return KVZ_ERR_UNSUPPORTED;
+    if (num_tokens == 0 || batch == 0) return KVZ_OK;
+    if (!q || !q_start || !seq_lens || !out || !ws || !status || (max_pages > 0 && !page_ids)) return KVZ_ERR_INVALID_ARG;
+    if (num_raw_pages > 0 && !raw_pool) return KVZ_ERR_INVALID_ARG;
+    if (X && (!X->tail_page || !X->meta || !X->arena || X->num_meta_pages < 0)) return KVZ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(ws, 16) || !aligned(out, 32) || !aligned(raw_pool, 16) || !aligned(seq_lens, 4) ||
+        !aligned(q_start, 4) || !aligned(page_ids, 4) || !aligned(status, 4))
+        return KVZ_ERR_ALIGNMENT;
+    if (X && (!aligned(X->meta, 16) || !aligned(X->arena, 256) || !aligned(X->tail_page, 4))) return KVZ_ERR_ALIGNMENT;
+    if (num_raw_pages * d.num_kv_heads * 32 >= (int64_t)1 << 31) return KVZ_ERR_UNSUPPORTED;
+    const int64_t restored = chunk_restored(d, batch, max_pages, X != nullptr);
+    if (restored < 0) return KVZ_ERR_UNSUPPORTED;
+    const int sms = sm_count();
+    if (sms < 1) return KVZ_ERR_DEVICE;
+    const ChunkLayout at = chunk_layout(sms, restored, d.num_kv_heads);
+    const size_t pad = (size_t)(-reinterpret_cast<uintptr_t>(ws) & 255);
+    if (pad + at.bytes > ws_bytes) return KVZ_ERR_WORKSPACE;
+    uint8_t *const base = static_cast<uint8_t *>(ws) + pad;
+    ChunkParams P;
+    memset(&P, 0, sizeof P);
+    P.batch = batch;
+    P.hkv = d.num_kv_heads;
+    P.G = G;
+    P.tokens = num_tokens;
+    P.max_pages = X ? max_pages + 1 : max_pages;
+    P.id_page = X ? d.num_kv_heads : 1;
+    P.id_head = X ? 1 : 0;
+    P.len_pages = max_pages;
+    P.tail = X != nullptr;
+    // a window that no length reaches is none; sinks without a window are nothing
+    P.window = window >= P.max_pages * kPage ? 0 : window;
+    P.sinks = P.window > 0 ? (sinks < P.max_pages * kPage ? sinks : P.max_pages * kPage) : 0;
+    P.tile_tokens = 256 / G;
+    P.grid = sms;
+    // blocks of 128 keys (8 steps of a sum) between folds.  Each step drops about half of the last bit, 2^-25 of the
+    // sum: 8 blocks keep a float32 output within 2^-18 of that bias, 512 keep it under a BF16 output's rounding
+    P.fold = out_type == KVZ_OUT_BF16 ? 512 : 8;
+    P.over_G = 0xFFFFFFFFu / (uint32_t)G + 1;
+    P.q = static_cast<const uint16_t *>(q);
+    P.q_start = q_start;
+    P.seq_lens = seq_lens;
+    P.part_o = reinterpret_cast<float *>(base + at.part_o);
+    P.part_ml = reinterpret_cast<float *>(base + at.part_ml);
+    P.merge = reinterpret_cast<int4 *>(base + at.merge);
+    P.out = out;
+    P.out_bf16 = out_type == KVZ_OUT_BF16;
+    P.status = status;
+    P.scale_log2 = (float)(1.4426950408889634 / 11.313708498984761);  // log2(e) / sqrt(128)
+    ChunkCoded Y;
+    memset(&Y, 0, sizeof Y);
+    const void *pool = raw_pool;
+    P.num_raw_pages = num_raw_pages;
+    P.page_ids = page_ids;
+    if (X) {
+        Y = *X;
+        Y.page_ids = page_ids;
+        Y.raw_pool = static_cast<const uint16_t *>(raw_pool);
+        Y.num_raw_pages = num_raw_pages;
+        Y.table = reinterpret_cast<int32_t *>(base + at.table);
+        Y.pages = reinterpret_cast<uint16_t *>(base + at.pages);
+        P.page_ids = Y.table;
+        P.num_raw_pages = restored;
+        pool = Y.pages;
+    }
+    CUtensorMap map;
+    // a pool with no pages still needs a valid map object; it is never dereferenced
+    int rc = prefix_tensor_map(pool ? pool : base, P.num_raw_pages > 0 ? P.num_raw_pages : 1, d.num_kv_heads, &map);
+    if (rc) return rc;
+    cudaError_t e = launch_chunk(P, Y, &map, sms, stream);
+    return e == cudaSuccess ? KVZ_OK : fail_cuda(e);
+}
+
+int kvz_chunk_attention(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int32_t batch,
+                        const int32_t *q_start, const int32_t *page_ids, int32_t max_pages, const int32_t *seq_lens,
+                        const int32_t *tail_page, const uint64_t *meta, int64_t num_meta_pages, const uint8_t *arena,
+                        uint64_t arena_bytes, const void *raw_pool, int64_t num_raw_pages, int32_t window,
+                        int32_t sinks, void *out, int32_t out_type, void *workspace, size_t workspace_bytes,
+                        uint32_t *status, kvz_stream_t stream)
+{
+    ChunkCoded X;
+    memset(&X, 0, sizeof X);
+    X.tail_page = tail_page;
+    X.meta = meta;
+    X.num_meta_pages = num_meta_pages;
+    X.arena = arena;
+    X.arena_bytes = arena_bytes;
+    return run_chunk(dims, num_tokens, num_q_heads, q, batch, q_start, page_ids, max_pages, seq_lens, &X, raw_pool,
+                     num_raw_pages, window, sinks, out, out_type, workspace, workspace_bytes, status,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kvz_chunk_attention_raw(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int32_t batch,
+                            const int32_t *q_start, const int32_t *page_ids, int32_t max_pages,
+                            const int32_t *seq_lens, const void *raw_pool, int64_t num_raw_pages, int32_t window,
+                            int32_t sinks, void *out, int32_t out_type, void *workspace, size_t workspace_bytes,
+                            uint32_t *status, kvz_stream_t stream)
+{
+    return run_chunk(dims, num_tokens, num_q_heads, q, batch, q_start, page_ids, max_pages, seq_lens, nullptr, raw_pool,
+                     num_raw_pages, window, sinks, out, out_type, workspace, workspace_bytes, status,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
 // What plan_step and release_pages have in common.
 static int check_plan(int32_t batch, const int32_t *rows, const int32_t *lens, int32_t num_rows, const int32_t *tables,
                       int32_t width, const int32_t *free_pages, int32_t free_capacity, const int32_t *free_count,

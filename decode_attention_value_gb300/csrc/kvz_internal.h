@@ -195,6 +195,42 @@ cudaError_t launch_own(const AttnParams &A, const PrefixParams &P, int format, c
 cudaError_t launch_prefix(const PrefixParams &P, int format, const void *prefix_map, const AttnParams &A,
                           const void *own_map, int sms, cudaStream_t stream);
 
+// Attention of several new tokens a sequence (chunk.cu).
+struct ChunkParams {
+    int batch, hkv, G, tokens;
+    int max_pages, id_page, id_head;  // page_ids: [batch][max_pages], by KV head with id_head = 1, id_page = hkv
+    int len_pages;                    // pages of the table that lengths are cut to,
+    bool tail;                        // and whether a raw page may stand behind them
+    int window, sinks;                // window 0: all keys (sinks 0 then)
+    int tile_tokens;                  // new tokens of a tile: 256 / G
+    int grid, fold;                   // CTAs; blocks of a stream summed in tensor memory at a time
+    uint32_t over_G;                  // ceil(2^32 / G)
+    const uint16_t *q;
+    const int32_t *q_start, *page_ids, *seq_lens;
+    int64_t num_raw_pages;
+    float *part_o;   // [2 grid][8][16][32][8]: slot, 32 rows of the tile, 8 columns, row
+    float *part_ml;  // [2 grid][256][2]
+    int4 *merge;     // [grid] the unit that a CTA began and did not finish: pieces, rows, first token, KV head
+    void *out;
+    bool out_bf16;
+    uint32_t *status;
+    float scale_log2;
+};
+// 12-bit pages: where they are, and the raw pages and their table that the kernel above reads (table null: none).
+struct ChunkCoded {
+    const int32_t *page_ids, *tail_page;  // [batch][len_pages], [batch]
+    const uint64_t *meta;
+    int64_t num_meta_pages;
+    const uint8_t *arena;
+    uint64_t arena_bytes;
+    const uint16_t *raw_pool;
+    int64_t num_raw_pages;
+    int32_t *table;   // [batch][max_pages][hkv]
+    uint16_t *pages;  // [batch * max_pages][hkv][2][16][128]
+};
+// map: tensor map of the raw pages read, boxes as for launch_prefix
+cudaError_t launch_chunk(const ChunkParams &P, const ChunkCoded &X, const void *map, int sms, cudaStream_t stream);
+
 cudaError_t launch_encode(const EncodeParams &P, cudaStream_t stream);
 cudaError_t launch_enc_prepare(const EncodeParams &P, cudaStream_t stream);
 cudaError_t launch_encode_sizes(const EncodeParams &P, cudaStream_t stream);

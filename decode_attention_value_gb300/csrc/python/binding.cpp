@@ -9,6 +9,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <sstream>
 #include <string>
 
@@ -359,7 +360,73 @@ PyObject *plan_step(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// q, q_start, page_ids, seq_lens, tail_page, meta, arena, raw_pool, window, sinks, out, status, workspace, stream; the raw
+// call has None for tail_page, meta and arena
+PyObject *chunk_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded([&] {
+        count(n, 14);
+        const int dev = device_of(a[11]);
+        const bool coded = a[5] != Py_None;
+        const at::Tensor &q = tensor(a[0], "q"), &start = tensor(a[1], "q_start"), &ids = tensor(a[2], "page_ids");
+        const at::Tensor &lens = tensor(a[3], "seq_lens"), &pool = tensor(a[7], "raw_pool"), &out = tensor(a[10], "out");
+        const at::Tensor &ws = tensor(a[12], "workspace");
+        dims_of(q, "q", {-1, -1, 128}, "[tokens][heads][128]");
+        dims_of(lens, "seq_lens", {-1}, "[batch]");
+        const int64_t B = lens.size(0);
+        dims_of(start, "q_start", {B + 1}, "[batch + 1]");
+        dims_of(ids, "page_ids", {B, -1}, "[batch][pages]");
+        if (out.sizes() != q.sizes()) throw Refused{"out: expected " + shape_of(q) + ", got " + shape_of(out)};
+        if (out.scalar_type() != at::kFloat && out.scalar_type() != kBf16)
+            throw Refused{std::string("out: expected torch.float32 or torch.bfloat16, got ") + c10::toString(out.scalar_type())};
+        dims_of(pool, "raw_pool", {-1, -1, 2, 16, 128}, "[pages][heads][2][16][128]");
+        const int64_t hkv = pool.size(1);
+        const int32_t type = out.scalar_type() == at::kFloat ? KVZ_OUT_F32 : KVZ_OUT_BF16;
+        const void *qp = data(q, "q", dev, kBf16, kBf16);
+        const auto *sp = static_cast<const int32_t *>(data(start, "q_start", dev, kI32, kI32));
+        const auto *ip = static_cast<const int32_t *>(data(ids, "page_ids", dev, kI32, kI32));
+        const auto *lp = static_cast<const int32_t *>(data(lens, "seq_lens", dev, kI32, kI32));
+        const void *poolp = data(pool, "raw_pool", dev, kBf16, kBf16);
+        void *outp = data(out, "out", dev, out.scalar_type(), out.scalar_type());
+        void *wsp = data(ws, "workspace", dev, kU8, kU8);
+        uint32_t *status = data<uint32_t>(a[11], "status", dev, kI32, at::kUInt32);
+        const int64_t window = PyLong_AsLongLong(a[8]), sinks = PyLong_AsLongLong(a[9]);
+        if (PyErr_Occurred()) throw Refused{"window, sinks: expected whole numbers"};
+        if (window < 0 || sinks < 0) throw Refused{"window, sinks: expected numbers >= 0"};
+        const kvz_stream_t stream = stream_of(a[13], dev);
+        const kvz_dims dims{i32(hkv, "raw_pool"), 128, 16};
+        const int32_t T = i32(q.size(0), "tokens"), hq = i32(q.size(1), "heads"), b = i32(B, "batch");
+        const int32_t pages = i32(ids.size(1), "page_ids");
+        // (more than any length is no limit)
+        const int32_t w = (int32_t)std::min<int64_t>(window, INT32_MAX), k = (int32_t)std::min<int64_t>(sinks, INT32_MAX);
+        const int64_t num = pool.size(0);
+        const size_t bytes = (size_t)ws.numel();
+        int rc = 0;
+        if (!coded) {
+            Py_BEGIN_ALLOW_THREADS;
+            rc = kvz_chunk_attention_raw(dims, T, hq, qp, b, sp, ip, pages, lp, poolp, num, w, k, outp, type, wsp, bytes, status,
+                                         stream);
+            Py_END_ALLOW_THREADS;
+            return rc;
+        }
+        const at::Tensor &tail = tensor(a[4], "tail_page"), &meta = tensor(a[5], "meta"), &arena = tensor(a[6], "arena");
+        dims_of(tail, "tail_page", {B}, "[batch]");
+        dims_of(meta, "meta", {-1, hkv, 2}, "[pages][heads of raw_pool][2]");
+        const auto *tp = static_cast<const int32_t *>(data(tail, "tail_page", dev, kI32, kI32));
+        const auto *mp = static_cast<const uint64_t *>(data(meta, "meta", dev, kI64, at::kUInt64));
+        const auto *ap = static_cast<const uint8_t *>(data(arena, "arena", dev, kU8, kU8));
+        const int64_t meta_pages = meta.size(0);
+        const uint64_t arena_bytes = (uint64_t)arena.numel();
+        Py_BEGIN_ALLOW_THREADS;
+        rc = kvz_chunk_attention(dims, T, hq, qp, b, sp, ip, pages, lp, tp, mp, meta_pages, ap, arena_bytes, poolp, num, w, k,
+                                 outp, type, wsp, bytes, status, stream);
+        Py_END_ALLOW_THREADS;
+        return rc;
+    });
+}
+
 PyMethodDef methods[] = {
+    {"chunk_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(chunk_attention)), METH_FASTCALL, nullptr},
     {"plan_step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan_step)), METH_FASTCALL, nullptr},
     {"append_tokens", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append_tokens)), METH_FASTCALL, nullptr},
     {"prefix_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(prefix_attention)), METH_FASTCALL, nullptr},

@@ -362,6 +362,45 @@ int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_he
                              void *raw_pool, int64_t num_raw_pages, uint32_t *status, kvz_stream_t stream);
 
 /* ---------------------------------------------------------------------------------
+ * kvz_chunk_attention / kvz_chunk_attention_raw -- attention of several new tokens a sequence over the paged cache
+ * that holds them already: prompt chunks, draft tokens and single tokens of one batch, each token with the keys up
+ * to its own, or with a sliding window and the sequence's first tokens.  The pages name no such call.  What
+ * is not listed is as in kvz_decode_attention and kvz_decode_attention_raw.
+ *
+ *  q            BF16 [num_tokens][num_q_heads][128], 16-byte aligned; num_tokens <= 2^24
+ *  q_start      int32 [batch + 1] (batch <= 1024), non-decreasing, within [0, num_tokens]: the new tokens of sequence b
+ *               are q_start[b] .. q_start[b + 1] - 1, any number of them.  Rows of no sequence (padding) are left
+ *               as they were.  Out of order or range: KVZ_STATUS_BAD_ORDER, and nothing is computed
+ *  seq_lens     int32 [batch] tokens of each sequence, the new ones with them: new token i of n stands at
+ *               p = seq_lens - n + i.  A token before the first (n > seq_lens) sees nothing: zero
+ *  page_ids, max_pages, tail_page: as in those calls; max_pages <= 2^26
+ *  window       0: token p sees the keys j <= p.  W > 0: of these j > p - W, and j < sinks.  Pages that no new token
+ *               sees are not read, and their ids may be anything
+ *  sinks        first tokens of each sequence that stay visible behind the window (nothing without one)
+ *  out          out_type KVZ_OUT_F32 or KVZ_OUT_BF16, [num_tokens][num_q_heads][128], 32-byte aligned:
+ *               softmax(q.K^T / sqrt(128)) V over what each token sees.  BF16 outputs take weights rounded to BF16,
+ *               float32 ones all bits of them
+ *  workspace    >= kvz_chunk_attention_workspace_size(dims, num_tokens, num_q_heads, batch, max_pages, coded)
+ *               bytes (16-B aligned), coded = 1 for kvz_chunk_attention, whose workspace also holds the pages
+ *               that it reads as raw pages: batch * (max_pages + 1) of one layer
+ * A value that is not finite may reach every new token of its sequence within 256 query rows of one that sees it.
+ * Results depend on the data, the shapes, the lengths and the device's SM count only.
+ * --------------------------------------------------------------------------------- */
+size_t kvz_chunk_attention_workspace_size(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
+                                          int32_t max_pages, int32_t coded);
+int kvz_chunk_attention(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int32_t batch,
+                        const int32_t *q_start, const int32_t *page_ids, int32_t max_pages, const int32_t *seq_lens,
+                        const int32_t *tail_page, const uint64_t *meta, int64_t num_meta_pages, const uint8_t *arena,
+                        uint64_t arena_bytes, const void *raw_pool, int64_t num_raw_pages, int32_t window,
+                        int32_t sinks, void *out, int32_t out_type, void *workspace, size_t workspace_bytes,
+                        uint32_t *status, kvz_stream_t stream);
+int kvz_chunk_attention_raw(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int32_t batch,
+                            const int32_t *q_start, const int32_t *page_ids, int32_t max_pages,
+                            const int32_t *seq_lens, const void *raw_pool, int64_t num_raw_pages, int32_t window,
+                            int32_t sinks, void *out, int32_t out_type, void *workspace, size_t workspace_bytes,
+                            uint32_t *status, kvz_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
  * kvz_plan_step / kvz_release_pages -- the tables of a serving step (several new tokens a request) built on the
  * GPU, with pages out of a free list and back.  The pages name no such calls; they fill the tables that
  * kvz_append_tokens and the attention calls over raw pages read, and can be captured into a graph with them.

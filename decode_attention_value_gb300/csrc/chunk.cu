@@ -7,9 +7,10 @@
 // group) of a tile are the rows of a matrix Q: S = Q K^T, P = exp2(S c - m) with scores of unseen keys minus
 // infinity, O = P V, with the running maximum m and sum l of each row, O / l at the end.
 //
-// Bound: the latency of a row's softmax (2039 tokens behind 30710, 32/8 heads: 822 us, 1.29 PFLOP/s, tensor pipe 53 % busy), then
-// the tensor cores for chunks, two products of 128 x 128 x 128 a tile of 128 rows and block of keys; the bytes
-// of the pages for few rows (64 single tokens with a window of 4096: 181 us, 6.0 TB/s).
+// Bound: the latency of a row's softmax (2039 tokens behind 30710, 32/8 heads: 1062 us, 1.0 PFLOP/s, 1.5 as issued with
+// the second part of each weight), then the tensor cores for chunks, three products of 128 x 128 x 128 a tile of 128
+// rows and block of keys (S, and O for each part); the bytes of the pages for few rows (64 single tokens with a
+// window of 4096: 185 us, 5.9 TB/s).
 //
 // Split: a unit is (sequence, KV head, tile of up to 256 rows) and has as many blocks of 128 keys as its rows see; the
 // units' blocks are one line, cut into equal ranges, a CTA each, so any mix of chunks and single tokens
@@ -475,14 +476,13 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
             if (last) mma_commit(go, sb + S::qempty + 8 * qtile);
         };
         // output of stream s: its weights of 64 tokens times half of the V block in slot
-        constexpr int kTwo = kParts == 1 ? 1 : 2;  // parts of a weight beside the scores they replace
         auto pv = [&](uint32_t s, uint32_t slot, uint32_t half, bool add) {
             const uint64_t b = smem_desc(sb + S::ring + slot * kChUnit + half * 8 * 1024, kChHalf, 1024);
             const uint32_t w = tm + s * 128 + half * 64, o = tm + kChColO + s * 128;
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // 16 tokens: two atoms of V rows, eight columns of weights
 #pragma unroll
-                for (int part = 0; part < kTwo; ++part)
+                for (int part = 0; part < 2; ++part)
                     mma_ts(go, o, w + (k >> 1) * 32 + part * 16 + (k & 1) * 8, b + ((k * 2 * 1024) >> 4), kPv,
                            part || k ? true : add);
             if (kParts == 3 && half == 0) mma_commit(go, sb + S::pused + 8 * s);
@@ -551,10 +551,11 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ================================ softmax ================================
         // Thread = query row.  The running maximum moves, and the output is rescaled, only when it grows by more
-        // than 2^8: weights up to 2^8 lose nothing in floating point.  BF16 outputs take one BF16 part of
-        // each weight: 2^-9 of it at most, as much as the output's own rounding; fp32 outputs three (all of it).  The
-        // sum is of the unrounded weights.  Every P.fold blocks the output is added to the rows' partials in
-        // memory and begins anew: the tensor cores' fp32 sums drop the bits below the accumulator's last.
+        // than 2^8: weights up to 2^8 lose nothing in floating point.  Weights are two BF16 parts, off by at most 2^-17
+        // of a weight, a 2^-9 part of a BF16 output's own rounding (one part: 2^-8, which made the error of an output
+        // 2.1e-3 where its rounding makes 1.6e-3); fp32 outputs take three (all of it).  The sum is of the
+        // unrounded weights.  Every P.fold blocks the output is added to the rows' partials in memory and begins
+        // anew: the tensor cores' fp32 sums drop the bits below the accumulator's last.
         const int s = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + kChColO + s * 128 + lanes;
@@ -712,20 +713,20 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
                                 const uint64_t e = pack2(p0, p1);
                                 sum[i & 1] = add2(sum[i & 1], e);
                                 hi2[i] = pack_bf16x2(p0, p1);
+                                auto rest = [&](uint64_t y, uint32_t part) {  // y without its BF16 part, exact
+                                    return fma2(pack2(__uint_as_float(part << 16), __uint_as_float(part & 0xFFFF0000u)), minus, y);
+                                };
+                                float r0, r1;
+                                const uint64_t d = rest(e, hi2[i]);
+                                unpack2(d, r0, r1);
+                                lo2[i] = pack_bf16x2(r0, r1);
                                 if (kParts == 3) {
-                                    auto rest = [&](uint64_t y, uint32_t part) {  // y without its BF16 part, exact
-                                        return fma2(pack2(__uint_as_float(part << 16), __uint_as_float(part & 0xFFFF0000u)), minus, y);
-                                    };
-                                    float r0, r1;
-                                    const uint64_t d = rest(e, hi2[i]);
-                                    unpack2(d, r0, r1);
-                                    lo2[i] = pack_bf16x2(r0, r1);
                                     unpack2(rest(d, lo2[i]), r0, r1);
                                     third[(kParts == 3 ? 2 * half : 0) + (kParts == 3 ? w : 0)][i] = pack_bf16x2(r0, r1);
                                 }
                             }
                             tmem_st16(tS + 64 * half + 32 * w, hi2);
-                            if (kParts == 3) tmem_st16(tS + 64 * half + 32 * w + 16, lo2);
+                            tmem_st16(tS + 64 * half + 32 * w + 16, lo2);
                         }
                         tmem_wait_st();
                     }
@@ -1026,7 +1027,7 @@ cudaError_t launch_chunk(const ChunkParams &P, const ChunkCoded &X, const void *
         const cudaError_t e = cudaLaunchKernelEx(&cfg, k_chunk_restore, P, X);
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = P.out_bf16 ? launch_chunk_impl<1>(P, m, cfg) : launch_chunk_impl<3>(P, m, cfg);
+    cudaError_t e = P.out_bf16 ? launch_chunk_impl<2>(P, m, cfg) : launch_chunk_impl<3>(P, m, cfg);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(P.grid, kChunkRows / 32);
     cfg.blockDim = dim3(kChMergeThreads);

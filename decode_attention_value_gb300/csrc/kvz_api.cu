@@ -1039,9 +1039,10 @@ static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const vo
     P.sinks = P.window > 0 ? (sinks < P.max_pages * kPage ? sinks : P.max_pages * kPage) : 0;
     P.tile_tokens = 256 / G;
     P.grid = sms;
-    // blocks of 128 keys (8 steps of a sum) between folds.  Each step drops about half of the last bit, 2^-25 of the
-    // sum: 4 blocks keep a float32 output within 2^-19 of that bias, 512 keep it under a BF16 output's rounding
-    P.fold = out_type == KVZ_OUT_BF16 ? 512 : 4;
+    // blocks of 128 keys (8 steps of a sum, for each weight part) between folds.  Each step drops about half of the last
+    // bit, 2^-25 of the sum: 4 blocks keep a float32 output within 2^-18 of that bias, 256 keep it under a BF16
+    // output's rounding (2^-13 beside 2^-8)
+    P.fold = out_type == KVZ_OUT_BF16 ? 256 : 4;
     P.over_G = 0xFFFFFFFFu / (uint32_t)G + 1;
     P.q = static_cast<const uint16_t *>(q);
     P.q_start = q_start;

@@ -378,8 +378,8 @@ int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_he
  *               sees are not read, and their ids may be anything
  *  sinks        first tokens of each sequence that stay visible behind the window (nothing without one)
  *  out          out_type KVZ_OUT_F32 or KVZ_OUT_BF16, [num_tokens][num_q_heads][128], 32-byte aligned:
- *               softmax(q.K^T / sqrt(128)) V over what each token sees.  BF16 outputs take weights rounded to BF16,
- *               float32 ones all bits of them
+ *               softmax(q.K^T / sqrt(128)) V over what each token sees.  BF16 outputs take weights to 2^-17 of
+ *               each, float32 ones all bits of them
  *  workspace    >= kvz_chunk_attention_workspace_size(dims, num_tokens, num_q_heads, batch, max_pages, coded)
  *               bytes (16-B aligned), coded = 1 for kvz_chunk_attention, whose workspace also holds the pages
  *               that it reads as raw pages: batch * (max_pages + 1) of one layer

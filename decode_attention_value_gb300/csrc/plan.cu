@@ -20,9 +20,9 @@ namespace kvz {
 constexpr int kPlanThreads = kMaxBatch, kPlanCtas = 8;
 constexpr int kPlanSeen = 4096;  // places of the rows already named: a quarter full at most
 
-__device__ __forceinline__ void cluster_meet()
+__device__ __forceinline__ void cluster_meet()  // thread by thread: lanes of a warp may come here apart
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Sums of two values over the threads before this one, and over all.

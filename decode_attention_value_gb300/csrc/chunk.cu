@@ -775,6 +775,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
                 if (active && !sg.whole()) {
                     fold(m);
                     if (lane < rows) *reinterpret_cast<float2 *>(P.part_ml + (slot0 + lane) * 2) = make_float2(m, l);
+                    __syncwarp();
                 } else if (active) {
                     const float f = !folded || fm == -INFINITY ? 0.f : ex2(fm - m), k = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -823,6 +824,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
                         const float y = fa ? (lane < rows ? at[(i >> 3) * 256 + (i & 7)] : 0.f) : __uint_as_float(v[i]);
                         o[i] = ka > 0.f ? y * ka : 0.f;
                     }
+                    __syncwarp();
                     if (nb > 1) {
                         tmem_ld32(tmem + kChColO + 128 + lanes + 32 * w, v);
                         tmem_wait_ld(v);
@@ -832,6 +834,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
                             const float y = fb ? (lane < rows ? bt[(i >> 3) * 256 + (i & 7)] : 0.f) : __uint_as_float(v[i]);
                             if (kb > 0.f) o[i] = fmaf(y, kb, o[i]);
                         }
+                        __syncwarp();
                     }
                     if (lane < rows) {
                         if (sg.whole()) {
@@ -848,6 +851,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
                 }
                 if (s == 0 && lane < rows && !sg.whole())
                     *reinterpret_cast<float2 *>(P.part_ml + ((int64_t)sg.slot * kChunkRows + r) * 2) = make_float2(top, sum);
+                __syncwarp();
                 tc_fence_before();
                 meet();  // (the next segment's first products overwrite both outputs)
                 if (!__all_sync(0xffffffffu, wait.ok)) break;

@@ -510,7 +510,8 @@ def plan_step(rows, new_tokens, lens, tables, free_pages, free_count, plan: Step
 
 
 def release_pages(rows, lens, tables, free_pages, free_count, status, stream=None):
-    """Give the pages of rows (int32 [B], -1: none) back to the free list of plan_step: their lens become 0."""
+    """Give the pages of rows (int32 [B], -1: none) back to the free list of plan_step: their lens become 0.  Entries of
+    tables that are -1 (pages behind a sliding window that were given back before) are passed over."""
     if tables.dim() != 2 or lens.numel() != tables.shape[0] or free_count.numel() != 1:
         raise ValueError("lens, tables, free_count: expected [rows], [rows][pages] and one value")
     i32 = torch.int32

@@ -69,6 +69,9 @@ __device__ __forceinline__ bool named_before(int32_t *seen, int32_t row)
 
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
 
+// Whether id is a page whose rows slots can name.
+__device__ __forceinline__ bool page_named(int32_t id) { return id >= 0 && id <= INT32_MAX / kPage; }
+
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1) k_plan(const PlanParams P)
 {
     __shared__ int32_t seen[kPlanSeen];
@@ -165,7 +168,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             }
             pos = after[lo] - (start[lo + 1] - start[lo]) + (i - start[lo]);
             const int32_t id = page(lo, pos / kPage);
-            if (id >= 0 && id <= INT32_MAX / kPage) slot = id * kPage + pos % kPage;
+            if (page_named(id)) slot = id * kPage + pos % kPage;
             else atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
         }
         P.positions[i] = pos;
@@ -174,12 +177,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 }
 
 // Pages of finished requests back to the end of the free list, the last page of each first, so that the next
-// request takes them in the order they were in.  One block: 4 KB of lengths and the rows' pages.
+// request takes them in the order they were in.  An entry that names no page (given back before from behind a
+// window) is passed over, so a row's pages are counted first.  One block: 4 KB of lengths and, twice, the rows' pages.
 __global__ void __launch_bounds__(kPlanThreads, 1) k_release(const PlanParams P)
 {
     __shared__ int32_t seen[kPlanSeen];
     __shared__ int64_t red[kPlanThreads / 32][2];
-    __shared__ int32_t begin[kMaxBatch], count[kMaxBatch], row_of[kMaxBatch];
+    __shared__ int32_t begin[kMaxBatch], held[kMaxBatch], span[kMaxBatch], row_of[kMaxBatch];
     __shared__ uint32_t bad;
     const int tid = threadIdx.x, lane = tid & 31;
     for (int i = tid; i < kPlanSeen; i += kPlanThreads) seen[i] = -1;
@@ -199,32 +203,50 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_release(const PlanParams P)
             flag |= KVZ_STATUS_BAD_INDEX;
         }
     }
-    if (flag) {
-        atomicOr(&bad, flag);
-        len = 0;
+    if (flag) atomicOr(&bad, flag);
+    span[tid] = flag || row < 0 ? 0 : pages_of(len);
+    row_of[tid] = row;
+    held[tid] = 0;
+    __syncthreads();
+    const bool any = bad == 0;
+    // a row's pages in order, one warp: f(place in the row, page, how many stand before it); returns how many they are
+    auto pages = [&](int b, auto &&f) {
+        const int32_t *from = P.tables + (int64_t)row_of[b] * P.width;
+        int n = 0;
+        for (int c0 = 0; c0 < span[b]; c0 += 256) {  // eight loads at once
+            int32_t id[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) id[k] = c0 + 32 * k + lane < span[b] ? from[c0 + 32 * k + lane] : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t live = __ballot_sync(0xffffffffu, page_named(id[k]));
+                f(c0 + 32 * k + lane, id[k], n + __popc(live & ((1u << lane) - 1)));
+                n += __popc(live);
+            }
+        }
+        return n;
+    };
+    for (int b = tid >> 5; b < P.batch && any; b += kPlanThreads / 32) {
+        const int n = pages(b, [](int, int32_t, int) {});
+        if (lane == 0) held[b] = n;
     }
-    int64_t v[2] = {pages_of(len), 0}, all[2];
+    __syncthreads();
+    int64_t v[2] = {held[tid], 0}, all[2];
     block_sums(v, all, red);
-    if (tid == 0 && !bad && all[0] > P.free_capacity - spare) bad = KVZ_STATUS_BAD_INDEX;  // more than there are
+    if (tid == 0 && any && all[0] > P.free_capacity - spare) bad = KVZ_STATUS_BAD_INDEX;  // more than there are
+    begin[tid] = spare + (int32_t)v[0];
     __syncthreads();
     if (bad) {  // nothing changes
         if (tid == 0) atomicOr(P.status, bad);
         return;
     }
-    if (tid < P.batch) {
-        begin[tid] = spare + (int32_t)v[0];
-        count[tid] = pages_of(len);
-        row_of[tid] = row;
-        if (row >= 0) P.lens_out[row] = 0;
-    }
+    if (tid < P.batch && row >= 0) P.lens_out[row] = 0;
     if (tid == 0) P.free_out[0] = spare + (int32_t)all[0];
-    __syncthreads();
     for (int b = tid >> 5; b < P.batch; b += kPlanThreads / 32)
-        for (int c = lane; c < count[b]; c += 32) {
-            int32_t *from = P.tables + (int64_t)row_of[b] * P.width + c;
-            P.free_out_pages[begin[b] + count[b] - 1 - c] = *from;
-            *from = -1;
-        }
+        pages(b, [&](int c, int32_t id, int nth) {
+            if (page_named(id)) P.free_out_pages[begin[b] + held[b] - 1 - nth] = id;
+            if (c < span[b]) P.tables[(int64_t)row_of[b] * P.width + c] = -1;
+        });
 }
 
 cudaError_t launch_plan(const PlanParams &P, bool release, cudaStream_t stream)

@@ -423,7 +423,9 @@ int kvz_chunk_attention_raw(kvz_dims dims, int32_t num_tokens, int32_t num_q_hea
  * gives slot -1 and KVZ_STATUS_BAD_INDEX.
  *
  * kvz_release_pages: the rows' pages go back to the end of the free list, their lens become 0, their tables -1.
- * The same conditions, and more pages than free_capacity has room for (KVZ_STATUS_BAD_INDEX), change nothing.
+ * Entries that no slot can name (-1 where a page behind a sliding window was given back before) are passed over: who
+ * gives back a page by other means sets its entry to -1, or it is free twice.  The same conditions, and more
+ * pages than free_capacity has room for (KVZ_STATUS_BAD_INDEX), change nothing.
  * --------------------------------------------------------------------------------- */
 int kvz_plan_step(int32_t batch, int32_t num_tokens, const int32_t *rows, const int32_t *new_tokens,
                   const int32_t *lens, int32_t num_rows, int32_t *tables, int32_t width, const int32_t *free_pages,

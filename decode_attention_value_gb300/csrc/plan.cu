@@ -7,7 +7,7 @@
 // same lengths give the same tables.
 //
 // Bound: launch and a chain of dependent reads (rows, lengths, prefix sums, pages): 256 requests x 512 pages
-// 10.0 us, 61 prompts of 29 K tokens x 2048 pages 13.0 us.
+// 10.3 us, 61 prompts of 29 K tokens x 2048 pages 13.1 us.
 //
 // Split: one cluster of eight blocks.  Each works out both sums itself (a thread a request, 4 KB of
 // lengths), they meet once, so that everything that a call may update in place has been read, and then
@@ -86,7 +86,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     __syncthreads();
     // ---- what the requests ask for ----
     const int32_t spare = P.free_count[0];
-    int row = -1, len = 0, fresh_tokens = 0;
+    int row = -1, len = 0, fresh_tokens = 0, last = 0;  // last: the page that takes its first new tokens
     uint32_t flag = spare < 0 || spare > P.free_capacity ? KVZ_STATUS_BAD_INDEX : 0;
     if (tid < P.batch) {
         row = P.rows[tid];
@@ -97,6 +97,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                 flag |= KVZ_STATUS_BAD_INDEX;
             else if (named_before(seen, row))
                 flag |= KVZ_STATUS_BAD_ORDER;
+            else if (fresh_tokens > 0 && len % kPage != 0)
+                last = P.tables[(int64_t)row * P.width + len / kPage];
         } else if (row != -1) {
             flag |= KVZ_STATUS_BAD_INDEX;
         }
@@ -112,7 +114,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         else if (all[1] > spare) bad = KVZ_STATUS_ARENA_FULL;
     }
     __syncthreads();
-    const bool ok = bad == 0;  // else: a step without requests, and nothing changes
+    // every page that takes a new token is one whose rows slots can name
+    const bool fits = bad == 0;
+    bool named = page_named(last);
+    if (fits)
+        for (int i = tid; i < (int)all[1]; i += kPlanThreads) named &= page_named(P.free_pages[spare - 1 - i]);
+    const uint32_t wrong = __syncthreads_or(!named) ? KVZ_STATUS_BAD_INDEX : 0;
+    const bool ok = fits && !wrong;  // else: a step without requests, and nothing changes
     if (tid < P.batch) {
         start[tid] = ok ? (int32_t)v[0] : 0;
         have[tid] = ok && row >= 0 ? pages_of(len) : 0;
@@ -121,7 +129,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         fresh[tid] = ok ? spare - 1 - (int32_t)v[1] : 0;  // its first page of the free list, the next ones before it
     }
     if (tid == 0) start[P.batch] = ok ? (int32_t)all[0] : 0;
-    if (cta == 0 && tid == 0 && !ok) atomicOr(P.status, bad);
+    if (cta == 0 && tid == 0 && !ok) atomicOr(P.status, fits ? wrong : bad);
     if (P.lens_out != P.lens)
         for (int i = at; i < P.num_rows; i += step) P.lens_out[i] = P.lens[i];
     cluster_meet();  // lengths and the free list's count have been read, copied lengths written
@@ -167,9 +175,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                 else hi = mid - 1;
             }
             pos = after[lo] - (start[lo + 1] - start[lo]) + (i - start[lo]);
-            const int32_t id = page(lo, pos / kPage);
-            if (page_named(id)) slot = id * kPage + pos % kPage;
-            else atomicOr(P.status, KVZ_STATUS_BAD_INDEX);
+            slot = page(lo, pos / kPage) * kPage + pos % kPage;
         }
         P.positions[i] = pos;
         P.slots[i] = slot;

@@ -418,9 +418,9 @@ int kvz_chunk_attention_raw(kvz_dims dims, int32_t num_tokens, int32_t num_q_hea
  *  positions, slots  int32 [num_tokens] of each new token; behind the last one 0 and -1 (padding)
  * No output may overlap an input or another output but for lens_out = lens and free_out = free_count.
  * A step that cannot be taken is empty and changes nothing (q_start and seq_lens 0, slots and page_ids -1): a row out
- * of range, a negative length, one beyond width pages, more tokens than num_tokens (KVZ_STATUS_BAD_INDEX), a row
- * named twice (KVZ_STATUS_BAD_ORDER), too few free pages (KVZ_STATUS_ARENA_FULL).  A page id that no slot can name
- * gives slot -1 and KVZ_STATUS_BAD_INDEX.
+ * of range, a negative length, one beyond width pages, more tokens than num_tokens, a new token whose page no slot can
+ * name (the id, held or free, outside 0 .. 2^27 - 1) (all KVZ_STATUS_BAD_INDEX), a row named twice
+ * (KVZ_STATUS_BAD_ORDER), too few free pages (KVZ_STATUS_ARENA_FULL).
  *
  * kvz_release_pages: the rows' pages go back to the end of the free list, their lens become 0, their tables -1.
  * Entries that no slot can name (-1 where a page behind a sliding window was given back before) are passed over: who

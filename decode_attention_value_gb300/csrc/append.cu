@@ -12,7 +12,7 @@
 //
 // With norm weights a head x of queries or keys becomes x / sqrt(mean x^2 + eps) * w first, in fp32 too: the rounding
 // to BF16 is still the only one.  The sum of squares is over the eight lanes that hold the head, so the norm
-// costs no pass over memory: 16381 tokens of 48 heads take 103 us with norms.
+// costs no pass over memory: 16381 tokens of 48 heads take 102 us with norms.
 //
 // Bound: memory.  (Hq + 2 Hkv) 256 bytes a token are read once and written once: 16381 tokens of 48
 // heads in 64 to 67 us, 6.0 to 6.2 TB/s, 0.88 to 0.91 of the measured copy bandwidth; one decode token is a launch.
@@ -32,7 +32,9 @@ namespace kvz {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = kAppendThreads / 8;  // rows a block handles at once
 constexpr int kAppendTokens = 8;                 // tokens a block may touch
-constexpr int kAppendResident = 3;               // blocks an SM holds
+// Blocks an SM holds.  With norms two, whose threads need 111 registers: at three, with 80, they spill (16381 tokens
+// of 48 heads 111 us instead of 102).
+constexpr int append_resident(bool norm) { return norm ? 2 : 3; }
 
 // cs: the first of the eight pairs' (cos, sin), the next ones eight further each
 __device__ __forceinline__ void rotate8(uint4 &x, uint4 &y, const float2 *cs, bool neighbours)
@@ -83,23 +85,36 @@ __device__ __forceinline__ void norm8(const AppendParams &P, uint4 &x, uint4 &y,
                                       const float2 *cs, uint32_t with)
 {
     uint32_t *u[2] = {reinterpret_cast<uint32_t *>(&x), reinterpret_cast<uint32_t *>(&y)};
+    auto value = [&](int i) {
+        const uint32_t two = u[i >> 3][i >> 1 & 3];
+        return __uint_as_float(i & 1 ? two & 0xFFFF0000u : two << 16);
+    };
+    auto mean = [&](float by, float eps) {  // of the squares of the head times by, and eps
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = value(i) * by;
+            sum = fmaf(v, v, sum);
+        }
+#pragma unroll
+        for (int off = 4; off; off >>= 1) sum += __shfl_xor_sync(with, sum, off);
+        return fmaf(sum, 1.f / kDim, eps);
+    };
+    float by = 1.f, t = mean(1.f, P.eps);
+    if (!(t > 0x1p-100f && t < INFINITY)) {
+        // the squares leave fp32's range (the eight lanes agree): the head and sqrt(eps) by a power of two that
+        // leaves the quotient as it is.  2^-68: 128 squares of the largest BF16 make 2^127; 2^100: values are below
+        // 2^-46 here, and the smallest's square is 2^-66
+        by = t > 1.f ? 0x1p-68f : 0x1p100f;
+        t = mean(by, P.eps * by * by);
+    }
+    // (square root and quotient are off by 2^-24 each; rsqrtf by up to 2^-22)
+    const float r = 1.f / sqrtf(t);
     float f[16], wt[16];
     norm_weights(P, w, e0, wt);
     norm_weights(P, w, e1, wt + 8);
-    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[2 * i] = __uint_as_float(u[i >> 2][i & 3] << 16);
-        f[2 * i + 1] = __uint_as_float(u[i >> 2][i & 3] & 0xFFFF0000u);
-        sum = fmaf(f[2 * i], f[2 * i], sum);
-        sum = fmaf(f[2 * i + 1], f[2 * i + 1], sum);
-    }
-#pragma unroll
-    for (int off = 4; off; off >>= 1) sum += __shfl_xor_sync(with, sum, off);
-    // (the two roundings of 1 / sqrt are 1.5 units of 2^-24; rsqrtf's 2)
-    const float r = 1.f / sqrtf(fmaf(sum, 1.f / kDim, P.eps));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] *= r * wt[i];
+    for (int i = 0; i < 16; ++i) f[i] = value(i) * by * r * wt[i];  // (a normed value is 11.4 at most, r * wt may be anything)
     auto turn = [&](float &a, float &b, const float2 t) {
         const float ra = a * t.x - b * t.y, rb = a * t.y + b * t.x;
         a = ra;
@@ -117,7 +132,7 @@ __device__ __forceinline__ void norm8(const AppendParams &P, uint4 &x, uint4 &y,
 }
 
 template <bool kNorm>
-__global__ void __launch_bounds__(kAppendThreads, kAppendResident) k_append(const AppendParams P)
+__global__ void __launch_bounds__(kAppendThreads, append_resident(kNorm)) k_append(const AppendParams P)
 {
     __shared__ float2 cs[kAppendTokens][64];
     const int H = P.hq + 2 * P.hkv, tid = threadIdx.x;
@@ -223,9 +238,10 @@ cudaError_t launch_append(AppendParams P, int sms, cudaStream_t stream)
 {
     const int H = P.hq + 2 * P.hkv;
     const int64_t rows = (int64_t)P.tokens * H;
+    const int64_t wave = (int64_t)kAppendRows * append_resident(P.q_norm || P.k_norm) * sms;  // rows handled at once
     // passes of a block: as few as let one wave hold all rows, at most eight (whole tokens share their
     // sines), and even, since a thread keeps two rows in flight (1021 tokens of 48 rows: 7.4 us with eight)
-    int64_t passes = (rows + (int64_t)kAppendRows * kAppendResident * sms - 1) / ((int64_t)kAppendRows * kAppendResident * sms);
+    int64_t passes = (rows + wave - 1) / wave;
     passes = passes <= 1 ? 1 : passes >= 8 ? 8 : (passes + 1) & ~1ll;
     int64_t per = passes * kAppendRows;
     const int64_t most = (int64_t)(kAppendTokens - 2) * H + 1;  // touches at most kAppendTokens tokens

@@ -345,7 +345,9 @@ int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, co
 
 /* kvz_append_tokens_normed -- kvz_append_tokens with a norm of each query and key head before the rotation:
  * x / sqrt(mean(x^2) + norm_eps) * weight over the head's 128 values, in fp32, with the rotation's rounding to
- * BF16 as the only one.
+ * BF16 as the only one.  Any finite head will do: squares that leave fp32's range are taken of a head scaled by a
+ * power of two.  (A value that is 2^-126 of its head's root mean square, or less, has fewer bits before it meets its
+ * weight, as fp32 has there.)
  *  q_norm, k_norm  weights [128], or [heads][128] with KVZ_NORM_Q_PER_HEAD / KVZ_NORM_K_PER_HEAD in norm_flags;
  *                  norm_type KVZ_OUT_F32: float32, KVZ_OUT_BF16: BF16; 16-byte aligned.  NULL: that operand
  *                  is not normed (both NULL: kvz_append_tokens)

@@ -753,6 +753,8 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
             }
             n0 += nb;
             // ---- the segment's rows: to the output, or to their partials ----
+            // (a maximum of minus infinity says that a partial has no key, which is not so where all scores were NaN)
+            const float ml = l != l ? 0.f : m;
             wait(sbase + S::ofull + 8 * s, seg & 1);
             if (!__all_sync(0xffffffffu, wait.ok)) break;
             tc_fence_after();
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
             if (!both) {
                 if (active && !sg.whole()) {
                     fold(m);
-                    if (lane < rows) *reinterpret_cast<float2 *>(P.part_ml + (slot0 + lane) * 2) = make_float2(m, l);
+                    if (lane < rows) *reinterpret_cast<float2 *>(P.part_ml + (slot0 + lane) * 2) = make_float2(ml, l);
                     __syncwarp();
                 } else if (active) {
                     const float f = !folded || fm == -INFINITY ? 0.f : ex2(fm - m), k = l == 0.f ? 0.f : 1.f / l;
@@ -802,7 +804,7 @@ __global__ void __launch_bounds__(kChThreads, 1) k_chunk(const ChunkParams P, co
                 // folded leaves all of its output in memory
                 const bool fa = (nb + 1) / 2 > P.fold, fb = nb / 2 > P.fold;
                 if (s == 0 ? fa : fb) fold(m);
-                xml[128 * s + r] = make_float2(m, l);
+                xml[128 * s + r] = make_float2(ml, l);
                 tc_fence_before();
                 meet();
                 if (!__all_sync(0xffffffffu, wait.ok)) break;

@@ -385,7 +385,8 @@ int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_he
  *  workspace    >= kvz_chunk_attention_workspace_size(dims, num_tokens, num_q_heads, batch, max_pages, coded)
  *               bytes (16-B aligned), coded = 1 for kvz_chunk_attention, whose workspace also holds the pages
  *               that it reads as raw pages: batch * (max_pages + 1) of one layer
- * A value that is not finite may reach every new token of its sequence within 256 query rows of one that sees it.
+ * A key or value that is not finite may reach every new token of its sequence within 256 query rows of one that sees it;
+ * a query that is not makes its own rows NaN.
  * Results depend on the data, the shapes, the lengths and the device's SM count only.
  * --------------------------------------------------------------------------------- */
 size_t kvz_chunk_attention_workspace_size(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,

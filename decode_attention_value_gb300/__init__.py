@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from typing import NamedTuple
 
@@ -63,7 +64,7 @@ EXPORTS = (
     "kvz_selftest_bounded_wait", "kvz_encode_sizes", "kvz_alloc_reserve_granules", "kvz_alloc_room",
     "kvz_f8_calibrate", "kvz_f8_encode_pages", "kvz_f8_decode_blocks", "kvz_f8_decode_attention",
     "kvz_decode_attention_ex", "kvz_decode_attention_raw_ex", "kvz_selftest_late_writer",
-    "kvz_chunk_attention_workspace_size", "kvz_chunk_attention", "kvz_chunk_attention_raw",
+    "kvz_chunk_attention_workspace_size", "kvz_chunk_attention_workspace_size_ex", "kvz_chunk_attention", "kvz_chunk_attention_raw",
     "kvz_append_tokens_normed", "kvz_plan_step", "kvz_release_pages",
     "kvz_append_tokens", "kvz_prefix_attention_workspace_size", "kvz_prefix_attention", "kvz_prefix_attention_raw",
 )
@@ -108,6 +109,7 @@ def _load() -> ctypes.CDLL:
         "kvz_append_tokens": (ctypes.c_int, [Dims, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P, i32, P, i32,
                                              ctypes.c_uint32, ctypes.c_float, P, P, i64, P, P]),
         "kvz_chunk_attention_workspace_size": (sz, [Dims, i32, i32, i32, i32, i32]),
+        "kvz_chunk_attention_workspace_size_ex": (sz, [Dims, i32, i32, i32, i32, i32, i32, i32, i64]),
         "kvz_chunk_attention": (ctypes.c_int, [Dims, i32, i32, P, i32, P, P, i32, P, P, P, i64, P, u64, P, i64, i32, i32,
                                                P, i32, P, sz, P, P]),
         "kvz_chunk_attention_raw": (ctypes.c_int, [Dims, i32, i32, P, i32, P, P, i32, P, P, i64, i32, i32, P, i32, P, sz,
@@ -388,21 +390,34 @@ def prefix_attention_raw(q, group_start, prefix_ids, prefix_lens, page_ids, seq_
 # attention of several new tokens a sequence
 # ------------------------------------------------------------------------------------
 def chunk_attention_workspace_size(hkv: int, tokens: int, num_q_heads: int, batch: int, pages: int,
-                                   coded: bool = False) -> int:
+                                   coded: bool = False, window: int = 0, sinks: int = 0,
+                                   seen_pages: int | None = None) -> int:
     """Workspace bytes of chunk_attention_raw, or (coded) chunk_attention, with q [tokens][num_q_heads][128] and
-    page_ids [batch][pages]."""
-    size = int(_lib.kvz_chunk_attention_workspace_size(_dims(hkv), tokens, num_q_heads, batch, pages, int(coded)))
+    page_ids [batch][pages].  A coded call's holds the pages that its tokens see as raw ones: all of the table unless
+    a window says less, or the caller, who knows the lengths, does: seen_pages, over all sequences."""
+    size = int(_lib.kvz_chunk_attention_workspace_size_ex(
+        _dims(hkv), tokens, num_q_heads, batch, pages, int(coded), min(window, 2**31 - 1), min(sinks, 2**31 - 1),
+        -1 if seen_pages is None else seen_pages))
     if size == 0:
         raise KvzError("kvz_chunk_attention_workspace_size", -1)
     return size
 
 
-def _chunk_workspace(q, page_ids, raw_pool, coded, stream):
+def _whole(x) -> int:
+    """x as the C calls take a number of tokens; 0 where it is none, which the call then refuses."""
+    try:
+        return min(operator.index(x), 2**31 - 1)
+    except TypeError:
+        return 0
+
+
+def _chunk_workspace(q, page_ids, raw_pool, coded, window, sinks, stream):
     """A workspace of the call's own; empty for shapes that the call then refuses."""
     if q.dim() != 3 or page_ids.dim() != 2 or raw_pool.dim() != 5:
         raise ValueError("q, page_ids, raw_pool: expected [tokens][heads][128], [batch][pages] and [pages][heads][2][16][128]")
-    size = _lib.kvz_chunk_attention_workspace_size(_dims(raw_pool.shape[1]), q.shape[0], q.shape[1], page_ids.shape[0],
-                                                   page_ids.shape[1], int(coded))
+    size = _lib.kvz_chunk_attention_workspace_size_ex(
+        _dims(raw_pool.shape[1]), q.shape[0], q.shape[1], page_ids.shape[0], page_ids.shape[1], int(coded),
+        _whole(window), _whole(sinks), -1)
     return _empty(size, torch.uint8, q, stream)
 
 
@@ -415,7 +430,7 @@ def chunk_attention(q, q_start, page_ids, seq_lens, tail_page, meta, arena, raw_
     if meta is None or arena is None:
         raise ValueError("meta, arena: expected tensors")
     if workspace is None:
-        workspace = _chunk_workspace(q, page_ids, raw_pool, True, stream)
+        workspace = _chunk_workspace(q, page_ids, raw_pool, True, window, sinks, stream)
     rc = _binding.chunk_attention(q, q_start, page_ids, seq_lens, tail_page, meta, arena, raw_pool, window, sinks, out,
                                   status, workspace, None if stream is None else stream.cuda_stream)
     if rc:
@@ -426,7 +441,7 @@ def chunk_attention_raw(q, q_start, page_ids, seq_lens, raw_pool, out, status, w
                         workspace=None, stream=None):
     """chunk_attention over plain BF16 pages: page_ids name raw pages and cover the last, partial ones."""
     if workspace is None:
-        workspace = _chunk_workspace(q, page_ids, raw_pool, False, stream)
+        workspace = _chunk_workspace(q, page_ids, raw_pool, False, window, sinks, stream)
     rc = _binding.chunk_attention(q, q_start, page_ids, seq_lens, None, None, None, raw_pool, window, sinks, out, status,
                                   workspace, None if stream is None else stream.cuda_stream)
     if rc:

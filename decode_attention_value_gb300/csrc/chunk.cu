@@ -906,31 +906,70 @@ __global__ void __launch_bounds__(kChMergeThreads) k_chunk_merge(const ChunkPara
 }
 
 // ---------------------------------------------------------------------------------
-// 12-bit pages that any new token sees, and the raw tails behind them, as raw pages of the workspace: page p of
-// sequence b is page b * max_pages + p there.  A warp a (page, KV head); tiles are put together in shared
-// memory by 8 x 8 matrices, then written as whole rows.
+// 12-bit pages that any new token sees, and the raw tails behind them, as raw pages of the workspace, one behind
+// the other in the sequences' order; the table of places goes by the sequence's pages.  Each block works out where
+// the pages of its groups of sequences begin, so the work is of the pages seen and not of the table's width.  A warp a
+// (page, KV head); tiles are put together in shared memory by 8 x 8 matrices, then written as whole rows.
 // ---------------------------------------------------------------------------------
-constexpr int kRestoreWarps = 4, kRestorePitch = 272;
+constexpr int kRestoreWarps = 4, kRestorePitch = 272, kRestoreGroups = kRestoreWarps * 32;
 
 __global__ void __launch_bounds__(kRestoreWarps * 32, 6) k_chunk_restore(const ChunkParams P, const ChunkCoded X)
 {
     __shared__ __align__(16) uint8_t buf[kRestoreWarps][2][kPage * kRestorePitch];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int64_t begin[kRestoreGroups + 1], red[kRestoreWarps];  // pages before a group, of a warp's groups
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait_primary();
-    const int64_t items = (int64_t)P.batch * P.max_pages * P.hkv, step = (int64_t)gridDim.x * kRestoreWarps;
+    auto seen = [&](int b, int &len) -> ChunkPages {  // of sequence b
+        const int start = P.q_start[b], end = P.q_start[b + 1];
+        if (start < 0 || start >= end || end > P.tokens) return ChunkPages{0, 0, 0};  // (out of order: flagged where nothing is computed)
+        len = named_tokens(P.seq_lens[b], P.len_pages, true);
+        return chunk_pages(P, end - start, len);
+    };
+    const int per = (P.batch + kRestoreGroups - 1) / kRestoreGroups;  // sequences of a group
+    {
+        int64_t n = 0;
+        for (int b = tid * per; b < min(P.batch, (tid + 1) * per); ++b) {
+            int len;
+            n += seen(b, len).count();
+        }
+        const int64_t own = n;
+        __syncwarp();
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, n, off);
+            if (lane >= off) n += y;
+        }
+        if (lane == 31) red[warp] = n;
+        __syncthreads();
+        n -= own;
+        for (int w = 0; w < warp; ++w) n += red[w];
+        begin[tid] = n;
+        if (tid == kRestoreGroups - 1) begin[kRestoreGroups] = n + own;
+        __syncthreads();
+    }
+    const int64_t items = begin[kRestoreGroups] * P.hkv, step = (int64_t)gridDim.x * kRestoreWarps;
     for (int64_t it = (int64_t)blockIdx.x * kRestoreWarps + warp; it < items; it += step) {
         const int64_t place = it / P.hkv;
-        const int kvh = (int)(it - place * P.hkv), b = (int)(place / P.max_pages), page = (int)(place - (int64_t)b * P.max_pages);
-        const int start = P.q_start[b], end = P.q_start[b + 1];
-        if (start < 0 || start >= end || end > P.tokens) continue;  // (out of order: flagged where nothing is computed)
-        const int len = named_tokens(P.seq_lens[b], P.len_pages, true), p0 = len - (end - start);
-        const int lo = P.window > 0 ? max(0, max(p0, 0) - P.window + 1) : 0;
-        if (!chunk_page_seen(P, lo, len, page * kPage)) continue;
+        const int kvh = (int)(it - place * P.hkv);
+        int lo = 0, top = kRestoreGroups - 1;
+        while (lo < top) {  // the last group that begins at or before the place: the one that holds it
+            const int mid = (lo + top + 1) >> 1;
+            if (begin[mid] <= place) lo = mid;
+            else top = mid - 1;
+        }
+        int b = lo * per, len = 0;
+        int64_t k = place - begin[lo];
+        ChunkPages g = seen(b, len);
+        for (; k >= g.count(); g = seen(++b, len)) k -= g.count();
+        const int page = g.page((int)k);
+        const int64_t at = ((int64_t)b * P.max_pages + page) * P.hkv + kvh;  // in the table
         uint4 *out = reinterpret_cast<uint4 *>(X.pages) + it * 512;
         uint32_t flag = 0;
         const bool coded = page < len / kPage;
         const int32_t id = coded ? X.page_ids[(int64_t)b * P.len_pages + page] : X.tail_page[b];
-        if (!coded) {
+        if (place >= X.places) {
+            flag = KVZ_STATUS_ARENA_FULL;
+        } else if (!coded) {
             if (id < 0 || id >= X.num_raw_pages) {
                 flag = id == -1 ? KVZ_STATUS_BAD_TAIL : KVZ_STATUS_BAD_INDEX;
             } else {
@@ -991,7 +1030,7 @@ __global__ void __launch_bounds__(kRestoreWarps * 32, 6) k_chunk_restore(const C
         }
         if (lane == 0) {
             if (flag) atomicOr(P.status, flag);
-            X.table[it] = flag ? kPageGone : (int32_t)place;
+            X.table[at] = flag ? kPageGone : (int32_t)place;
         }
     }
 }
@@ -1027,8 +1066,8 @@ cudaError_t launch_chunk(const ChunkParams &P, const ChunkCoded &X, const void *
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (X.table) {
-        const int64_t want = ((int64_t)P.batch * P.max_pages * P.hkv + kRestoreWarps - 1) / kRestoreWarps, wave = (int64_t)sms * 6;
-        cfg.gridDim = dim3((unsigned)(want < wave ? want : wave));
+        const int64_t want = ((int64_t)X.places * P.hkv + kRestoreWarps - 1) / kRestoreWarps, wave = (int64_t)sms * 6;
+        cfg.gridDim = dim3((unsigned)(want < 1 ? 1 : want < wave ? want : wave));
         cfg.blockDim = dim3(kRestoreWarps * 32);
         const cudaError_t e = cudaLaunchKernelEx(&cfg, k_chunk_restore, P, X);
         if (e != cudaSuccess) return e;

@@ -50,6 +50,23 @@ __device__ __forceinline__ bool chunk_page_seen(const ChunkParams &P, int lo, in
     return at < hi && (at + kPage > lo || at < P.sinks);
 }
 
+// Pages that any new token of a sequence sees: [0, sinks) and [first, end).
+struct ChunkPages {
+    int sinks, first, end;
+    __device__ __forceinline__ int count() const { return sinks + end - first; }
+    __device__ __forceinline__ int page(int k) const { return k < sinks ? k : first + k - sinks; }
+};
+
+__device__ __forceinline__ ChunkPages chunk_pages(const ChunkParams &P, int n, int len)
+{
+    ChunkPages g;
+    const int p0 = len - n, lo = P.window > 0 ? max(0, max(p0, 0) - P.window + 1) : 0, s = min(P.sinks, len);
+    g.first = lo / kPage;
+    g.end = len / kPage + (len % kPage != 0);
+    g.sinks = min(g.first, s / kPage + (s % kPage != 0));
+    return g;
+}
+
 // First block of CTA c's range of W blocks over C CTAs.
 __device__ __forceinline__ int64_t chunk_first(int64_t c, int64_t W, int C) { return (c * W + C - 1) / C; }
 

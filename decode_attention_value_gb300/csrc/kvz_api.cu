@@ -960,39 +960,70 @@ int kvz_append_tokens(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, co
                                     num_raw_pages, status, stream);
 }
 
-// Where the parts of a chunk attention workspace are, from its start rounded up to 256 bytes.
+// Where the parts of a chunk attention workspace are, from its start rounded up to 256 bytes.  Coded: with a table of
+// max_pages + 1 places a sequence and, last, room for restored pages.
 struct ChunkLayout {
-    size_t part_o = 0, part_ml, merge, table, pages, bytes;
+    size_t part_o = 0, part_ml, merge, table, pages;
 };
-static ChunkLayout chunk_layout(int grid, int64_t restored, int hkv)
+static ChunkLayout chunk_layout(int grid, int64_t batch, int64_t max_pages, int hkv, bool coded)
 {
     ChunkLayout l;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     l.part_ml = (size_t)grid * 2 * 256 * kDim * 4;
     l.merge = l.part_ml + (size_t)grid * 2 * 256 * 8;
     l.table = up(l.merge + (size_t)grid * 16);
-    l.pages = up(l.table + (size_t)restored * hkv * 4);
-    l.bytes = l.pages + (size_t)restored * hkv * 2 * kPage * kDim * 2;
+    l.pages = up(l.table + (coded ? (size_t)batch * (max_pages + 1) * hkv * 4 : 0));
     return l;
 }
-// Raw pages that a call with 12-bit pages restores into its workspace (0 for a raw call), -1: too many.
-static int64_t chunk_restored(const kvz_dims &d, int batch, int max_pages, bool coded)
+// Window and first tokens as the kernels take them, of tables of max_pages pages and, coded, a tail: a window that no
+// length reaches is none; sinks without a window are nothing.
+static void chunk_window(int32_t window, int32_t sinks, int32_t max_pages, bool coded, int32_t *w, int32_t *s)
 {
-    const int64_t n = coded ? (int64_t)batch * (max_pages + 1LL) : 0;
-    return n * d.num_kv_heads * 32 >= (int64_t)1 << 31 ? -1 : n;
+    const int32_t all = (max_pages + (coded ? 1 : 0)) * kPage;
+    *w = window >= all ? 0 : window;
+    *s = *w > 0 ? (sinks < all ? sinks : all) : 0;
 }
+// Pages that the new tokens of a batch can see at most.  n new tokens and the window before the first of them are n +
+// window - 1 keys in a row, which touch (n + window + 13) / 16 + 1 pages at most.
+static int64_t chunk_pages_most(int64_t tokens, int64_t batch, int64_t max_pages, int64_t window, int64_t sinks)
+{
+    int64_t most = batch * (max_pages + 1);
+    if (window > 0) {
+        const int64_t some = batch < tokens ? batch : tokens;  // sequences with a new token
+        const int64_t seen = tokens / kPage + 1 + some * ((window + 13 + kPage - 1) / kPage + 1 + (sinks + kPage - 1) / kPage);
+        most = seen < most ? seen : most;
+    }
+    return most;
+}
+static int64_t chunk_places_most(int hkv) { return (((int64_t)1 << 31) - 1) / (32 * hkv); }  // rows of a tensor map
 constexpr int kChunkMaxPages = 1 << 26;  // of a table: its keys are counted in 30 bits
 
-size_t kvz_chunk_attention_workspace_size(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
-                                          int32_t max_pages, int32_t coded)
+size_t kvz_chunk_attention_workspace_size_ex(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
+                                             int32_t max_pages, int32_t coded, int32_t window, int32_t sinks,
+                                             int64_t seen_pages)
 {
     if (!dims_ok(dims) || num_tokens < 0 || batch < 0 || batch > kMaxBatch || max_pages < 0 || max_pages > kChunkMaxPages)
         return 0;
     if (num_q_heads < 1 || num_q_heads % dims.num_kv_heads != 0 || num_q_heads / dims.num_kv_heads > 8) return 0;
+    if (window < 0 || sinks < 0) return 0;
     const int sms = sm_count();
-    const int64_t restored = chunk_restored(dims, batch, max_pages, coded != 0);
-    if (sms < 1 || restored < 0) return 0;
-    return chunk_layout(sms, restored, dims.num_kv_heads).bytes + 240;  // (from 16-byte alignment to 256)
+    if (sms < 1) return 0;
+    int64_t places = 0;
+    if (coded) {
+        int32_t w, s;
+        chunk_window(window, sinks, max_pages, true, &w, &s);
+        places = chunk_pages_most(num_tokens, batch, max_pages, w, s);
+        if (seen_pages >= 0 && seen_pages < places) places = seen_pages;
+        if (places > chunk_places_most(dims.num_kv_heads)) places = chunk_places_most(dims.num_kv_heads);
+    }
+    return chunk_layout(sms, batch, max_pages, dims.num_kv_heads, coded != 0).pages +
+           (size_t)places * dims.num_kv_heads * 2 * kPage * kDim * 2 + 240;  // (from 16-byte alignment to 256)
+}
+
+size_t kvz_chunk_attention_workspace_size(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
+                                          int32_t max_pages, int32_t coded)
+{
+    return kvz_chunk_attention_workspace_size_ex(dims, num_tokens, num_q_heads, batch, max_pages, coded, 0, 0, -1);
 }
 
 static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const void *q, int32_t batch,
@@ -1015,13 +1046,11 @@ static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const vo
         return KVZ_ERR_ALIGNMENT;
     if (X && (!aligned(X->meta, 16) || !aligned(X->arena, 256) || !aligned(X->tail_page, 4))) return KVZ_ERR_ALIGNMENT;
     if (num_raw_pages * d.num_kv_heads * 32 >= (int64_t)1 << 31) return KVZ_ERR_UNSUPPORTED;
-    const int64_t restored = chunk_restored(d, batch, max_pages, X != nullptr);
-    if (restored < 0) return KVZ_ERR_UNSUPPORTED;
     const int sms = sm_count();
     if (sms < 1) return KVZ_ERR_DEVICE;
-    const ChunkLayout at = chunk_layout(sms, restored, d.num_kv_heads);
+    const ChunkLayout at = chunk_layout(sms, batch, max_pages, d.num_kv_heads, X != nullptr);
     const size_t pad = (size_t)(-reinterpret_cast<uintptr_t>(ws) & 255);
-    if (pad + at.bytes > ws_bytes) return KVZ_ERR_WORKSPACE;
+    if (pad + at.pages > ws_bytes) return KVZ_ERR_WORKSPACE;
     uint8_t *const base = static_cast<uint8_t *>(ws) + pad;
     ChunkParams P;
     memset(&P, 0, sizeof P);
@@ -1034,9 +1063,7 @@ static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const vo
     P.id_head = X ? 1 : 0;
     P.len_pages = max_pages;
     P.tail = X != nullptr;
-    // a window that no length reaches is none; sinks without a window are nothing
-    P.window = window >= P.max_pages * kPage ? 0 : window;
-    P.sinks = P.window > 0 ? (sinks < P.max_pages * kPage ? sinks : P.max_pages * kPage) : 0;
+    chunk_window(window, sinks, max_pages, X != nullptr, &P.window, &P.sinks);
     P.tile_tokens = 256 / G;
     P.grid = sms;
     // blocks of 128 keys (8 steps of a sum, for each weight part) between folds.  Each step drops about half of the last
@@ -1066,8 +1093,13 @@ static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const vo
         Y.num_raw_pages = num_raw_pages;
         Y.table = reinterpret_cast<int32_t *>(base + at.table);
         Y.pages = reinterpret_cast<uint16_t *>(base + at.pages);
+        const int64_t room = (int64_t)((ws_bytes - pad - at.pages) / ((size_t)d.num_kv_heads * 2 * kPage * kDim * 2));
+        int64_t places = chunk_pages_most(num_tokens, batch, max_pages, P.window, P.sinks);
+        places = room < places ? room : places;
+        places = chunk_places_most(d.num_kv_heads) < places ? chunk_places_most(d.num_kv_heads) : places;
+        Y.places = (int32_t)places;
         P.page_ids = Y.table;
-        P.num_raw_pages = restored;
+        P.num_raw_pages = places;
         pool = Y.pages;
     }
     CUtensorMap map;

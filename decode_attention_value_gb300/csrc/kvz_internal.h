@@ -225,8 +225,9 @@ struct ChunkCoded {
     uint64_t arena_bytes;
     const uint16_t *raw_pool;
     int64_t num_raw_pages;
-    int32_t *table;   // [batch][max_pages][hkv]
-    uint16_t *pages;  // [batch * max_pages][hkv][2][16][128]
+    int32_t *table;   // [batch][max_pages][hkv] where a page stands among the restored ones
+    uint16_t *pages;  // [places][hkv][2][16][128]
+    int32_t places;   // pages that the workspace has room for; those behind them are left out and flagged
 };
 // map: tensor map of the raw pages read, boxes as for launch_prefix
 cudaError_t launch_chunk(const ChunkParams &P, const ChunkCoded &X, const void *map, int sms, cudaStream_t stream);

@@ -384,13 +384,20 @@ int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_he
  *               each, float32 ones all bits of them
  *  workspace    >= kvz_chunk_attention_workspace_size(dims, num_tokens, num_q_heads, batch, max_pages, coded)
  *               bytes (16-B aligned), coded = 1 for kvz_chunk_attention, whose workspace also holds the pages
- *               that it reads as raw pages: batch * (max_pages + 1) of one layer
+ *               that it reads as raw pages (num_kv_heads * 8 KB each): batch * (max_pages + 1).  The _ex form asks for
+ *               room for the pages that the step's tokens can see at most: with a window, that window's, and never
+ *               more than seen_pages (-1: not known), the pages (tails too) that they see over all sequences.
+ *               Pages seen beyond the room that a workspace has are left out, in the order of the sequences and
+ *               their pages, with KVZ_STATUS_ARENA_FULL
  * A key or value that is not finite may reach every new token of its sequence within 256 query rows of one that sees it;
  * a query that is not makes its own rows NaN.
  * Results depend on the data, the shapes, the lengths and the device's SM count only.
  * --------------------------------------------------------------------------------- */
 size_t kvz_chunk_attention_workspace_size(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
                                           int32_t max_pages, int32_t coded);
+size_t kvz_chunk_attention_workspace_size_ex(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
+                                             int32_t max_pages, int32_t coded, int32_t window, int32_t sinks,
+                                             int64_t seen_pages);
 int kvz_chunk_attention(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, const void *q, int32_t batch,
                         const int32_t *q_start, const int32_t *page_ids, int32_t max_pages, const int32_t *seq_lens,
                         const int32_t *tail_page, const uint64_t *meta, int64_t num_meta_pages, const uint8_t *arena,

@@ -85,3 +85,45 @@ def test_heads_that_are_not_finite():
         assert torch.equal(out.isnan(), want.isnan())
         assert torch.equal(out.nan_to_num(7.0)[4:], want.nan_to_num(7.0)[4:])
         assert (out[1:3].nan_to_num(0.0) == 0).all()
+
+
+@pytest.mark.parametrize("T,hq,hkv", [(1, 1, 1), (5003, 32, 8), (16381, 32, 8), (9001, 5, 5)])
+@pytest.mark.parametrize("rot,interleaved,per_head,dtype", [(128, False, True, BF16), (64, True, False, torch.float32)])
+def test_many_rows_a_block_and_padding_tokens(T, hq, hkv, rot, interleaved, per_head, dtype):
+    """Several passes a block with two rows in flight, results of more than 64 MB written past L2, rows without a slot
+    among the eight-lane groups of a warp; either operand normed alone too."""
+    import decode_attention_value_gb300 as kvz
+
+    g = torch.Generator(device="cuda").manual_seed(T)
+    qkv = (torch.randn((T, hq + 2 * hkv, D), generator=g, device="cuda") * 3).to(BF16)
+    q, k, v = qkv.split((hq, hkv, hkv), 1)
+    qw, kw = (torch.randn(((h, D) if per_head else (D,)), generator=g, device="cuda").to(dtype) for h in (hq, hkv))
+    pages = T // PAGE + 3
+    slots = torch.randperm(pages * PAGE, generator=g, device="cuda")[:T].to(torch.int32)
+    if T > 1:
+        slots[torch.rand(T, generator=g, device="cuda") < 0.05] = -1
+    live = slots >= 0
+    at = slots[live].long()
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    inv = 10000.0 ** (-torch.arange(rot // 2, dtype=torch.float64) / (rot // 2))
+    table, status, ang = kvz.rope_table(inv).cuda(), kvz.new_status(), torch.outer(pos.double(), inv.cuda())[:, None]
+    for qn, kn in ((qw, kw), (qw, None), (None, kw)):
+        pool = torch.full((pages, hkv, 2, PAGE, D), 77.0, dtype=BF16, device="cuda")
+        out = kvz.append_tokens(k, v, slots, pool, status, q=q, rope=table, positions=pos, interleaved=interleaved, q_norm=qn,
+                                k_norm=kn)
+        if qn is not None:
+            _close(out, *_wanted(q, qn, float(torch.tensor(1e-6)), ang, interleaved, rot))
+        if kn is not None:
+            want = _wanted(k, kn, float(torch.tensor(1e-6)), ang, interleaved, rot)
+            _close(pool[at // PAGE, :, 0, at % PAGE], *(x[live] if x.shape[0] == T else x for x in want))
+        # an operand without a norm is what the call without norms gives
+        bare = torch.full_like(pool, 77.0)
+        ref = kvz.append_tokens(k, v, slots, bare, status, q=q, rope=table, positions=pos, interleaved=interleaved)
+        if qn is None:
+            assert torch.equal(out, ref)
+        if kn is None:
+            assert torch.equal(pool, bare)
+        assert torch.equal(pool[:, :, 1], bare[:, :, 1]) and int(status.item()) == 0
+        rows = torch.zeros(pages * PAGE, dtype=torch.bool, device="cuda")
+        rows[at] = True
+        assert (pool.permute(0, 3, 1, 2, 4).reshape(pages * PAGE, hkv, 2, D)[~rows] == 77.0).all()

@@ -7,10 +7,10 @@
 // group) of a tile are the rows of a matrix Q: S = Q K^T, P = exp2(S c - m) with scores of unseen keys minus
 // infinity, O = P V, with the running maximum m and sum l of each row, O / l at the end.
 //
-// Bound: the latency of a row's softmax (2039 tokens behind 30710, 32/8 heads: 1062 us, 1.0 PFLOP/s, 1.5 as issued with
-// the second part of each weight), then the tensor cores for chunks, three products of 128 x 128 x 128 a tile of 128
-// rows and block of keys (S, and O for each part); the bytes of the pages for few rows (64 single tokens with a
-// window of 4096: 185 us, 5.9 TB/s).
+// Bound: the tensor cores for chunks, three products of 128 x 128 x 128 a tile of 128 rows and block of keys (S, and O for
+// each part of the weights), and the latency of a row's softmax (2039 tokens behind 30710, 32/8 heads: 1050 us,
+// 1.0 PFLOP/s, 1.5 as issued, tensor pipe 70 % busy); the bytes of the pages for few rows (64 single tokens with a
+// window of 4096: 184 us, 5.9 TB/s).
 //
 // Split: a unit is (sequence, KV head, tile of up to 256 rows) and has as many blocks of 128 keys as its rows see; the
 // units' blocks are one line, cut into equal ranges, a CTA each, so any mix of chunks and single tokens

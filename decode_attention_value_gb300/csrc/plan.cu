@@ -79,7 +79,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     __shared__ int32_t start[kMaxBatch + 1], have[kMaxBatch], row_of[kMaxBatch], fresh[kMaxBatch], after[kMaxBatch];
     __shared__ uint32_t bad;
     const int tid = threadIdx.x, cta = blockIdx.x, lane = tid & 31;
-    const int at = cta * kPlanThreads + tid, step = kPlanCtas * kPlanThreads;
+    const int at = cta * kPlanThreads + tid, step = kPlanCtas * kPlanThreads;  // (counts near 2^31: steps in 32 unsigned bits)
     for (int i = tid; i < kPlanSeen; i += kPlanThreads) seen[i] = -1;
     if (tid == 0) bad = 0;
     pdl_wait_primary();
@@ -118,7 +118,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const bool fits = bad == 0;
     bool named = page_named(last);
     if (fits)
-        for (int i = tid; i < (int)all[1]; i += kPlanThreads) named &= page_named(P.free_pages[spare - 1 - i]);
+        for (uint32_t i = tid; i < (uint32_t)all[1]; i += kPlanThreads) named &= page_named(P.free_pages[spare - 1 - (int)i]);
     const uint32_t wrong = __syncthreads_or(!named) ? KVZ_STATUS_BAD_INDEX : 0;
     const bool ok = fits && !wrong;  // else: a step without requests, and nothing changes
     if (tid < P.batch) {
@@ -131,7 +131,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (tid == 0) start[P.batch] = ok ? (int32_t)all[0] : 0;
     if (cta == 0 && tid == 0 && !ok) atomicOr(P.status, fits ? wrong : bad);
     if (P.lens_out != P.lens)
-        for (int i = at; i < P.num_rows; i += step) P.lens_out[i] = P.lens[i];
+        for (uint32_t i = at; i < (uint32_t)P.num_rows; i += step) P.lens_out[i] = P.lens[i];
     cluster_meet();  // lengths and the free list's count have been read, copied lengths written
     if (cta == 0 && tid < P.batch && ok && row >= 0) P.lens_out[row] = len + fresh_tokens;
     if (cta == 0 && tid == 0) P.free_out[0] = ok ? spare - (int32_t)all[1] : spare;
@@ -165,7 +165,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         }
     }
     // ---- the tokens ----
-    for (int i = at; i < P.tokens; i += step) {
+    for (uint32_t u = at; u < (uint32_t)P.tokens; u += step) {
+        const int i = (int)u;
         int32_t pos = 0, slot = -1;
         if (i < start[P.batch]) {
             int lo = 0, hi = P.batch - 1;

@@ -389,7 +389,7 @@ int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_he
  *               more than seen_pages (-1: not known), the pages (tails too) that they see over all sequences.
  *               Pages seen beyond the room that a workspace has are left out, in the order of the sequences and
  *               their pages, with KVZ_STATUS_ARENA_FULL
- * A key or value that is not finite may reach every new token of its sequence within 256 query rows of one that sees it;
+ * A key or value that is not finite may make every new token of its sequence within 256 query rows of one that sees it NaN;
  * a query that is not makes its own rows NaN.
  * Results depend on the data, the shapes, the lengths and the device's SM count only.
  * --------------------------------------------------------------------------------- */

@@ -997,6 +997,7 @@ static int64_t chunk_pages_most(int64_t tokens, int64_t batch, int64_t max_pages
 }
 static int64_t chunk_places_most(int hkv) { return (((int64_t)1 << 31) - 1) / (32 * hkv); }  // rows of a tensor map
 constexpr int kChunkMaxPages = 1 << 26;  // of a table: its keys are counted in 30 bits
+constexpr int kChunkMaxHeads = 1 << 20;  // KV heads: numbered in 23 bits
 
 size_t kvz_chunk_attention_workspace_size_ex(kvz_dims dims, int32_t num_tokens, int32_t num_q_heads, int32_t batch,
                                              int32_t max_pages, int32_t coded, int32_t window, int32_t sinks,
@@ -1005,7 +1006,7 @@ size_t kvz_chunk_attention_workspace_size_ex(kvz_dims dims, int32_t num_tokens, 
     if (!dims_ok(dims) || num_tokens < 0 || batch < 0 || batch > kMaxBatch || max_pages < 0 || max_pages > kChunkMaxPages)
         return 0;
     if (num_q_heads < 1 || num_q_heads % dims.num_kv_heads != 0 || num_q_heads / dims.num_kv_heads > 8) return 0;
-    if (window < 0 || sinks < 0) return 0;
+    if (window < 0 || sinks < 0 || dims.num_kv_heads > kChunkMaxHeads) return 0;
     const int sms = sm_count();
     if (sms < 1) return 0;
     int64_t places = 0;
@@ -1037,6 +1038,7 @@ static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const vo
     if (hq % d.num_kv_heads != 0 || (out_type != KVZ_OUT_F32 && out_type != KVZ_OUT_BF16)) return KVZ_ERR_INVALID_ARG;
     const int G = hq / d.num_kv_heads;
     if (G > 8 || batch > kMaxBatch || max_pages > kChunkMaxPages || num_tokens > 1 << 24) return KVZ_ERR_UNSUPPORTED;
+    if (d.num_kv_heads > kChunkMaxHeads) return KVZ_ERR_UNSUPPORTED;
     if (num_tokens == 0 || batch == 0) return KVZ_OK;
     if (!q || !q_start || !seq_lens || !out || !ws || !status || (max_pages > 0 && !page_ids)) return KVZ_ERR_INVALID_ARG;
     if (num_raw_pages > 0 && !raw_pool) return KVZ_ERR_INVALID_ARG;
@@ -1045,7 +1047,7 @@ static int run_chunk(const kvz_dims &d, int32_t num_tokens, int32_t hq, const vo
         !aligned(q_start, 4) || !aligned(page_ids, 4) || !aligned(status, 4))
         return KVZ_ERR_ALIGNMENT;
     if (X && (!aligned(X->meta, 16) || !aligned(X->arena, 256) || !aligned(X->tail_page, 4))) return KVZ_ERR_ALIGNMENT;
-    if (num_raw_pages * d.num_kv_heads * 32 >= (int64_t)1 << 31) return KVZ_ERR_UNSUPPORTED;
+    if (num_raw_pages > chunk_places_most(d.num_kv_heads)) return KVZ_ERR_UNSUPPORTED;
     const int sms = sm_count();
     if (sms < 1) return KVZ_ERR_DEVICE;
     const ChunkLayout at = chunk_layout(sms, batch, max_pages, d.num_kv_heads, X != nullptr);

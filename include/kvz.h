@@ -375,7 +375,7 @@ int kvz_append_tokens_normed(kvz_dims dims, int32_t num_tokens, int32_t num_q_he
  *               as they were.  Out of order or range: KVZ_STATUS_BAD_ORDER, and nothing is computed
  *  seq_lens     int32 [batch] tokens of each sequence, the new ones with them: new token i of n stands at
  *               p = seq_lens - n + i.  A token before the first (n > seq_lens) sees nothing: zero
- *  page_ids, max_pages, tail_page: as in those calls; max_pages <= 2^26
+ *  page_ids, max_pages, tail_page: as in those calls; max_pages <= 2^26; num_kv_heads <= 2^20
  *  window       0: token p sees the keys j <= p.  W > 0: of these j > p - W, and j < sinks.  Pages that no new token
  *               sees are not read, and their ids may be anything
  *  sinks        first tokens of each sequence that stay visible behind the window (nothing without one)
